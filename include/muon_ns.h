@@ -246,6 +246,99 @@ MNS_API int adamw_step(int ntensors, void* const* params, const void* const* gra
 MNS_API int gram_ns_trace(const mns_tensor* G, const mns_tensor* O, const mns_ns_params* p, void* ws,
                    size_t ws_bytes, float* trace, void* stream);
 
+/*
+ * ------------------------------------------------------------------------------------------
+ * The layer whose matrices the Muon step updates: a layer norm in front of a mixture of
+ * experts, forward and backward. Gradients come out in the optimizer's own layouts: dW as the
+ * batch of rows x cols matrices that muon_step takes, dweight and dbias as the flat tensors that
+ * adamw_step takes.
+ *
+ * The conventions above hold, with these additions:
+ *  - A buffer of rows (mns_tensor with batch 1 unless said otherwise) may have 0 rows; its
+ *    element offsets may pass 32 bits. At most 2^24 rows, 2^20 columns, ld <= 2^20; more is
+ *    MNS_ERR_SHAPE. Any alignment of the element size and any ld is accepted; rows of whole
+ *    16-byte chunks at 16-byte aligned addresses run the fast kernels.
+ *  - Outputs must not overlap inputs or each other (MNS_ERR_ARG).
+ *  - Sums are fp32 in a fixed order; each result is rounded once to its buffer's dtype, so equal
+ *    calls give equal bits.
+ *  - Workspaces are device memory aligned to 16 bytes.
+ *
+ * Routing: T tokens pick k of E experts each. Slot t * k + j is token t's j-th pick, S = T * k
+ * slots in all. The slots are sorted by expert, ties by slot number; expert e's rows are
+ * offsets[e] .. offsets[e + 1] - 1 (int32 [E + 1], offsets[0] = 0) and rank[t * k + j] is a
+ * slot's row (int32 [T * k]), -1 for a pick outside 0 .. E - 1: a padded token, or an expert that
+ * lives on another GPU. Rows from offsets[E] to S - 1 belong to no expert and are written as
+ * zeros. E is at most 1024. offsets and rank stay on the device and are not read on the host: a
+ * rank outside 0 .. S - 1 counts as -1, offsets are cut to 0 .. S and an expert whose end lies
+ * before its beginning has no rows, so no buffer contents lead to an access out of range.
+ */
+
+/*
+ * Layer norm of every row of X (any batch): with mean and rstd = 1 / sqrt(var + eps) over the
+ * columns, Y = (X - mean) rstd weight + bias. weight, bias: device [cols] of wdtype, which is X's
+ * dtype or F32; NULL = 1 and 0. Y: X's batch, rows, cols and dtype. mean, rstd: device float
+ * [batch * rows], written (the backward pass reads them).
+ */
+MNS_API int layer_norm(const mns_tensor* X, const void* weight, const void* bias, int32_t wdtype, float eps,
+                       const mns_tensor* Y, float* mean, float* rstd, void* stream);
+
+/* Workspace bytes of layer_norm_backward for this X (host-only; only its shape is read). */
+MNS_API int mns_layer_norm_workspace_bytes(const mns_tensor* X, size_t* bytes);
+
+/*
+ * Gradients of layer_norm: with xh = (X - mean) rstd and g = dY weight,
+ * dX = rstd (g - mean_cols(g) - xh mean_cols(g xh)), dweight = sum_rows(dY xh),
+ * dbias = sum_rows(dY). dweight, dbias: device [cols] of wdtype, or NULL where not wanted (the
+ * workspace is then not needed if both are). Zero rows give dweight = dbias = 0.
+ */
+MNS_API int layer_norm_backward(const mns_tensor* dY, const mns_tensor* X, const float* mean, const float* rstd,
+                                const void* weight, int32_t wdtype, const mns_tensor* dX, void* dweight, void* dbias,
+                                void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of expert_sort (0 for few slots; host-only). */
+MNS_API int mns_expert_sort_workspace_bytes(int64_t slots, int32_t experts, size_t* bytes);
+
+/*
+ * offsets and rank of the picks ids (contiguous int32 or int64, id_bytes 4 or 8, [slots]).
+ */
+MNS_API int expert_sort(const void* ids, int32_t id_bytes, int64_t slots, int32_t experts, int32_t* offsets, int32_t* rank,
+                        void* ws, size_t ws_bytes, void* stream);
+
+/* XS[rank[t * k + j]] = X[t], the rows of no expert zero. X: T rows, XS: T * k rows. */
+MNS_API int expert_dispatch(const mns_tensor* X, const int32_t* rank, int32_t k, const int32_t* offsets, int32_t experts,
+                            const mns_tensor* XS, void* stream);
+
+/* Its gradient: dX[t] = sum_j dXS[rank[t * k + j]] (slots without a row add nothing). */
+MNS_API int expert_dispatch_backward(const mns_tensor* dXS, const int32_t* rank, int32_t k, const mns_tensor* dX, void* stream);
+
+/*
+ * Y[t] = sum_j weights[t * k + j] YS[rank[t * k + j]]. weights: contiguous [T * k] of wdtype, the
+ * rows' dtype or F32. The weight of a slot without a row is not read into the sum.
+ */
+MNS_API int expert_combine(const mns_tensor* YS, const void* weights, int32_t wdtype, const int32_t* rank, int32_t k,
+                           const mns_tensor* Y, void* stream);
+
+/*
+ * Its gradients: dYS[rank[t * k + j]] = weights[t * k + j] dY[t], the rows of no expert zero, and
+ * dweights[t * k + j] = sum_cols(dY[t] YS[rank[t * k + j]]), 0 for a slot without a row (wdtype).
+ */
+MNS_API int expert_combine_backward(const mns_tensor* dY, const mns_tensor* YS, const void* weights, int32_t wdtype,
+                                    const int32_t* rank, int32_t k, const int32_t* offsets, int32_t experts,
+                                    const mns_tensor* dYS, void* dweights, void* stream);
+
+/*
+ * The experts' products, W a batch of E matrices N x K (the Muon step's layout), all of one dtype:
+ *   expert_matmul              Y[s] = W[e] X[s]             X: S x K, Y: S x N, row s of expert e
+ *   expert_matmul_grad_input   dX[s] = W[e]^T dY[s]         dY: S x N, dX: S x K
+ *   expert_matmul_grad_weight  dW[e] = sum_s dY[s] X[s]^T   dW: E matrices N x K, 0 without rows
+ * Rows of no expert get zeros. MFMA with fp32 accumulation.
+ */
+MNS_API int expert_matmul(const mns_tensor* X, const mns_tensor* W, const int32_t* offsets, const mns_tensor* Y, void* stream);
+MNS_API int expert_matmul_grad_input(const mns_tensor* dY, const mns_tensor* W, const int32_t* offsets, const mns_tensor* dX,
+                                     void* stream);
+MNS_API int expert_matmul_grad_weight(const mns_tensor* dY, const mns_tensor* X, const int32_t* offsets, const mns_tensor* dW,
+                                      void* stream);
+
 /* Static English text for a status code (never NULL). */
 MNS_API const char* mns_status_string(int code);
 

@@ -12,7 +12,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libmuon_ns.so")
-SOURCES = ["muon_ns.hip"]
+SOURCES = ["muon_ns.hip", os.path.join("layer", "layer.hip")]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
@@ -29,24 +29,38 @@ def hipcc() -> str:
     return "hipcc"
 
 
-def build(verbose: bool = False) -> str:
-    tmp = LIB + ".tmp"
-    cmd = [hipcc(), *HIPCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-I", CSRC,
-           *[os.path.join(CSRC, s) for s in SOURCES], "-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    errs = [l for l in r.stderr.splitlines() if "packed-fp32-ops" not in l]
-    if r.returncode != 0:
-        raise RuntimeError("hipcc failed:\n" + "\n".join(errs))
-    if verbose and errs:
-        print("\n".join(errs))
-    os.replace(tmp, LIB)
-    return LIB
-
-
 BUILD = os.path.join(ROOT, "_build")
 HOSTSAN_LIB = os.path.join(BUILD, "libmuon_ns_hostsan.so")
+
+
+def _run(cmds, verbose: bool, what: str) -> None:
+    """Run the commands side by side; raise with the compiler's messages if one fails."""
+    if verbose:
+        for cmd in cmds:
+            print(" ".join(cmd), flush=True)
+    procs = [subprocess.Popen(c, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True) for c in cmds]
+    for p, (_, err) in zip(procs, [p.communicate() for p in procs]):
+        errs = [l for l in err.splitlines() if "packed-fp32-ops" not in l]
+        if p.returncode != 0:
+            raise RuntimeError(f"{what} failed:\n" + "\n".join(errs))
+        if verbose and errs:
+            print("\n".join(errs))
+
+
+def _object(source: str, suffix: str) -> str:
+    return os.path.join(BUILD, os.path.splitext(os.path.basename(source))[0] + suffix)
+
+
+def build(verbose: bool = False) -> str:
+    os.makedirs(BUILD, exist_ok=True)
+    tmp = LIB + ".tmp"
+    objs = [_object(s, ".o") for s in SOURCES]
+    flags = [f for f in HIPCC_FLAGS if f != "-shared"]
+    _run([[hipcc(), *flags, "-I", os.path.join(ROOT, "include"), "-I", CSRC, "-c", os.path.join(CSRC, s), "-o", o]
+          for s, o in zip(SOURCES, objs)], verbose, "hipcc")
+    _run([[hipcc(), *HIPCC_FLAGS, *objs, "-o", tmp]], verbose, "hipcc (link)")
+    os.replace(tmp, LIB)
+    return LIB
 
 
 def llvm_tool(name: str) -> str:
@@ -57,31 +71,26 @@ def llvm_tool(name: str) -> str:
 def build_hostsan(verbose: bool = False) -> str:
     """A copy of the library whose host code (argument checks, workspace arithmetic, launch
     set-up) is built with AddressSanitizer and UndefinedBehaviorSanitizer, for CPU-side tests.
-    Its device code is the built library's own GPU binary (its .hip_fatbin section), so only
+    Its device code is the built objects' own GPU binaries (their .hip_fatbin sections), so only
     the host pass is compiled here; no device code is instrumented. Load it only in a process
     that preloads the ASan runtime, and never on a GPU."""
-    if not os.path.exists(LIB):
-        raise FileNotFoundError(f"{LIB} is missing: run build() first")
-    os.makedirs(BUILD, exist_ok=True)
-    fatbin = os.path.join(BUILD, "muon_ns_gfx950.hipfb")
-    r = subprocess.run([llvm_tool("llvm-objcopy"), "-O", "binary", "--only-section=.hip_fatbin", LIB, fatbin],
-                       capture_output=True, text=True)
-    if r.returncode != 0 or not os.path.getsize(fatbin):
-        raise RuntimeError("could not extract the GPU binary:\n" + r.stderr)
-    flags = [f for f in HIPCC_FLAGS if f != "-O3"]
+    objs = [_object(s, ".o") for s in SOURCES]
+    if not os.path.exists(LIB) or not all(os.path.exists(o) for o in objs):
+        raise FileNotFoundError(f"{LIB} or its objects are missing: run build() first")
+    fatbins = [_object(s, "_gfx950.hipfb") for s in SOURCES]
+    _run([[llvm_tool("llvm-objcopy"), "-O", "binary", "--only-section=.hip_fatbin", o, f]
+          for o, f in zip(objs, fatbins)], False, "extracting the GPU binary")
+    if not all(os.path.getsize(f) for f in fatbins):
+        raise RuntimeError("an object holds no GPU binary")
+    flags = [f for f in HIPCC_FLAGS if f not in ("-O3", "-shared")]
+    san = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
+           "-Xarch_host", "-fno-sanitize-recover=undefined", "-Xarch_host", "-fno-omit-frame-pointer"]
+    sans = [_object(s, "_hostsan.o") for s in SOURCES]
+    _run([[hipcc(), *flags, "-O1", "-g", *san, "--cuda-host-only", "-Xclang", "-fcuda-include-gpubinary", "-Xclang", f,
+           "-I", os.path.join(ROOT, "include"), "-I", CSRC, "-c", os.path.join(CSRC, s), "-o", o]
+          for s, f, o in zip(SOURCES, fatbins, sans)], verbose, "hipcc (host sanitizers)")
     tmp = HOSTSAN_LIB + ".tmp"
-    cmd = [hipcc(), *flags, "-O1", "-g",
-           "-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
-           "-Xarch_host", "-fno-sanitize-recover=undefined", "-Xarch_host", "-fno-omit-frame-pointer",
-           "--cuda-host-only", "-Xclang", "-fcuda-include-gpubinary", "-Xclang", fatbin,
-           "-I", os.path.join(ROOT, "include"), "-I", CSRC,
-           *[os.path.join(CSRC, s) for s in SOURCES], "-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("hipcc (host sanitizers) failed:\n" +
-                           "\n".join(l for l in r.stderr.splitlines() if "packed-fp32-ops" not in l))
+    _run([[hipcc(), *flags, "-shared", *san, *sans, "-o", tmp]], verbose, "hipcc (host sanitizers, link)")
     os.replace(tmp, HOSTSAN_LIB)
     return HOSTSAN_LIB
 

@@ -1,0 +1,311 @@
+// The experts' matrix products over rows sorted by expert.
+//
+//   forward            Y[s][n]     = sum_k X[s][k] W[e][n][k]     s in expert e's rows
+//   input gradient     dX[s][k]    = sum_n dY[s][n] W[e][n][k]
+//   weight gradient    dW[e][n][k] = sum_s dY[s][n] X[s][k]       s over expert e's rows
+//
+// expert e's rows are offsets[e] .. offsets[e + 1]; W and dW are batches of rows x cols matrices,
+// the layout the Muon step takes. Rows of nobody (from offsets[E] on) get zeros, an expert
+// without rows a zero gradient. Each product is C[i][j] = sum_c A(i, c) B(j, c) on MFMA with fp32
+// accumulation, rounded once; an operand is read contraction-contiguous or contraction-major
+// ("KM"), through gfx950's transposing LDS reads, so nothing is ever transposed in memory:
+//
+//                  i, j, c         A            B
+//   forward        s, n, k         X            W
+//   input grad     s, k, n         dY           W   KM
+//   weight grad    n, k, s         dY  KM       X   KM
+//
+// The row counts live on the GPU only: every workgroup reads the offsets, adds up the experts'
+// tiles in LDS and walks its share of them, so a call never waits for the host. Offsets that run
+// outside 0 .. S are cut to it, and an expert whose end lies before its beginning has no rows.
+#pragma once
+
+#include "norm.hpp"
+
+namespace mns {
+
+constexpr int EXPERT_MAX = 1024;
+
+struct ExpertArgs {
+  const char* A; int64_t lda, sA;   // elements; s: matrix stride of W, unused for row operands
+  const char* B; int64_t ldb, sB;
+  char* C; int64_t ldc, sC;
+  const int32_t* offsets;
+  int experts;
+  int64_t rows;                     // S
+  int n;                            // columns of C (extent of j)
+  int m, k;                         // extents of i / of the contraction, where fixed
+  int tiles_n;
+  int c_vec;                        // 16-byte stores fit C
+};
+
+// Beginning and end of expert e's rows.
+__device__ inline void expert_rows(const ExpertArgs& p, int e, int64_t* lo, int64_t* hi) {
+  const int64_t a = p.offsets[e], b = p.offsets[e + 1];
+  *lo = a < 0 ? 0 : (a > p.rows ? p.rows : a);
+  *hi = b < *lo ? *lo : (b > p.rows ? p.rows : b);
+}
+
+// first[e] = tile rows (of BM) of the experts before e, e = 0 .. E + 1: entry E begins the tile
+// rows over the rows of nobody, entry E + 1 is the total. Ends with a barrier.
+template <int NT, int BM>
+__device__ inline void expert_tiles(const ExpertArgs& p, int* first, int* wsum) {
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  int base = 0;
+  for (int e0 = 0; e0 <= p.experts; e0 += NT) {
+    const int e = e0 + threadIdx.x;
+    int n = 0;
+    if (e < p.experts) {
+      int64_t lo, hi;
+      expert_rows(p, e, &lo, &hi);
+      n = (int)((hi - lo + BM - 1) / BM);
+    } else if (e == p.experts) {
+      const int64_t a = p.offsets[e], lo = a < 0 ? 0 : (a > p.rows ? p.rows : a);
+      n = (int)((p.rows - lo + BM - 1) / BM);
+    }
+    int run = n;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(run, o);
+      if (lane >= o) run += v;
+    }
+    if (lane == 63) wsum[wv] = run;
+    __syncthreads();
+    int before = base, all = 0;
+    for (int w = 0; w < NT / 64; ++w) {
+      if (w < wv) before += wsum[w];
+      all += wsum[w];
+    }
+    base += all;
+    if (e <= p.experts) first[e] = before + run - n;
+    if (e == p.experts) first[e + 1] = before + run;
+    __syncthreads();
+  }
+}
+
+// One output tile: where it lies and what it sums over.
+struct ExpertTile {
+  int64_t a_row, b_row;   // first row of the A / B operand (sorted rows), or its matrix in W
+  int row0, col0;         // of the tile, within its expert's result
+  int m, k;               // rows of the expert's result, contraction length
+  char* c;                // the expert's result
+  const char* a; const char* b;
+};
+
+// 16 bytes of an operand row: elements e0 .. of a row `len` long, zero past the end.
+template <typename T, bool VEC>
+__device__ inline u32x4 load_chunk(const T* row, int e0, int len) {
+  constexpr int N = 16 / (int)sizeof(T);
+  if constexpr (VEC) {
+    return e0 < len ? *reinterpret_cast<const u32x4*>(row + e0) : u32x4{0, 0, 0, 0};
+  } else {
+    typedef T TN __attribute__((ext_vector_type(N)));
+    TN v;
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[e] = e0 + e < len ? row[e0 + e] : (T)0.f;
+    return __builtin_bit_cast(u32x4, v);
+  }
+}
+
+// Which product, with which operands contraction-major.
+enum { EX_FWD = 0, EX_DX = 1, EX_DW = 2 };
+
+// Tile t of the launch's list: expert by expert, within one down the tile rows, then one tile
+// column right, so that tiles that run together share a panel of W in L2.
+template <int MODE, typename T, class CFG>
+__device__ inline ExpertTile expert_tile(const ExpertArgs& p, const int* first, int64_t t) {
+  constexpr int ES = sizeof(T);
+  ExpertTile x;
+  if constexpr (MODE == EX_DW) {
+    const int tiles_m = (p.m + CFG::BM - 1) / CFG::BM, per = tiles_m * p.tiles_n;
+    const int e = (int)(t / per), r = (int)(t - (int64_t)e * per);
+    int64_t lo, hi;
+    expert_rows(p, e, &lo, &hi);
+    x.row0 = (r % tiles_m) * CFG::BM;
+    x.col0 = (r / tiles_m) * CFG::BN;
+    x.m = p.m;
+    x.k = (int)(hi - lo);
+    x.a = p.A + lo * p.lda * ES;
+    x.b = p.B + lo * p.ldb * ES;
+    x.c = p.C + (int64_t)e * p.sC * ES;
+  } else {
+    // the expert whose tiles hold t
+    int e = 0, top = p.experts;
+    while (e < top) {
+      const int mid = (e + top + 1) >> 1;
+      if ((int64_t)first[mid] * p.tiles_n <= t) e = mid; else top = mid - 1;
+    }
+    const int tm = first[e + 1] - first[e];
+    const int r = (int)(t - (int64_t)first[e] * p.tiles_n);
+    int64_t lo, hi;
+    if (e < p.experts) {
+      expert_rows(p, e, &lo, &hi);
+    } else {
+      const int64_t a = p.offsets[e];
+      lo = a < 0 ? 0 : (a > p.rows ? p.rows : a);
+      hi = p.rows;
+    }
+    x.row0 = (r % tm) * CFG::BM;
+    x.col0 = (r / tm) * CFG::BN;
+    x.m = (int)(hi - lo);
+    x.k = e < p.experts ? p.k : 0;
+    x.a = p.A + lo * p.lda * ES;
+    x.b = p.B + (int64_t)(e < p.experts ? e : 0) * p.sB * ES;
+    x.c = p.C + lo * p.ldc * ES;
+  }
+  return x;
+}
+
+// Accumulators to C: through an fp32 slab in LDS, whole rows of 16-byte vectors out.
+template <typename T, class CFG>
+__device__ inline void expert_store(const ExpertArgs& p, const ExpertTile& x, char* lds, const f32x16 (&acc)[CFG::TM][CFG::TN], int lane) {
+  constexpr int BN = CFG::BN, NT = CFG::NT, WTM = CFG::WTM, CP = CFG::CP;
+  constexpr int SR = CFG::SR, SROWS = SR * WTM, VPR = BN / 8;
+  const int wave = wave_uniform(threadIdx.x >> 6), tid = wave * 64 + lane;
+  const int wm = wave / CFG::WVN, wn = wave % CFG::WVN;
+  constexpr int DT = sizeof(T) == 4 ? F32 : (__is_same(T, __bf16) ? BF16 : F16);
+  float* Cs = reinterpret_cast<float*>(lds);
+  for (int sl = 0; sl < CFG::WVM / SR; ++sl) {
+    if (wm / SR == sl) acc_to_slab<CFG>(Cs, acc, lane, wn, (wm % SR) * WTM);
+    lds_barrier();
+#pragma unroll 1
+    for (int idx = tid; idx < SROWS * VPR; idx += NT) {
+      const int lr = idx / VPR, lc = (idx - lr * VPR) * 8;
+      const int r = x.row0 + sl * SROWS + lr, c = x.col0 + lc;
+      if (r < x.m && c < p.n) {
+        const f32x4 a = *reinterpret_cast<const f32x4*>(Cs + lr * CP + lc);
+        const f32x4 b = *reinterpret_cast<const f32x4*>(Cs + lr * CP + lc + 4);
+        const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+        T* out = reinterpret_cast<T*>(x.c) + (int64_t)r * p.ldc;
+        if (p.c_vec && c + 8 <= p.n) {
+          VecIO<T>::store(out, c, v);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (c + e < p.n) store_elem(out, DT, c + e, v[e]);
+        }
+      }
+    }
+    lds_barrier();
+  }
+}
+
+// Operands staged through registers: every type and any alignment (VEC: rows of whole 16-byte
+// chunks). 128 x 128 tiles of 4 waves.
+template <int MODE, typename T, bool VEC, class CFG>
+__global__ void __launch_bounds__(CFG::NT, CFG::OCC) expert_gemm_staged(const ExpertArgs p) {
+  constexpr int ES = sizeof(T), BM = CFG::BM, BN = CFG::BN, NT = CFG::NT, KB = CFG::KB, ROWB = CFG::ROWB;
+  constexpr int EPC = 16 / ES, BK = KB / ES, CPR = CFG::CPR, TM = CFG::TM, TN = CFG::TN;
+  constexpr bool AKM = MODE == EX_DW, BKM = MODE != EX_FWD;
+  constexpr int CPM = BM * ES / 16, CPN = BN * ES / 16;   // chunks per contraction-major row
+  __shared__ __align__(16) char lds[CFG::LDS];
+  __shared__ int first[EXPERT_MAX + 2];
+  __shared__ int wsum[NT / 64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = wave_uniform(tid >> 6);
+  const int wm = wave / CFG::WVN, wn = wave % CFG::WVN;
+  int64_t total;
+  if constexpr (MODE == EX_DW) {
+    total = (int64_t)p.experts * ((p.m + BM - 1) / BM) * p.tiles_n;
+  } else {
+    expert_tiles<NT, BM>(p, first, wsum);
+    total = (int64_t)first[p.experts + 1] * p.tiles_n;
+  }
+  // XCD x takes the x-th eighth of the list: neighbouring tiles share an L2
+  const int xcd = blockIdx.x & 7;
+  const int64_t lo = total * xcd / 8, hi = total * (xcd + 1) / 8;
+  for (int64_t t = lo + (blockIdx.x >> 3); t < hi; t += gridDim.x >> 3) {
+    const ExpertTile x = expert_tile<MODE, T, CFG>(p, first, t);
+    f32x16 acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+    const T* A = reinterpret_cast<const T*>(x.a);
+    const T* B = reinterpret_cast<const T*>(x.b);
+    u32x4 ra[CFG::CA], rb[CFG::CB];
+    const u32x4 zero = {0, 0, 0, 0};
+    auto load_stage = [&](int k0) {
+#pragma unroll
+      for (int q = 0; q < CFG::CA; ++q) {
+        const int c = tid + NT * q;
+        if constexpr (AKM) {
+          const int k = k0 + c / CPM, i = x.row0 + (c % CPM) * EPC;
+          ra[q] = k < x.k ? load_chunk<T, VEC>(A + (int64_t)k * p.lda, i, x.m) : zero;
+        } else {
+          const int i = x.row0 + c / CPR;
+          ra[q] = i < x.m ? load_chunk<T, VEC>(A + (int64_t)i * p.lda, k0 + (c % CPR) * EPC, x.k) : zero;
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < CFG::CB; ++q) {
+        const int c = tid + NT * q;
+        if constexpr (BKM) {
+          const int k = k0 + c / CPN, j = x.col0 + (c % CPN) * EPC;
+          rb[q] = k < x.k ? load_chunk<T, VEC>(B + (int64_t)k * p.ldb, j, p.n) : zero;
+        } else {
+          const int j = x.col0 + c / CPR;
+          rb[q] = j < p.n ? load_chunk<T, VEC>(B + (int64_t)j * p.ldb, k0 + (c % CPR) * EPC, x.k) : zero;
+        }
+      }
+    };
+    auto store_stage = [&](int buf) {
+      char* As = lds + buf * CFG::STAGE;
+      char* Bs = As + BM * ROWB;
+#pragma unroll
+      for (int q = 0; q < CFG::CA; ++q) {
+        const int c = tid + NT * q;
+        if constexpr (AKM)
+          *reinterpret_cast<u32x4*>(As + (c / CPM) * (BM * ES) + (((c % CPM) ^ kmajor_swizzle((c / CPM) & 3)) << 4)) = ra[q];
+        else
+          *reinterpret_cast<u32x4*>(As + (c / CPR) * ROWB + (c % CPR) * 16) = ra[q];
+      }
+#pragma unroll
+      for (int q = 0; q < CFG::CB; ++q) {
+        const int c = tid + NT * q;
+        if constexpr (BKM)
+          *reinterpret_cast<u32x4*>(Bs + (c / CPN) * (BN * ES) + (((c % CPN) ^ kmajor_swizzle((c / CPN) & 3)) << 4)) = rb[q];
+        else
+          *reinterpret_cast<u32x4*>(Bs + (c / CPR) * ROWB + (c % CPR) * 16) = rb[q];
+      }
+    };
+    typedef typename Frag<T>::type F;
+    F fa[TM], fb[TN];
+    int aoff[TM], boff[TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i) aoff[i] = AKM ? kmajor_frag_off<BM * ES>(lane, wm * CFG::WTM + i * 32) : 0;
+#pragma unroll
+    for (int j = 0; j < TN; ++j) boff[j] = BKM ? kmajor_frag_off<BN * ES>(lane, wn * CFG::WTN + j * 32) : 0;
+    const int nk = (x.k + BK - 1) / BK;
+    if (nk) {
+      load_stage(0);
+      store_stage(0);
+      __syncthreads();
+    }
+    for (int kt = 0; kt < nk; ++kt) {
+      if (kt + 1 < nk) load_stage((kt + 1) * BK);
+      const char* As = lds + (kt & 1) * CFG::STAGE;
+      const char* Bs = As + BM * ROWB;
+#pragma unroll
+      for (int g = 0; g < CFG::NG; ++g) {
+        if constexpr (!AKM)
+          load_frags<T, TM, TN, ROWB, !BKM>(As + (wm * CFG::WTM) * ROWB, Bs + (wn * CFG::WTN) * ROWB, lane, g, fa, fb);
+        else if constexpr (ES == 2)
+          load_b_kmajor<T, TM, BM * ES>(As, aoff, g, fa);
+        else
+          load_b_kmajor_f32<TM, BM * ES>(As, lane, wm * CFG::WTM, g, fa);
+        if constexpr (BKM && ES == 2)
+          load_b_kmajor<T, TN, BN * ES>(Bs, boff, g, fb);
+        else if constexpr (BKM)
+          load_b_kmajor_f32<TN, BN * ES>(Bs, lane, wn * CFG::WTN, g, fb);
+        mma<T, TM, TN>(fa, fb, acc);
+      }
+      if (kt + 1 < nk) store_stage((kt & 1) ^ 1);
+      __syncthreads();
+    }
+    expert_store<T, CFG>(p, x, lds, acc, lane);
+  }
+}
+
+}  // namespace mns

@@ -93,6 +93,25 @@ def declare(lib):
     lib.adamw_step.argtypes = [ctypes.c_int, pp, pp, pp, pp, P(ctypes.c_int64), ctypes.c_int32,
                                P(MnsAdamwParams), vp]
     lib.adamw_step.restype = ctypes.c_int
+    t, i32, i64 = P(MnsTensor), ctypes.c_int32, ctypes.c_int64
+    layer = {
+        "layer_norm": [t, vp, vp, i32, ctypes.c_float, t, vp, vp, vp],
+        "mns_layer_norm_workspace_bytes": [t, P(sz)],
+        "layer_norm_backward": [t, t, vp, vp, vp, i32, t, vp, vp, vp, sz, vp],
+        "mns_expert_sort_workspace_bytes": [i64, i32, P(sz)],
+        "expert_sort": [vp, i32, i64, i32, vp, vp, vp, sz, vp],
+        "expert_dispatch": [t, vp, i32, vp, i32, t, vp],
+        "expert_dispatch_backward": [t, vp, i32, t, vp],
+        "expert_combine": [t, vp, i32, vp, i32, t, vp],
+        "expert_combine_backward": [t, t, vp, i32, vp, i32, vp, i32, t, vp, vp],
+        "expert_matmul": [t, t, vp, t, vp],
+        "expert_matmul_grad_input": [t, t, vp, t, vp],
+        "expert_matmul_grad_weight": [t, t, vp, t, vp],
+    }
+    for name, argtypes in layer.items():
+        fn = getattr(lib, name)
+        fn.argtypes = argtypes
+        fn.restype = ctypes.c_int
     lib.mns_status_string.argtypes = [ctypes.c_int]
     lib.mns_status_string.restype = ctypes.c_char_p
     lib.mns_last_hip_error.argtypes = []
@@ -492,6 +511,313 @@ def hybrid_step(matrix_groups, vector_params, *, muon: dict, adamw: dict):
     if vector_params:
         ps, gs, ms, vs = (list(x) for x in zip(*vector_params))
         adamw_step(ps, gs, ms, vs, **adamw)
+
+
+# ------------------------------------------------------------------ the layer around the experts
+# Layer norm and a mixture of experts, forward and backward, next to the optimizer that takes
+# their gradients: expert_matmul_backward's dW is muon_step's G, the norm's are adamw_step's.
+# Gradients are explicit calls; a call that autograd would have to record is refused.
+
+MAX_EXPERTS = 1024
+
+
+def _check_recorded(what, *ts):
+    if _torch().is_grad_enabled():
+        for t in ts:
+            if t is not None and t.requires_grad:
+                raise RuntimeError(f"{what}: not recorded by autograd; call it under torch.no_grad() (or in an "
+                                   "autograd.Function) and its gradient explicitly")
+
+
+def _check_rows(what, ref, **named):
+    """Row buffers: 2-D tensors of ref's dtype."""
+    for name, t in named.items():
+        if t is None:
+            continue
+        if t.dim() != 2:
+            raise ValueError(f"{what}: {name} must be 2-D, got {t.dim()}-D")
+        if t.dtype != ref.dtype:
+            raise TypeError(f"{what}: {name} is {t.dtype}, expected {ref.dtype}")
+
+
+def _check_shape(what, name, t, shape):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _check_flat(what, ref, dtypes, **named):
+    """Contiguous buffers of one of the dtypes."""
+    for name, t in named.items():
+        if t is None:
+            continue
+        if t.dtype not in dtypes:
+            raise TypeError(f"{what}: {name} is {t.dtype}, expected " + " or ".join(str(d) for d in dtypes))
+        if not t.is_contiguous():
+            raise ValueError(f"{what}: {name} must be contiguous")
+
+
+def _check_rank(what, rank, offsets=None):
+    torch = _torch()
+    if rank.dim() != 2:
+        raise ValueError(f"{what}: rank must be [tokens, k], got {rank.dim()}-D")
+    _check_flat(what, rank, (torch.int32,), rank=rank, offsets=offsets)
+    if offsets is not None:
+        _check_offsets(what, offsets)
+
+
+def _check_offsets(what, offsets):
+    torch = _torch()
+    _check_flat(what, offsets, (torch.int32,), offsets=offsets)
+    if offsets.dim() != 1 or not 2 <= offsets.numel() <= MAX_EXPERTS + 1:
+        raise ValueError(f"{what}: offsets must be [experts + 1] with 1 to {MAX_EXPERTS} experts, got {tuple(offsets.shape)}")
+
+
+def _ptr(t):
+    return None if t is None or t.numel() == 0 else t.data_ptr()
+
+
+def _launch(what, ref, *args):
+    """Call the C function `what` on ref's device and its current stream there."""
+    torch = _torch()
+    fn = getattr(_lib(), what)
+    if ref.device.index == torch.cuda.current_device():
+        code = fn(*args, torch.cuda.current_stream(ref.device).cuda_stream)
+    else:
+        with torch.cuda.device(ref.device):
+            code = fn(*args, torch.cuda.current_stream(ref.device).cuda_stream)
+    _check(code, what)
+
+
+def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, out=None):
+    """(y, mean, rstd): layer norm over the columns of x ([rows, cols] or [batch, rows, cols]; C ABI
+    ``layer_norm``). weight and bias: [cols] of x's dtype or float32. mean and rstd: float32, one per
+    row, for the backward pass."""
+    torch = _torch()
+    what = "layer_norm"
+    _check_recorded(what, x, weight, bias)
+    xd = describe(x)
+    params = [t for t in (weight, bias) if t is not None]
+    _check_flat(what, x, (x.dtype, torch.float32), weight=weight, bias=bias)
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None:
+            _check_shape(what, name, t, x.shape[-1:])
+    if len(params) == 2 and weight.dtype != bias.dtype:
+        raise TypeError(f"{what}: weight is {weight.dtype}, bias is {bias.dtype}")
+    if out is not None:
+        _check_same_shape(what, x, out=out)
+        if out.dtype != x.dtype:
+            raise TypeError(f"{what}: out must have x's dtype {x.dtype}, got {out.dtype}")
+    _check_device(what, x, weight=weight, bias=bias, out=out)
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
+    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    _launch(what, x, xd, _ptr(weight), _ptr(bias), dtype_code(params[0]) if params else F32, eps, describe(y),
+            _ptr(mean), _ptr(rstd))
+    return y, mean, rstd
+
+
+def layer_norm_workspace_bytes(x) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib().mns_layer_norm_workspace_bytes(ctypes.byref(describe(x)), ctypes.byref(n)), "mns_layer_norm_workspace_bytes")
+    return n.value
+
+
+def layer_norm_backward(dy, x, mean, rstd, weight=None, *, param_grads: bool = True, out=None, workspace=None):
+    """(dx, dweight, dbias) of layer_norm (C ABI ``layer_norm_backward``). dweight and dbias have
+    weight's dtype; they are None without weight or with param_grads=False."""
+    torch = _torch()
+    what = "layer_norm_backward"
+    _check_recorded(what, dy, x, weight)
+    _check_same_shape(what, x, dy=dy, out=out)
+    for name, t in (("dy", dy), ("out", out)):
+        if t is not None and t.dtype != x.dtype:
+            raise TypeError(f"{what}: {name} is {t.dtype}, expected {x.dtype}")
+    _check_flat(what, x, (torch.float32,), mean=mean, rstd=rstd)
+    _check_flat(what, x, (x.dtype, torch.float32), weight=weight)
+    for name, t, shape in (("mean", mean, x.shape[:-1]), ("rstd", rstd, x.shape[:-1]), ("weight", weight, x.shape[-1:])):
+        if t is not None:
+            _check_shape(what, name, t, shape)
+    _check_workspace(what, workspace)
+    _check_device(what, x, dy=dy, mean=mean, rstd=rstd, weight=weight, out=out, workspace=workspace)
+    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
+    dw = db = None
+    if weight is not None and param_grads:
+        dw, db = torch.empty_like(weight), torch.empty_like(weight)
+        if workspace is None:
+            workspace = torch.empty(layer_norm_workspace_bytes(x), dtype=torch.uint8, device=x.device)
+    _launch(what, x, describe(dy), describe(x), _ptr(mean), _ptr(rstd), _ptr(weight),
+            dtype_code(weight) if weight is not None else F32, describe(dx), _ptr(dw), _ptr(db), _ptr(workspace),
+            0 if workspace is None else _ws_bytes(workspace))
+    return dx, dw, db
+
+
+def expert_sort_workspace_bytes(slots: int, num_experts: int) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib().mns_expert_sort_workspace_bytes(slots, num_experts, ctypes.byref(n)), "mns_expert_sort_workspace_bytes")
+    return n.value
+
+
+def expert_sort(experts, num_experts: int, *, workspace=None):
+    """(offsets, rank) of the picks experts ([tokens, k] int32 or int64; C ABI ``expert_sort``): expert
+    e's sorted rows are offsets[e] .. offsets[e + 1] - 1 (int32 [num_experts + 1]), rank[t, j] is the
+    row of token t's j-th pick (int32 [tokens, k]), -1 for a pick outside 0 .. num_experts - 1."""
+    torch = _torch()
+    what = "expert_sort"
+    if experts.dim() != 2 or experts.shape[1] < 1:
+        raise ValueError(f"{what}: experts must be [tokens, k], got {tuple(experts.shape)}")
+    if not 1 <= num_experts <= MAX_EXPERTS:
+        raise ValueError(f"{what}: num_experts must be 1 to {MAX_EXPERTS}, got {num_experts}")
+    _check_flat(what, experts, (torch.int32, torch.int64), experts=experts)
+    _check_workspace(what, workspace)
+    _check_device(what, experts, workspace=workspace)
+    slots = experts.numel()
+    offsets = torch.empty(num_experts + 1, dtype=torch.int32, device=experts.device)
+    rank = torch.empty(experts.shape, dtype=torch.int32, device=experts.device)
+    if workspace is None:
+        n = expert_sort_workspace_bytes(slots, num_experts)
+        workspace = torch.empty(n, dtype=torch.uint8, device=experts.device) if n else None
+    _launch(what, experts, _ptr(experts), experts.element_size(), slots, num_experts, offsets.data_ptr(), _ptr(rank),
+            _ptr(workspace), 0 if workspace is None else _ws_bytes(workspace))
+    return offsets, rank
+
+
+def expert_dispatch(x, rank, offsets, *, out=None):
+    """The tokens' rows sorted by expert: out[rank[t, j]] = x[t], the rows of no expert zero
+    ([tokens * k, dim]; C ABI ``expert_dispatch``)."""
+    torch = _torch()
+    what = "expert_dispatch"
+    _check_recorded(what, x)
+    _check_rank(what, rank, offsets)
+    _check_rows(what, x, x=x, out=out)
+    _check_shape(what, "rank", rank, (x.shape[0], rank.shape[1]))
+    if out is not None:
+        _check_shape(what, "out", out, (rank.numel(), x.shape[1]))
+    _check_device(what, x, rank=rank, offsets=offsets, out=out)
+    xs = torch.empty(rank.numel(), x.shape[1], dtype=x.dtype, device=x.device) if out is None else out
+    _launch(what, x, describe(x), _ptr(rank), rank.shape[1], offsets.data_ptr(), offsets.numel() - 1, describe(xs))
+    return xs
+
+
+def expert_dispatch_backward(dxs, rank, *, out=None):
+    """dx[t] = sum_j dxs[rank[t, j]] (C ABI ``expert_dispatch_backward``)."""
+    torch = _torch()
+    what = "expert_dispatch_backward"
+    _check_recorded(what, dxs)
+    _check_rank(what, rank)
+    _check_rows(what, dxs, dxs=dxs, out=out)
+    _check_shape(what, "dxs", dxs, (rank.numel(), dxs.shape[1]))
+    if out is not None:
+        _check_shape(what, "out", out, (rank.shape[0], dxs.shape[1]))
+    _check_device(what, dxs, rank=rank, out=out)
+    dx = torch.empty(rank.shape[0], dxs.shape[1], dtype=dxs.dtype, device=dxs.device) if out is None else out
+    _launch(what, dxs, describe(dxs), _ptr(rank), rank.shape[1], describe(dx))
+    return dx
+
+
+def expert_combine(ys, weights, rank, *, out=None):
+    """y[t] = sum_j weights[t, j] ys[rank[t, j]] (C ABI ``expert_combine``). weights: [tokens, k] of ys's
+    dtype or float32; a slot without a row adds nothing, whatever its weight."""
+    torch = _torch()
+    what = "expert_combine"
+    _check_recorded(what, ys, weights)
+    _check_rank(what, rank)
+    _check_rows(what, ys, ys=ys, out=out)
+    _check_flat(what, ys, (ys.dtype, torch.float32), weights=weights)
+    _check_shape(what, "weights", weights, rank.shape)
+    _check_shape(what, "ys", ys, (rank.numel(), ys.shape[1]))
+    if out is not None:
+        _check_shape(what, "out", out, (rank.shape[0], ys.shape[1]))
+    _check_device(what, ys, weights=weights, rank=rank, out=out)
+    y = torch.empty(rank.shape[0], ys.shape[1], dtype=ys.dtype, device=ys.device) if out is None else out
+    _launch(what, ys, describe(ys), _ptr(weights), dtype_code(weights), _ptr(rank), rank.shape[1], describe(y))
+    return y
+
+
+def expert_combine_backward(dy, ys, weights, rank, offsets, *, out=None):
+    """(dys, dweights) of expert_combine (C ABI ``expert_combine_backward``); dweights has weights'
+    dtype, 0 for a slot without a row."""
+    torch = _torch()
+    what = "expert_combine_backward"
+    _check_recorded(what, dy, ys, weights)
+    _check_rank(what, rank, offsets)
+    _check_rows(what, ys, dy=dy, ys=ys, out=out)
+    _check_flat(what, ys, (ys.dtype, torch.float32), weights=weights)
+    _check_shape(what, "weights", weights, rank.shape)
+    _check_shape(what, "ys", ys, (rank.numel(), ys.shape[1]))
+    _check_shape(what, "dy", dy, (rank.shape[0], ys.shape[1]))
+    if out is not None:
+        _check_shape(what, "out", out, ys.shape)
+    _check_device(what, ys, dy=dy, weights=weights, rank=rank, offsets=offsets, out=out)
+    dys = torch.empty(ys.shape, dtype=ys.dtype, device=ys.device) if out is None else out
+    dw = torch.empty_like(weights)
+    _launch(what, ys, describe(dy), describe(ys), _ptr(weights), dtype_code(weights), _ptr(rank), rank.shape[1],
+            offsets.data_ptr(), offsets.numel() - 1, describe(dys), _ptr(dw))
+    return dys, dw
+
+
+def _check_product(what, w, offsets, **rows):
+    _check_recorded(what, w, *rows.values())
+    _check_offsets(what, offsets)
+    if w.dim() != 3:
+        raise ValueError(f"{what}: w must be [experts, rows, cols], got {w.dim()}-D")
+    if w.shape[0] != offsets.numel() - 1:
+        raise ValueError(f"{what}: w holds {w.shape[0]} experts, offsets {offsets.numel() - 1}")
+    _check_rows(what, w, **rows)
+
+
+def expert_matmul(x, w, offsets, *, out=None):
+    """y[s] = w[e] x[s] for the rows s of expert e, the rows of no expert zero (C ABI ``expert_matmul``).
+    x: [rows, K] sorted by expert, w: [experts, N, K], offsets as expert_sort gives them."""
+    torch = _torch()
+    what = "expert_matmul"
+    _check_product(what, w, offsets, x=x, out=out)
+    _check_shape(what, "x", x, (x.shape[0], w.shape[2]))
+    if out is not None:
+        _check_shape(what, "out", out, (x.shape[0], w.shape[1]))
+    _check_device(what, x, w=w, offsets=offsets, out=out)
+    y = torch.empty(x.shape[0], w.shape[1], dtype=x.dtype, device=x.device) if out is None else out
+    _launch(what, x, describe(x), describe(w), offsets.data_ptr(), describe(y))
+    return y
+
+
+def expert_matmul_grad_input(dy, w, offsets, *, out=None):
+    """dx[s] = w[e]^T dy[s] for the rows s of expert e (C ABI ``expert_matmul_grad_input``)."""
+    torch = _torch()
+    what = "expert_matmul_grad_input"
+    _check_product(what, w, offsets, dy=dy, out=out)
+    _check_shape(what, "dy", dy, (dy.shape[0], w.shape[1]))
+    if out is not None:
+        _check_shape(what, "out", out, (dy.shape[0], w.shape[2]))
+    _check_device(what, dy, w=w, offsets=offsets, out=out)
+    dx = torch.empty(dy.shape[0], w.shape[2], dtype=dy.dtype, device=dy.device) if out is None else out
+    _launch(what, dy, describe(dy), describe(w), offsets.data_ptr(), describe(dx))
+    return dx
+
+
+def expert_matmul_grad_weight(dy, x, offsets, *, out=None):
+    """dw[e] = sum over expert e's rows of dy[s] x[s]^T, zero for an expert without rows (C ABI
+    ``expert_matmul_grad_weight``): [experts, N, K], the gradient batch that muon_step takes."""
+    torch = _torch()
+    what = "expert_matmul_grad_weight"
+    _check_recorded(what, dy, x, out)
+    _check_offsets(what, offsets)
+    _check_rows(what, x, dy=dy, x=x)
+    _check_shape(what, "dy", dy, (x.shape[0], dy.shape[1]))
+    shape = (offsets.numel() - 1, dy.shape[1], x.shape[1])
+    if out is not None:
+        _check_shape(what, "out", out, shape)
+        if out.dtype != x.dtype:
+            raise TypeError(f"{what}: out is {out.dtype}, expected {x.dtype}")
+    _check_device(what, x, dy=dy, offsets=offsets, out=out)
+    dw = torch.empty(shape, dtype=x.dtype, device=x.device) if out is None else out
+    _launch(what, x, describe(dy), describe(x), offsets.data_ptr(), describe(dw))
+    return dw
+
+
+def expert_matmul_backward(dy, x, w, offsets):
+    """(dx, dw) of expert_matmul."""
+    _check_product("expert_matmul_backward", w, offsets, dy=dy, x=x)
+    return expert_matmul_grad_input(dy, w, offsets), expert_matmul_grad_weight(dy, x, offsets)
 
 
 def gram_trace(G, *, steps: int = DEFAULT_STEPS, coeffs=None, eps: float = DEFAULT_EPS,
