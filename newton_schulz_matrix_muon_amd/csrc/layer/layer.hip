@@ -93,7 +93,41 @@ int check_wdtype(const mns_tensor* x, int32_t wdtype) {
   return wdtype == x->dtype || wdtype == F32 ? MNS_OK : MNS_ERR_DTYPE;
 }
 
-int norm_parts(int64_t rows) { return (int)std::max<int64_t>(1, std::min<int64_t>(rows, 512)); }
+// Columns that NT threads of VPT pieces hold.
+constexpr int held(int nt, int vpt) { return nt * vpt * 8; }
+constexpr int kNormHeld = held(1024, 2);   // longer rows take the kernels that read them again
+
+// Workgroups that share the rows of a backward pass, each with a part of dweight and dbias: enough
+// to fill the chip (two of 512 threads a CU, or four of 256 where rows are short).
+int norm_parts(int64_t rows, int64_t cols) {
+  return (int)std::max<int64_t>(1, cols <= held(64, 2) ? std::min<int64_t>((rows + 3) / 4, 1024) : std::min<int64_t>(rows, cols <= held(256, 1) ? 1024 : 512));
+}
+
+template <typename T, typename WT, bool VEC>
+void launch_norm_fwd(const NormArgs& a, hipStream_t s) {
+  const dim3 one((unsigned)a.rows), four((unsigned)((a.rows + 3) / 4));
+  if (a.cols <= held(64, 1)) hipLaunchKernelGGL((norm_fwd_row<T, WT, 64, 1, VEC>), four, dim3(256), 0, s, a);
+  else if (a.cols <= held(64, 2)) hipLaunchKernelGGL((norm_fwd_row<T, WT, 64, 2, VEC>), four, dim3(256), 0, s, a);
+  else if (a.cols <= held(64, 4)) hipLaunchKernelGGL((norm_fwd_row<T, WT, 64, 4, VEC>), four, dim3(256), 0, s, a);
+  else if (a.cols <= held(256, 2)) hipLaunchKernelGGL((norm_fwd_row<T, WT, 256, 2, VEC>), one, dim3(256), 0, s, a);
+  else if (a.cols <= held(256, 4)) hipLaunchKernelGGL((norm_fwd_row<T, WT, 256, 4, VEC>), one, dim3(256), 0, s, a);
+  else if (a.cols <= held(1024, 2)) hipLaunchKernelGGL((norm_fwd_row<T, WT, 1024, 2, VEC>), one, dim3(1024), 0, s, a);
+  else hipLaunchKernelGGL((norm_fwd_any<T, WT>), one, dim3(256), 0, s, a);
+}
+
+template <typename T, typename WT, bool VEC>
+void launch_norm_bwd(const NormArgs& a, hipStream_t s) {
+  const dim3 g((unsigned)a.nparts);
+  if (a.cols <= held(64, 1)) hipLaunchKernelGGL((norm_bwd_row<T, WT, 64, 1, VEC>), g, dim3(256), 0, s, a);
+  else if (a.cols <= held(64, 2)) hipLaunchKernelGGL((norm_bwd_row<T, WT, 64, 2, VEC>), g, dim3(256), 0, s, a);
+  else if (a.cols <= held(256, 1)) hipLaunchKernelGGL((norm_bwd_row<T, WT, 256, 1, VEC>), g, dim3(256), 0, s, a);
+  else if (a.cols <= held(256, 2)) hipLaunchKernelGGL((norm_bwd_row<T, WT, 256, 2, VEC>), g, dim3(256), 0, s, a);
+  else if (a.cols <= held(512, 2)) {
+    // wider elements, or single ones, need the registers of two pieces for one
+    if constexpr (VEC && sizeof(T) == 2) hipLaunchKernelGGL((norm_bwd_row<T, WT, 512, 2, VEC>), g, dim3(512), 0, s, a);
+    else hipLaunchKernelGGL((norm_bwd_row<T, WT, 1024, 1, VEC>), g, dim3(1024), 0, s, a);
+  } else hipLaunchKernelGGL((norm_bwd_row<T, WT, 1024, 2, VEC>), g, dim3(1024), 0, s, a);
+}
 
 template <class F>
 int by_norm_types(int dt, int wdt, F&& f) {
@@ -266,11 +300,15 @@ int layer_norm(const mns_tensor* X, const void* weight, const void* bias, int32_
   a.cols = (int)X->cols;
   a.eps = eps;
   a.n = (float)X->cols;
+  const bool vec = vec_rows(X) && vec_rows(Y) && X->cols % 8 == 0 && aligned16(weight) && aligned16(bias);
   const hipStream_t s = as_stream(stream);
   return by_norm_types(X->dtype, wdtype, [&](auto x, auto w) {
     using T = decltype(x);
     using WT = decltype(w);
-    return launch(K_LAYER_NORM, s, [&] { hipLaunchKernelGGL((norm_fwd_any<T, WT>), dim3((unsigned)rows), dim3(256), 0, s, a); });
+    return launch(K_LAYER_NORM, s, [&] {
+      if (vec) launch_norm_fwd<T, WT, true>(a, s);
+      else launch_norm_fwd<T, WT, false>(a, s);
+    });
   });
 }
 
@@ -280,7 +318,7 @@ int mns_layer_norm_workspace_bytes(const mns_tensor* X, size_t* bytes) {
   t.ptr = nullptr;
   if (t.rows > 0) t.ptr = reinterpret_cast<void*>(16);   // the pointer does not matter here
   if (int st = check_rows(&t)) return st;
-  *bytes = (size_t)norm_parts(X->batch * X->rows) * 2 * (size_t)X->cols * 4;
+  *bytes = (size_t)norm_parts(X->batch * X->rows, X->cols) * 2 * (size_t)X->cols * 4;
   return MNS_OK;
 }
 
@@ -294,7 +332,7 @@ int layer_norm_backward(const mns_tensor* dY, const mns_tensor* X, const float* 
   const int64_t rows = X->batch * X->rows;
   if (rows && (!mean || !rstd)) return MNS_ERR_ARG;
   const bool grads = dweight || dbias;
-  const size_t need = (size_t)norm_parts(rows) * 2 * (size_t)X->cols * 4;
+  const size_t need = (size_t)norm_parts(rows, X->cols) * 2 * (size_t)X->cols * 4;
   if (grads && rows && (!ws || ws_bytes < need || !aligned16(ws))) return MNS_ERR_WORKSPACE;
   const int64_t wb = X->cols * dtype_size(wdtype);
   if (clash({span(dX), span(dweight, wb), span(dbias, wb), span(grads ? ws : nullptr, (int64_t)need)},
@@ -310,15 +348,22 @@ int layer_norm_backward(const mns_tensor* dY, const mns_tensor* X, const float* 
   a.rows = rows;
   a.cols = (int)X->cols;
   a.n = (float)X->cols;
-  a.part = reinterpret_cast<float*>(ws);
-  a.nparts = rows ? norm_parts(rows) : 0;
+  a.part = grads ? reinterpret_cast<float*>(ws) : nullptr;
+  a.nparts = rows ? norm_parts(rows, X->cols) : 0;
   a.dw = dweight;
   a.db = dbias;
+  const bool vec = vec_rows(X) && vec_rows(dY) && vec_rows(dX) && X->cols % 8 == 0 && aligned16(weight);
   const hipStream_t s = as_stream(stream);
   return by_norm_types(X->dtype, wdtype, [&](auto x, auto w) {
     using T = decltype(x);
     using WT = decltype(w);
-    if (rows) {
+    if (rows && a.cols <= kNormHeld) {
+      if (int st = launch(K_LAYER_NORM, s, [&] {
+            if (vec) launch_norm_bwd<T, WT, true>(a, s);
+            else launch_norm_bwd<T, WT, false>(a, s);
+          }))
+        return st;
+    } else if (rows) {
       if (int st = launch(K_LAYER_NORM, s, [&] { hipLaunchKernelGGL((norm_dx_any<T, WT>), dim3((unsigned)rows), dim3(256), 0, s, a); })) return st;
       if (grads)
         if (int st = launch(K_LAYER_NORM, s, [&] {
@@ -327,7 +372,7 @@ int layer_norm_backward(const mns_tensor* dY, const mns_tensor* X, const float* 
           return st;
     }
     if (!grads) return (int)MNS_OK;
-    return launch(K_LAYER_NORM, s, [&] { hipLaunchKernelGGL((norm_dw_sum<WT>), dim3((a.cols + 63) / 64), dim3(1024), 0, s, a); });
+    return launch(K_LAYER_NORM, s, [&] { hipLaunchKernelGGL((norm_dw_sum<WT>), dim3((a.cols + 63) / 64, 2), dim3(1024), 0, s, a); });
   });
 }
 

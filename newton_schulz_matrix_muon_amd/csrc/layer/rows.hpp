@@ -67,7 +67,9 @@ __global__ void __launch_bounds__(SORT_NT) sort_place(const SortArgs p) {
   __shared__ int at[SORT_WAVES][SORT_MAX_E];   // next row of (wave, expert)
   __shared__ int scan[SORT_WAVES];
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  for (int i = threadIdx.x; i < SORT_WAVES * p.experts; i += SORT_NT) at[i / p.experts][i % p.experts] = 0;
+  for (int e = threadIdx.x; e < p.experts; e += SORT_NT)
+#pragma unroll
+    for (int w = 0; w < SORT_WAVES; ++w) at[w][e] = 0;
   __syncthreads();
   const int64_t s0 = ((int64_t)blockIdx.x * SORT_WAVES + wv) * 64 * p.steps + lane;
   for (int i = 0; i < p.steps; ++i) {
@@ -83,10 +85,15 @@ __global__ void __launch_bounds__(SORT_NT) sort_place(const SortArgs p) {
       if (p.nblocks == 1) {
         for (int w = 0; w < SORT_WAVES; ++w) total += at[w][e];
       } else {
-        for (int b = 0; b < p.nblocks; ++b) {
-          const int n = p.hist[(int64_t)b * p.experts + e];
-          total += n;
-          before += b < (int)blockIdx.x ? n : 0;
+        for (int b0 = 0; b0 < p.nblocks; b0 += 16) {
+          int n[16];
+#pragma unroll
+          for (int b = 0; b < 16; ++b) n[b] = b0 + b < p.nblocks ? p.hist[(int64_t)(b0 + b) * p.experts + e] : 0;
+#pragma unroll
+          for (int b = 0; b < 16; ++b) {
+            total += n[b];
+            before += b0 + b < (int)blockIdx.x ? n[b] : 0;
+          }
         }
       }
     }
@@ -191,13 +198,18 @@ __global__ void __launch_bounds__(ROWS_NT) rows_dispatch(const RowsArgs p) {
   zero_rest<U, ROWS_NT>(p, p.out, p.out_ld);
 }
 
-// V consecutive elements of type T as fp32, and back (V = 8: whole 16-byte vectors; V = 1: any
-// alignment).
-template <typename T, int V>
-__device__ inline void load_v(const char* row, int u, float (&v)[V]) {
-  if constexpr (V == 8) VecIO<T>::load(row, (int64_t)u * 8, v);
-  else v[0] = as_f32(reinterpret_cast<const T*>(row)[u]);
-}
+// V consecutive elements of type T, as loaded, as fp32, and back (V = 8: whole 16-byte vectors;
+// V = 1: any alignment).
+template <typename T, int V> struct Unit {
+  typename VecIO<T>::raw v;
+  __device__ inline void load(const char* row, int u) { v = VecIO<T>::load_raw(row, (int64_t)u * 8); }
+  __device__ inline void unpack(float (&f)[V]) const { VecIO<T>::unpack(v, f); }
+};
+template <typename T> struct Unit<T, 1> {
+  T v;
+  __device__ inline void load(const char* row, int u) { v = reinterpret_cast<const T*>(row)[u]; }
+  __device__ inline void unpack(float (&f)[1]) const { f[0] = as_f32(v); }
+};
 template <typename T, int V>
 __device__ inline void store_v(char* row, int u, const float (&v)[V]) {
   if constexpr (V == 8) VecIO<T>::store(row, (int64_t)u * 8, v);
@@ -215,18 +227,24 @@ __global__ void __launch_bounds__(ROWS_NT) rows_gather(const RowsArgs p) {
   for (int e = 0; e < V; ++e) acc[e] = 0.f;
   for (int j0 = 0; j0 < p.k; j0 += ROWS_KU) {
     int r[ROWS_KU];
-    float v[ROWS_KU][V];
+    float w[ROWS_KU];
+    Unit<T, V> v[ROWS_KU];
 #pragma unroll
-    for (int j = 0; j < ROWS_KU; ++j) r[j] = j0 + j < p.k ? p.rank[t * p.k + j0 + j] : -1;
+    for (int j = 0; j < ROWS_KU; ++j) {
+      r[j] = j0 + j < p.k ? p.rank[t * p.k + j0 + j] : -1;
+      w[j] = WEIGHTED && j0 + j < p.k ? load_elem(p.weights, p.w_dt, t * p.k + j0 + j) : 1.f;
+    }
+    // a slot without a row reads row 0 and is left out of the sum: no branch between the loads
 #pragma unroll
     for (int j = 0; j < ROWS_KU; ++j)
-      if (has_row(p, r[j])) load_v<T, V>(p.row + r[j] * p.row_ld, u, v[j]);
+      if (j0 + j < p.k) v[j].load(p.row + (has_row(p, r[j]) ? r[j] : 0) * p.row_ld, u);
 #pragma unroll
     for (int j = 0; j < ROWS_KU; ++j)
       if (has_row(p, r[j])) {
-        const float w = WEIGHTED ? load_elem(p.weights, p.w_dt, t * p.k + j0 + j) : 1.f;
+        float f[V];
+        v[j].unpack(f);
 #pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] += w * v[j][e];
+        for (int e = 0; e < V; ++e) acc[e] += w[j] * f[e];
       }
   }
   store_v<T, V>(p.out + t * p.out_ld, u, acc);
@@ -248,16 +266,21 @@ __global__ void __launch_bounds__(NT) rows_combine_bwd(const RowsArgs p) {
       dot[j] = 0.f;
     }
     for (int u = threadIdx.x; u < p.units; u += NT) {
+      Unit<T, V> gu, y[ROWS_KU];
+      gu.load(dy, u);
+#pragma unroll
+      for (int j = 0; j < ROWS_KU; ++j)
+        if (j0 + j < p.k) y[j].load(p.row + (has_row(p, r[j]) ? r[j] : 0) * p.row_ld, u);
       float g[V];
-      load_v<T, V>(dy, u, g);
+      gu.unpack(g);
 #pragma unroll
       for (int j = 0; j < ROWS_KU; ++j)
         if (has_row(p, r[j])) {
-          float y[V], o[V];
-          load_v<T, V>(p.row + r[j] * p.row_ld, u, y);
+          float f[V], o[V];
+          y[j].unpack(f);
 #pragma unroll
           for (int e = 0; e < V; ++e) {
-            dot[j] += g[e] * y[e];
+            dot[j] += g[e] * f[e];
             o[e] = w[j] * g[e];
           }
           store_v<T, V>(p.out + r[j] * p.out_ld, u, o);
