@@ -39,11 +39,11 @@ struct ExpertArgs {
   int c_vec;                        // 16-byte stores fit C
 };
 
-// Beginning and end of expert e's rows.
-__device__ inline void expert_rows(const ExpertArgs& p, int e, int64_t* lo, int64_t* hi) {
-  const int64_t a = p.offsets[e], b = p.offsets[e + 1];
-  *lo = a < 0 ? 0 : (a > p.rows ? p.rows : a);
-  *hi = b < *lo ? *lo : (b > p.rows ? p.rows : b);
+// Beginning and end of expert e's rows; e = E: the rows of nobody.
+__device__ inline void expert_rows(const ExpertArgs& p, int e, int* lo, int* hi) {
+  const int rows = (int)p.rows, a = p.offsets[e], b = e < p.experts ? p.offsets[e + 1] : rows;
+  *lo = min(max(a, 0), rows);
+  *hi = min(max(b, *lo), rows);
 }
 
 // first[e] = tile rows (of BM) of the experts before e, e = 0 .. E + 1: entry E begins the tile
@@ -55,13 +55,10 @@ __device__ inline void expert_tiles(const ExpertArgs& p, int* first, int* wsum) 
   for (int e0 = 0; e0 <= p.experts; e0 += NT) {
     const int e = e0 + threadIdx.x;
     int n = 0;
-    if (e < p.experts) {
-      int64_t lo, hi;
+    if (e <= p.experts) {
+      int lo, hi;
       expert_rows(p, e, &lo, &hi);
-      n = (int)((hi - lo + BM - 1) / BM);
-    } else if (e == p.experts) {
-      const int64_t a = p.offsets[e], lo = a < 0 ? 0 : (a > p.rows ? p.rows : a);
-      n = (int)((p.rows - lo + BM - 1) / BM);
+      n = (hi - lo + BM - 1) / BM;
     }
     int run = n;
 #pragma unroll
@@ -83,13 +80,13 @@ __device__ inline void expert_tiles(const ExpertArgs& p, int* first, int* wsum) 
   }
 }
 
-// One output tile: where it lies and what it sums over.
+// One output tile: its expert's operands and result, where it lies in the result, and what it
+// sums over. Equal in every lane.
 struct ExpertTile {
-  int64_t a_row, b_row;   // first row of the A / B operand (sorted rows), or its matrix in W
   int row0, col0;         // of the tile, within its expert's result
   int m, k;               // rows of the expert's result, contraction length
-  char* c;                // the expert's result
   const char* a; const char* b;
+  char* c;
 };
 
 // 16 bytes of an operand row: elements e0 .. of a row `len` long, zero past the end.
@@ -116,42 +113,40 @@ template <int MODE, typename T, class CFG>
 __device__ inline ExpertTile expert_tile(const ExpertArgs& p, const int* first, int64_t t) {
   constexpr int ES = sizeof(T);
   ExpertTile x;
+  int e, r, tm;
   if constexpr (MODE == EX_DW) {
-    const int tiles_m = (p.m + CFG::BM - 1) / CFG::BM, per = tiles_m * p.tiles_n;
-    const int e = (int)(t / per), r = (int)(t - (int64_t)e * per);
-    int64_t lo, hi;
-    expert_rows(p, e, &lo, &hi);
-    x.row0 = (r % tiles_m) * CFG::BM;
-    x.col0 = (r / tiles_m) * CFG::BN;
-    x.m = p.m;
-    x.k = (int)(hi - lo);
-    x.a = p.A + lo * p.lda * ES;
-    x.b = p.B + lo * p.ldb * ES;
-    x.c = p.C + (int64_t)e * p.sC * ES;
+    tm = (p.m + CFG::BM - 1) / CFG::BM;
+    e = (int)(t / (tm * p.tiles_n));
+    r = (int)(t - (int64_t)e * tm * p.tiles_n);
   } else {
     // the expert whose tiles hold t
-    int e = 0, top = p.experts;
+    e = 0;
+    int top = p.experts;
     while (e < top) {
       const int mid = (e + top + 1) >> 1;
-      if ((int64_t)first[mid] * p.tiles_n <= t) e = mid; else top = mid - 1;
+      if ((int64_t)wave_uniform(first[mid]) * p.tiles_n <= t) e = mid; else top = mid - 1;
     }
-    const int tm = first[e + 1] - first[e];
-    const int r = (int)(t - (int64_t)first[e] * p.tiles_n);
-    int64_t lo, hi;
-    if (e < p.experts) {
-      expert_rows(p, e, &lo, &hi);
-    } else {
-      const int64_t a = p.offsets[e];
-      lo = a < 0 ? 0 : (a > p.rows ? p.rows : a);
-      hi = p.rows;
-    }
-    x.row0 = (r % tm) * CFG::BM;
-    x.col0 = (r / tm) * CFG::BN;
-    x.m = (int)(hi - lo);
+    const int f = wave_uniform(first[e]);
+    tm = wave_uniform(first[e + 1]) - f;
+    r = (int)(t - (int64_t)f * p.tiles_n);
+  }
+  int lo, hi;
+  expert_rows(p, e, &lo, &hi);
+  lo = wave_uniform(lo);
+  hi = wave_uniform(hi);
+  x.row0 = (r % tm) * CFG::BM;
+  x.col0 = (r / tm) * CFG::BN;
+  x.a = p.A + (int64_t)lo * p.lda * ES;
+  if constexpr (MODE == EX_DW) {
+    x.m = p.m;
+    x.k = hi - lo;
+    x.b = p.B + (int64_t)lo * p.ldb * ES;
+    x.c = p.C + (int64_t)e * p.sC * ES;
+  } else {
+    x.m = hi - lo;
     x.k = e < p.experts ? p.k : 0;
-    x.a = p.A + lo * p.lda * ES;
     x.b = p.B + (int64_t)(e < p.experts ? e : 0) * p.sB * ES;
-    x.c = p.C + lo * p.ldc * ES;
+    x.c = p.C + (int64_t)lo * p.ldc * ES;
   }
   return x;
 }
@@ -305,6 +300,271 @@ __global__ void __launch_bounds__(CFG::NT, CFG::OCC) expert_gemm_staged(const Ex
       __syncthreads();
     }
     expert_store<T, CFG>(p, x, lds, acc, lane);
+  }
+}
+
+// ---------------------------------------------------------------- large products, 16-bit types
+// 256 x 256 tiles, 16 waves of 64 x 64 at four per SIMD, operands DMA'd global -> LDS into a ring
+// of two 128-byte (64-element) stages, as the Newton-Schulz products. The tiles of a workgroup
+// form one stream of stages: the next tile's first stage is on its way during this tile's last
+// one and its stores, so a tile pays neither a first wait nor an epilogue in LDS. The stores
+// leave the registers directly: the MFMAs run with the operands swapped, so a lane holds runs of
+// four columns of one row, and one swap of lane halves makes them 16 bytes.
+
+// A value the compiler cannot see through: what is computed from it is computed where it stands
+// and not kept in registers across the loops.
+__device__ inline int opaque(int v) {
+  __asm__ __volatile__("" : "+v"(v));
+  return v;
+}
+
+// acc[i][j] += B_j A_i^T: lane (l, h) register r holds row 32 i + l, column 32 j + 8 (r / 4) + 4 h + r % 4.
+template <typename T, int TM, int TN>
+__device__ inline void mma_swapped(const typename Frag<T>::type (&a)[TM], const typename Frag<T>::type (&b)[TN], f32x16 (&acc)[TM][TN]) {
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      if constexpr (__is_same(T, __bf16)) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[j], a[i], acc[i][j], 0, 0, 0);
+      else acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(b[j], a[i], acc[i][j], 0, 0, 0);
+    }
+}
+
+// The fragments of one k-group: two 32-row blocks of either operand, from a contraction-major
+// stage (KM: two transposing reads a block, see load_b_kmajor) or a contraction-contiguous one (a
+// 16-byte read a block). Reads and their wait stand in one block: for reads that it can see, the
+// compiler waits for the whole DMA queue first, because the next stage's DMA writes the same
+// array (2048 x 7168, 27 experts, 32768 rows: 1100 us with such waits).
+template <typename T, bool AKM, bool BKM, int RBA, int RBB, int NEXT>
+__device__ inline void load_frags_asm(unsigned a0, unsigned a1, unsigned b0, unsigned b1, typename Frag<T>::type (&a)[2],
+                                      typename Frag<T>::type (&b)[2]) {
+  typedef typename Frag<T>::type F;
+  auto join = [](s16x4 lo, s16x4 hi) {
+    return __builtin_bit_cast(F, (s16x8)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+  if constexpr (AKM && BKM) {
+    s16x4 al0, ah0, al1, ah1, bl0, bh0, bl1, bh1;
+    __asm__ __volatile__(
+        "ds_read_b64_tr_b16 %0, %8\n\t"
+        "ds_read_b64_tr_b16 %1, %8 offset:%12\n\t"
+        "ds_read_b64_tr_b16 %2, %9\n\t"
+        "ds_read_b64_tr_b16 %3, %9 offset:%12\n\t"
+        "ds_read_b64_tr_b16 %4, %10\n\t"
+        "ds_read_b64_tr_b16 %5, %10 offset:%13\n\t"
+        "ds_read_b64_tr_b16 %6, %11\n\t"
+        "ds_read_b64_tr_b16 %7, %11 offset:%13\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(al0), "=&v"(ah0), "=&v"(al1), "=&v"(ah1), "=&v"(bl0), "=&v"(bh0), "=&v"(bl1), "=&v"(bh1)
+        : "v"(a0), "v"(a1), "v"(b0), "v"(b1), "i"(4 * RBA), "i"(4 * RBB)
+        : "memory");
+    a[0] = join(al0, ah0);
+    a[1] = join(al1, ah1);
+    b[0] = join(bl0, bh0);
+    b[1] = join(bl1, bh1);
+  } else if constexpr (BKM) {
+    s16x4 bl0, bh0, bl1, bh1;
+    __asm__ __volatile__(
+        "ds_read_b128 %0, %6\n\t"
+        "ds_read_b128 %1, %6 offset:%9\n\t"
+        "ds_read_b64_tr_b16 %2, %7\n\t"
+        "ds_read_b64_tr_b16 %3, %7 offset:%10\n\t"
+        "ds_read_b64_tr_b16 %4, %8\n\t"
+        "ds_read_b64_tr_b16 %5, %8 offset:%10\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(a[0]), "=&v"(a[1]), "=&v"(bl0), "=&v"(bh0), "=&v"(bl1), "=&v"(bh1)
+        : "v"(a0), "v"(b0), "v"(b1), "i"(NEXT), "i"(4 * RBB)
+        : "memory");
+    b[0] = join(bl0, bh0);
+    b[1] = join(bl1, bh1);
+  } else {
+    __asm__ __volatile__(
+        "ds_read_b128 %0, %4\n\t"
+        "ds_read_b128 %1, %4 offset:%6\n\t"
+        "ds_read_b128 %2, %5\n\t"
+        "ds_read_b128 %3, %5 offset:%6\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(a[0]), "=&v"(a[1]), "=&v"(b[0]), "=&v"(b[1])
+        : "v"(a0), "v"(b0), "i"(NEXT)
+        : "memory");
+  }
+}
+
+// Accumulators to C: 16-byte stores, 32 contiguous bytes of 32 rows each. Rows and columns past
+// the end fall to the buffer's range check, so every wave issues TM * TN * 2 stores whatever its
+// tile (the stage stream counts them).
+template <typename T, class CFG>
+__device__ inline void expert_store_direct(const ExpertArgs& p, const ExpertTile& x, const f32x16 (&acc)[CFG::TM][CFG::TN], int lane, int wm, int wn) {
+  const __amdgpu_buffer_rsrc_t rs = make_rsrc(x.c + ((int64_t)x.row0 * p.ldc + x.col0) * 2, 0x7ffffff0u);
+  const int h = lane >> 5;
+#pragma unroll
+  for (int i = 0; i < CFG::TM; ++i) {
+    const int r = wm * CFG::WTM + i * 32 + (lane & 31);
+    const bool rin = x.row0 + r < x.m;
+#pragma unroll
+    for (int j = 0; j < CFG::TN; ++j)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int c = wn * CFG::WTN + j * 32 + q * 16 + h * 8;
+        uint32_t w[2][2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) w[u][e] = pack2<T>(acc[i][j][q * 8 + u * 4 + 2 * e], acc[i][j][q * 8 + u * 4 + 2 * e + 1]);
+        const auto s0 = __builtin_amdgcn_permlane32_swap(w[0][0], w[1][0], false, false);
+        const auto s1 = __builtin_amdgcn_permlane32_swap(w[0][1], w[1][1], false, false);
+        const u32x4 v = {s0[0], s1[0], s0[1], s1[1]};
+        const uint32_t off = rin && x.col0 + c < p.n ? (uint32_t)(r * (int)p.ldc + c) * 2 : OOB;
+        __builtin_amdgcn_raw_buffer_store_b128(v, rs, off, 0, 0);
+      }
+  }
+}
+
+template <int MODE, typename T, class CFG>
+__global__ void __launch_bounds__(CFG::NT, CFG::OCC) expert_gemm_dma(const ExpertArgs p) {
+  constexpr int ES = 2, BM = CFG::BM, BN = CFG::BN, NT = CFG::NT, KB = CFG::KB;
+  constexpr int BK = KB / ES, CPR = CFG::CPR, TM = CFG::TM, TN = CFG::TN, STG = CFG::STG;
+  constexpr bool AKM = MODE == EX_DW, BKM = MODE != EX_FWD;
+  constexpr int NWAVE = NT / 64;
+  constexpr int AW = NWAVE * BM / (BM + BN);           // waves that bring A; the others bring B
+  constexpr int D = (BM + BN) * KB / 1024 / NWAVE;     // 1 KB pieces a wave brings per stage
+  constexpr int STORES = TM * TN * 2;
+  static_assert(sizeof(T) == 2 && TM == 2 && TN == 2 && CPR == 8 && CFG::NST == 2, "tile");
+  static_assert(AW * D * 1024 == BM * KB && (NWAVE - AW) * D * 1024 == BN * KB, "pieces divide over the waves");
+  static_assert(D % 4 == 0, "a wave's pieces begin at a multiple of four");
+  __shared__ __align__(1024) char lds[2 * STG];
+  __shared__ int first[EXPERT_MAX + 2];
+  __shared__ int wsum[NWAVE];
+  const int wave = wave_uniform(threadIdx.x >> 6);
+  const int wm = wave / CFG::WVN, wn = wave % CFG::WVN;
+  const int lane0 = threadIdx.x & 63;
+  int64_t total;
+  if constexpr (MODE == EX_DW) {
+    total = (int64_t)p.experts * ((p.m + BM - 1) / BM) * p.tiles_n;
+  } else {
+    expert_tiles<NT, BM>(p, first, wsum);
+    total = (int64_t)wave_uniform(first[p.experts + 1]) * p.tiles_n;
+  }
+  const int xcd = blockIdx.x & 7;
+  const int64_t hi = total * (xcd + 1) / 8, step = gridDim.x >> 3;
+  int64_t t = total * xcd / 8 + (blockIdx.x >> 3);
+  if (t >= hi) return;
+
+  // what this wave brings of the tile whose stages are being issued: where its operand begins,
+  // bytes from one contraction index to the next, and per piece the lane's offset (past the
+  // range where it lies outside) and contraction index within the stage
+  const bool isa = wave < AW;
+  const int piece0 = (isa ? wave : wave - AW) * D;
+  char* const dst = lds + (isa ? 0 : BM * KB) + piece0 * 1024;
+  const char* src = nullptr;
+  int64_t kstep = 0;
+  uint32_t goff[D];
+  int kin[D];
+  int klen = 0;
+  auto aim = [&](const ExpertTile& x) {
+    const bool km = isa ? AKM : BKM;
+    const int64_t ld = isa ? p.lda : p.ldb;
+    const int lo = isa ? x.row0 : x.col0, ext = (isa ? x.m : p.n) - lo;   // extent of i or j from the tile on
+    klen = x.k;
+    kstep = km ? ld * ES : ES;
+    src = (isa ? x.a : x.b) + (km ? (int64_t)lo * ES : (int64_t)lo * ld * ES);
+    const int lane = opaque(lane0);
+#pragma unroll
+    for (int j = 0; j < D; ++j) {
+      if (km) {
+        constexpr int CPK = BM * ES / 16;                // chunks of a contraction row (BM = BN)
+        const int k = (piece0 + j) * (1024 / (BM * ES)) + lane / CPK;
+        const int c = ((lane % CPK) ^ kmajor_swizzle(k & 3)) * 8;
+        kin[j] = k;
+        goff[j] = c < ext ? (uint32_t)(k * (int)ld + c) * ES : OOB;
+      } else {
+        const int r = (piece0 + j) * 8 + lane / CPR;
+        const int c = ((lane % CPR) ^ chunk_swizzle<CPR>(r)) * 8;
+        kin[j] = c;
+        goff[j] = r < ext ? (uint32_t)(r * (int)ld + c) * ES : OOB;
+      }
+    }
+  };
+  static_assert(BM == BN, "one row length of the contraction-major stages");
+  auto issue = [&](int k0, int slot) {
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(src + k0 * kstep, 0x7ffffff0u);
+#pragma unroll
+    for (int j = 0; j < D; ++j) dma16(rs, dst + slot * STG + j * 1024, k0 + kin[j] < klen ? goff[j] : OOB);
+  };
+
+  typedef __attribute__((address_space(3))) const char* lds_ptr;
+  typename Frag<T>::type fa[TM], fb[TN];
+  f32x16 acc[TM][TN];
+  // one stage: all but its last group's products; that group's fragments stay in fa, fb
+  auto stage = [&](int s) {
+    const unsigned sb = (unsigned)(size_t)(lds_ptr)lds + s * STG;
+    const int lane = opaque(lane0);
+    // block 0 and 1 of either operand, k-group 0; a contraction-major group is 16 rows further,
+    // a contiguous one two chunks, whose place depends on the row
+    const unsigned a0 = sb + (AKM ? kmajor_frag_off<BM * ES>(lane, wm * CFG::WTM) : (wm * CFG::WTM + (lane & 31)) * KB);
+    const unsigned a1 = AKM ? sb + kmajor_frag_off<BM * ES>(lane, wm * CFG::WTM + 32) : 0u;
+    const unsigned bb = sb + BM * KB;
+    const unsigned b0 = bb + (BKM ? kmajor_frag_off<BN * ES>(lane, wn * CFG::WTN) : (wn * CFG::WTN + (lane & 31)) * KB);
+    const unsigned b1 = BKM ? bb + kmajor_frag_off<BN * ES>(lane, wn * CFG::WTN + 32) : 0u;
+    const int sw = chunk_swizzle<CPR>(lane & 31);
+#pragma unroll
+    for (int g = 0; g < CFG::NG; ++g) {
+      const unsigned ck = ((2 * g + (lane >> 5)) ^ sw) << 4;
+      load_frags_asm<T, AKM, BKM, BM * ES, BN * ES, 32 * KB>(a0 + (AKM ? 16 * g * BM * ES : ck), a1 + 16 * g * BM * ES,
+                                                             b0 + (BKM ? 16 * g * BN * ES : ck), b1 + 16 * g * BN * ES, fa, fb);
+      if (g + 1 < CFG::NG) mma_swapped<T, TM, TN>(fa, fb, acc);
+    }
+  };
+
+  ExpertTile x = expert_tile<MODE, T, CFG>(p, first, t);
+  aim(x);
+  int slot = 0;                      // of the tile's first stage
+  if (x.k > 0) issue(0, 0);
+  bool begin = true;
+  for (;;) {
+    const int nk = (x.k + BK - 1) / BK;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+    if (nk) {
+      // this tile's first stage: only the stores of the tile before it were issued after it
+      if (begin) wait_vmcnt<0>(); else wait_vmcnt<STORES>();
+      barrier_nofence();
+    }
+    for (int kt = 0; kt + 1 < nk; ++kt) {
+      // the last group of the stage before, whose fragments were read before the barrier
+      if (kt) mma_swapped<T, TM, TN>(fa, fb, acc);
+      issue((kt + 1) * BK, (slot + kt + 1) & 1);
+      stage((slot + kt) & 1);
+      wait_vmcnt<0>();
+      barrier_nofence();
+      pin_frags<T, TM, TN>(fa, fb);
+    }
+    if (nk > 1) mma_swapped<T, TM, TN>(fa, fb, acc);
+    // the last stage, and the next tile's first one into the slot before it
+    const ExpertTile now = x;
+    const int last = slot + nk - 1;
+    slot = (slot + nk) & 1;
+    t += step;
+    const bool more = t < hi;
+    if (more) {
+      x = expert_tile<MODE, T, CFG>(p, first, t);
+      aim(x);
+      if (x.k > 0) issue(0, slot);
+    }
+    if (nk) {
+      stage(last & 1);
+      barrier_nofence();
+      pin_frags<T, TM, TN>(fa, fb);
+      mma_swapped<T, TM, TN>(fa, fb, acc);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    expert_store_direct<T, CFG>(p, now, acc, opaque(lane0), wm, wn);
+    __builtin_amdgcn_sched_barrier(0);
+    if (!more) break;
+    begin = false;
   }
 }
 

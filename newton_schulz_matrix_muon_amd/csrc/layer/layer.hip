@@ -249,6 +249,26 @@ int run_staged(ExpertArgs a, int dt, bool vec, hipStream_t s) {
   });
 }
 
+template <int MODE, class CFG>
+int run_dma(ExpertArgs a, int dt, hipStream_t s) {
+  a.tiles_n = (a.n + CFG::BN - 1) / CFG::BN;
+  const unsigned g = gemm_grid<CFG>(MODE, a, a.n);
+  return launch(K_EXPERT_GEMM, s, [&] {
+    if (dt == BF16) hipLaunchKernelGGL((expert_gemm_dma<MODE, __bf16, CFG>), dim3(g), dim3(CFG::NT), 0, s, a);
+    else hipLaunchKernelGGL((expert_gemm_dma<MODE, _Float16, CFG>), dim3(g), dim3(CFG::NT), 0, s, a);
+  });
+}
+
+// The kernel of a product. The 256 x 256 tiles need 16-bit types and whole 16-byte chunks
+// everywhere, and enough rows to fill them.
+template <int MODE>
+int run_product(const ExpertArgs& a, int dt, bool vec, hipStream_t s) {
+  const bool whole = vec && a.c_vec && a.n % 8 == 0 && dt != F32;
+  const int64_t rows = a.rows / a.experts;
+  if (whole && (MODE == EX_DW ? a.m >= 256 && a.n >= 256 : rows >= 128)) return run_dma<MODE, Tile256>(a, dt, s);
+  return run_staged<MODE, Tile128>(a, dt, vec, s);
+}
+
 ExpertArgs product_args(const mns_tensor* A, const mns_tensor* B, const mns_tensor* C, const int32_t* offsets, int experts, int64_t rows) {
   ExpertArgs a{};
   a.A = reinterpret_cast<const char*>(A->ptr);
@@ -498,7 +518,7 @@ int expert_matmul(const mns_tensor* X, const mns_tensor* W, const int32_t* offse
   if (!X->rows) return MNS_OK;
   ExpertArgs a = product_args(X, W, Y, offsets, (int)W->batch, X->rows);
   a.k = (int)W->cols;
-  return run_staged<EX_FWD, Tile128>(a, W->dtype, vec_rows(X) && vec_rows(W), as_stream(stream));
+  return run_product<EX_FWD>(a, W->dtype, vec_rows(X) && vec_rows(W), as_stream(stream));
 }
 
 int expert_matmul_grad_input(const mns_tensor* dY, const mns_tensor* W, const int32_t* offsets, const mns_tensor* dX, void* stream) {
@@ -508,7 +528,7 @@ int expert_matmul_grad_input(const mns_tensor* dY, const mns_tensor* W, const in
   if (!dY->rows) return MNS_OK;
   ExpertArgs a = product_args(dY, W, dX, offsets, (int)W->batch, dY->rows);
   a.k = (int)W->rows;
-  return run_staged<EX_DX, Tile128>(a, W->dtype, vec_rows(dY) && vec_rows(W), as_stream(stream));
+  return run_product<EX_DX>(a, W->dtype, vec_rows(dY) && vec_rows(W), as_stream(stream));
 }
 
 int expert_matmul_grad_weight(const mns_tensor* dY, const mns_tensor* X, const int32_t* offsets, const mns_tensor* dW, void* stream) {
@@ -517,7 +537,7 @@ int expert_matmul_grad_weight(const mns_tensor* dY, const mns_tensor* X, const i
   if (clash({span(dW)}, {span(dY), span(X), span(offsets, offsets_bytes(dW->batch))})) return MNS_ERR_ARG;
   ExpertArgs a = product_args(dY, X, dW, offsets, (int)dW->batch, dY->rows);
   a.m = (int)dW->rows;
-  return run_staged<EX_DW, Tile128>(a, dW->dtype, vec_rows(dY) && vec_rows(X), as_stream(stream));
+  return run_product<EX_DW>(a, dW->dtype, vec_rows(dY) && vec_rows(X), as_stream(stream));
 }
 
 }  // extern "C"
