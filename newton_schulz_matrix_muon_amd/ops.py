@@ -146,28 +146,32 @@ def _torch():
     return torch
 
 
+_DTYPE_CODES = {}
+
+
 def dtype_code(t) -> int:
-    torch = _torch()
-    m = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
-    if t.dtype not in m:
+    if not _DTYPE_CODES:
+        torch = _torch()
+        _DTYPE_CODES.update({torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16})
+    code = _DTYPE_CODES.get(t.dtype)
+    if code is None:
         raise TypeError(f"unsupported dtype {t.dtype}")
-    return m[t.dtype]
+    return code
 
 
 def describe(t) -> MnsTensor:
     """mns_tensor for a 2-D (one matrix) or 3-D (batch) tensor with unit column stride."""
-    if t.dim() == 2:
-        t3 = t.unsqueeze(0)
-    elif t.dim() == 3:
-        t3 = t
+    shape, strides = t.shape, t.stride()
+    if len(shape) == 2:
+        b, (r, c) = 1, shape
+    elif len(shape) == 3:
+        b, r, c = shape
     else:
         raise ValueError("expected a 2-D matrix or a 3-D batch")
-    if t3.stride(-1) != 1:
+    if strides[-1] != 1:
         raise ValueError("rows must be contiguous (stride(-1) == 1)")
-    b, r, c = t3.shape
-    ld = t3.stride(-2) if r > 1 else c
-    stride = t3.stride(0) if b > 1 else r * ld
-    return MnsTensor(t3.data_ptr(), dtype_code(t3), b, r, c, ld, stride)
+    ld = strides[-2] if r > 1 else c
+    return MnsTensor(t.data_ptr(), dtype_code(t), b, r, c, ld, strides[0] if b > 1 else r * ld)
 
 
 # ------------------------------------------------------------------ argument checks
@@ -522,11 +526,10 @@ MAX_EXPERTS = 1024
 
 
 def _check_recorded(what, *ts):
-    if _torch().is_grad_enabled():
-        for t in ts:
-            if t is not None and t.requires_grad:
-                raise RuntimeError(f"{what}: not recorded by autograd; call it under torch.no_grad() (or in an "
-                                   "autograd.Function) and its gradient explicitly")
+    for t in ts:
+        if t is not None and t.requires_grad and _torch().is_grad_enabled():
+            raise RuntimeError(f"{what}: not recorded by autograd; call it under torch.no_grad() (or in an "
+                               "autograd.Function) and its gradient explicitly")
 
 
 def _check_rows(what, ref, **named):
@@ -581,10 +584,10 @@ def _launch(what, ref, *args):
     torch = _torch()
     fn = getattr(_lib(), what)
     if ref.device.index == torch.cuda.current_device():
-        code = fn(*args, torch.cuda.current_stream(ref.device).cuda_stream)
+        code = fn(*args, torch.cuda.current_stream().cuda_stream)
     else:
         with torch.cuda.device(ref.device):
-            code = fn(*args, torch.cuda.current_stream(ref.device).cuda_stream)
+            code = fn(*args, torch.cuda.current_stream().cuda_stream)
     _check(code, what)
 
 
@@ -608,9 +611,10 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, out=None):
         if out.dtype != x.dtype:
             raise TypeError(f"{what}: out must have x's dtype {x.dtype}, got {out.dtype}")
     _check_device(what, x, weight=weight, bias=bias, out=out)
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
-    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    y = x.new_empty(x.shape) if out is None else out
+    lead = x.shape[:-1]
+    mean = torch.empty(lead, dtype=torch.float32, device=x.device)
+    rstd = torch.empty(lead, dtype=torch.float32, device=x.device)
     _launch(what, x, xd, _ptr(weight), _ptr(bias), dtype_code(params[0]) if params else F32, eps, describe(y),
             _ptr(mean), _ptr(rstd))
     return y, mean, rstd
@@ -639,7 +643,7 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, *, param_grads: bool = T
             _check_shape(what, name, t, shape)
     _check_workspace(what, workspace)
     _check_device(what, x, dy=dy, mean=mean, rstd=rstd, weight=weight, out=out, workspace=workspace)
-    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
+    dx = x.new_empty(x.shape) if out is None else out
     dw = db = None
     if weight is not None and param_grads:
         dw, db = torch.empty_like(weight), torch.empty_like(weight)
@@ -671,8 +675,8 @@ def expert_sort(experts, num_experts: int, *, workspace=None):
     _check_workspace(what, workspace)
     _check_device(what, experts, workspace=workspace)
     slots = experts.numel()
-    offsets = torch.empty(num_experts + 1, dtype=torch.int32, device=experts.device)
-    rank = torch.empty(experts.shape, dtype=torch.int32, device=experts.device)
+    offsets = experts.new_empty(num_experts + 1, dtype=torch.int32)
+    rank = experts.new_empty(experts.shape, dtype=torch.int32)
     if workspace is None:
         n = expert_sort_workspace_bytes(slots, num_experts)
         workspace = torch.empty(n, dtype=torch.uint8, device=experts.device) if n else None
@@ -693,7 +697,7 @@ def expert_dispatch(x, rank, offsets, *, out=None):
     if out is not None:
         _check_shape(what, "out", out, (rank.numel(), x.shape[1]))
     _check_device(what, x, rank=rank, offsets=offsets, out=out)
-    xs = torch.empty(rank.numel(), x.shape[1], dtype=x.dtype, device=x.device) if out is None else out
+    xs = x.new_empty((rank.numel(), x.shape[1])) if out is None else out
     _launch(what, x, describe(x), _ptr(rank), rank.shape[1], offsets.data_ptr(), offsets.numel() - 1, describe(xs))
     return xs
 
@@ -709,7 +713,7 @@ def expert_dispatch_backward(dxs, rank, *, out=None):
     if out is not None:
         _check_shape(what, "out", out, (rank.shape[0], dxs.shape[1]))
     _check_device(what, dxs, rank=rank, out=out)
-    dx = torch.empty(rank.shape[0], dxs.shape[1], dtype=dxs.dtype, device=dxs.device) if out is None else out
+    dx = dxs.new_empty((rank.shape[0], dxs.shape[1])) if out is None else out
     _launch(what, dxs, describe(dxs), _ptr(rank), rank.shape[1], describe(dx))
     return dx
 
@@ -728,7 +732,7 @@ def expert_combine(ys, weights, rank, *, out=None):
     if out is not None:
         _check_shape(what, "out", out, (rank.shape[0], ys.shape[1]))
     _check_device(what, ys, weights=weights, rank=rank, out=out)
-    y = torch.empty(rank.shape[0], ys.shape[1], dtype=ys.dtype, device=ys.device) if out is None else out
+    y = ys.new_empty((rank.shape[0], ys.shape[1])) if out is None else out
     _launch(what, ys, describe(ys), _ptr(weights), dtype_code(weights), _ptr(rank), rank.shape[1], describe(y))
     return y
 
@@ -748,7 +752,7 @@ def expert_combine_backward(dy, ys, weights, rank, offsets, *, out=None):
     if out is not None:
         _check_shape(what, "out", out, ys.shape)
     _check_device(what, ys, dy=dy, weights=weights, rank=rank, offsets=offsets, out=out)
-    dys = torch.empty(ys.shape, dtype=ys.dtype, device=ys.device) if out is None else out
+    dys = ys.new_empty(ys.shape) if out is None else out
     dw = torch.empty_like(weights)
     _launch(what, ys, describe(dy), describe(ys), _ptr(weights), dtype_code(weights), _ptr(rank), rank.shape[1],
             offsets.data_ptr(), offsets.numel() - 1, describe(dys), _ptr(dw))
@@ -775,7 +779,7 @@ def expert_matmul(x, w, offsets, *, out=None):
     if out is not None:
         _check_shape(what, "out", out, (x.shape[0], w.shape[1]))
     _check_device(what, x, w=w, offsets=offsets, out=out)
-    y = torch.empty(x.shape[0], w.shape[1], dtype=x.dtype, device=x.device) if out is None else out
+    y = x.new_empty((x.shape[0], w.shape[1])) if out is None else out
     _launch(what, x, describe(x), describe(w), offsets.data_ptr(), describe(y))
     return y
 
@@ -789,7 +793,7 @@ def expert_matmul_grad_input(dy, w, offsets, *, out=None):
     if out is not None:
         _check_shape(what, "out", out, (dy.shape[0], w.shape[2]))
     _check_device(what, dy, w=w, offsets=offsets, out=out)
-    dx = torch.empty(dy.shape[0], w.shape[2], dtype=dy.dtype, device=dy.device) if out is None else out
+    dx = dy.new_empty((dy.shape[0], w.shape[2])) if out is None else out
     _launch(what, dy, describe(dy), describe(w), offsets.data_ptr(), describe(dx))
     return dx
 
@@ -809,7 +813,7 @@ def expert_matmul_grad_weight(dy, x, offsets, *, out=None):
         if out.dtype != x.dtype:
             raise TypeError(f"{what}: out is {out.dtype}, expected {x.dtype}")
     _check_device(what, x, dy=dy, offsets=offsets, out=out)
-    dw = torch.empty(shape, dtype=x.dtype, device=x.device) if out is None else out
+    dw = x.new_empty(shape) if out is None else out
     _launch(what, x, describe(dy), describe(x), offsets.data_ptr(), describe(dw))
     return dw
 
