@@ -26,6 +26,9 @@ namespace mns {
 
 constexpr int EXPERT_MAX = 1024;
 
+// Which product: forward, input gradient, weight gradient.
+enum { EX_FWD = 0, EX_DX = 1, EX_DW = 2 };
+
 struct ExpertArgs {
   const char* A; int64_t lda, sA;   // elements; s: matrix stride of W, unused for row operands
   const char* B; int64_t ldb, sB;
@@ -104,13 +107,38 @@ __device__ inline u32x4 load_chunk(const T* row, int e0, int len) {
   }
 }
 
-// Which product, with which operands contraction-major.
-enum { EX_FWD = 0, EX_DX = 1, EX_DW = 2 };
+// The part of the launch's tile list that one XCD takes (an eighth, so that neighbouring tiles
+// share an L2), for the workgroups on it to walk side by side. When the last round of whole tiles
+// would leave half of them idle or more, its tiles are cut into an upper and a lower half: the
+// round then takes about 0.6 of a whole one (a half tile still brings all of its columns of W).
+struct ExpertList {
+  int64_t lo;       // first tile
+  int64_t whole;    // whole tiles, then
+  int64_t n;        // all pieces
+};
+template <int MODE, class CFG>
+__device__ inline ExpertList expert_list(const ExpertArgs& p, const int* first) {
+  const int64_t total = (int64_t)p.tiles_n * (MODE == EX_DW ? p.experts * ((p.m + CFG::BM - 1) / CFG::BM) : wave_uniform(first[p.experts + 1]));
+  const int xcd = blockIdx.x & 7, wgs = gridDim.x >> 3;
+  ExpertList l;
+  l.lo = total * xcd / 8;
+  l.n = l.whole = total * (xcd + 1) / 8 - l.lo;
+  const int rest = (int)(l.n % wgs);
+  if (2 * rest <= wgs) {
+    l.whole -= rest;
+    l.n += rest;
+  }
+  return l;
+}
 
-// Tile t of the launch's list: expert by expert, within one down the tile rows, then one tile
-// column right, so that tiles that run together share a panel of W in L2.
+// Piece t of an XCD's list. Tiles go expert by expert, within one in bands of EXPERT_BAND tile
+// rows, down a band, then one tile column right, so that the tiles that run together share panels
+// of both operands in L2.
+constexpr int EXPERT_BAND = 8;
 template <int MODE, typename T, class CFG>
-__device__ inline ExpertTile expert_tile(const ExpertArgs& p, const int* first, int64_t t) {
+__device__ inline ExpertTile expert_tile(const ExpertArgs& p, const int* first, const ExpertList& l, int64_t t) {
+  const int half = t < l.whole ? 0 : 1 + (int)((t - l.whole) & 1);   // 0: whole, 1: upper, 2: lower
+  t = l.lo + (half ? l.whole + ((t - l.whole) >> 1) : t);
   constexpr int ES = sizeof(T);
   ExpertTile x;
   int e, r, tm;
@@ -134,8 +162,10 @@ __device__ inline ExpertTile expert_tile(const ExpertArgs& p, const int* first, 
   expert_rows(p, e, &lo, &hi);
   lo = wave_uniform(lo);
   hi = wave_uniform(hi);
-  x.row0 = (r % tm) * CFG::BM;
-  x.col0 = (r / tm) * CFG::BN;
+  const int band = r / (EXPERT_BAND * p.tiles_n), high = min(tm - band * EXPERT_BAND, EXPERT_BAND);
+  r -= band * EXPERT_BAND * p.tiles_n;
+  x.row0 = (band * EXPERT_BAND + r % high) * CFG::BM;
+  x.col0 = (r / high) * CFG::BN;
   x.a = p.A + (int64_t)lo * p.lda * ES;
   if constexpr (MODE == EX_DW) {
     x.m = p.m;
@@ -147,6 +177,11 @@ __device__ inline ExpertTile expert_tile(const ExpertArgs& p, const int* first, 
     x.k = e < p.experts ? p.k : 0;
     x.b = p.B + (int64_t)(e < p.experts ? e : 0) * p.sB * ES;
     x.c = p.C + (int64_t)lo * p.ldc * ES;
+  }
+  if (half == 1) x.m = min(x.m, x.row0 + CFG::BM / 2);
+  if (half == 2) {
+    x.row0 += CFG::BM / 2;
+    if (x.row0 >= x.m) x.k = 0;   // nothing there: nothing is read, and no store is in range
   }
   return x;
 }
@@ -198,18 +233,10 @@ __global__ void __launch_bounds__(CFG::NT, CFG::OCC) expert_gemm_staged(const Ex
   __shared__ int wsum[NT / 64];
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_uniform(tid >> 6);
   const int wm = wave / CFG::WVN, wn = wave % CFG::WVN;
-  int64_t total;
-  if constexpr (MODE == EX_DW) {
-    total = (int64_t)p.experts * ((p.m + BM - 1) / BM) * p.tiles_n;
-  } else {
-    expert_tiles<NT, BM>(p, first, wsum);
-    total = (int64_t)first[p.experts + 1] * p.tiles_n;
-  }
-  // XCD x takes the x-th eighth of the list: neighbouring tiles share an L2
-  const int xcd = blockIdx.x & 7;
-  const int64_t lo = total * xcd / 8, hi = total * (xcd + 1) / 8;
-  for (int64_t t = lo + (blockIdx.x >> 3); t < hi; t += gridDim.x >> 3) {
-    const ExpertTile x = expert_tile<MODE, T, CFG>(p, first, t);
+  if constexpr (MODE != EX_DW) expert_tiles<NT, BM>(p, first, wsum);
+  const ExpertList l = expert_list<MODE, CFG>(p, first);
+  for (int64_t t = blockIdx.x >> 3; t < l.n; t += gridDim.x >> 3) {
+    const ExpertTile x = expert_tile<MODE, T, CFG>(p, first, l, t);
     f32x16 acc[TM][TN];
 #pragma unroll
     for (int i = 0; i < TM; ++i)
@@ -437,17 +464,11 @@ __global__ void __launch_bounds__(CFG::NT, CFG::OCC) expert_gemm_dma(const Exper
   const int wave = wave_uniform(threadIdx.x >> 6);
   const int wm = wave / CFG::WVN, wn = wave % CFG::WVN;
   const int lane0 = threadIdx.x & 63;
-  int64_t total;
-  if constexpr (MODE == EX_DW) {
-    total = (int64_t)p.experts * ((p.m + BM - 1) / BM) * p.tiles_n;
-  } else {
-    expert_tiles<NT, BM>(p, first, wsum);
-    total = (int64_t)wave_uniform(first[p.experts + 1]) * p.tiles_n;
-  }
-  const int xcd = blockIdx.x & 7;
-  const int64_t hi = total * (xcd + 1) / 8, step = gridDim.x >> 3;
-  int64_t t = total * xcd / 8 + (blockIdx.x >> 3);
-  if (t >= hi) return;
+  if constexpr (MODE != EX_DW) expert_tiles<NT, BM>(p, first, wsum);
+  const ExpertList l = expert_list<MODE, CFG>(p, first);
+  const int64_t step = gridDim.x >> 3;
+  int64_t t = blockIdx.x >> 3;
+  if (t >= l.n) return;
 
   // what this wave brings of the tile whose stages are being issued: where its operand begins,
   // bytes from one contraction index to the next, and per piece the lane's offset (past the
@@ -515,7 +536,7 @@ __global__ void __launch_bounds__(CFG::NT, CFG::OCC) expert_gemm_dma(const Exper
     }
   };
 
-  ExpertTile x = expert_tile<MODE, T, CFG>(p, first, t);
+  ExpertTile x = expert_tile<MODE, T, CFG>(p, first, l, t);
   aim(x);
   int slot = 0;                      // of the tile's first stage
   if (x.k > 0) issue(0, 0);
@@ -533,32 +554,36 @@ __global__ void __launch_bounds__(CFG::NT, CFG::OCC) expert_gemm_dma(const Exper
       if (begin) wait_vmcnt<0>(); else wait_vmcnt<STORES>();
       barrier_nofence();
     }
+    // a wave whose rows all lie outside only brings operands
+    const bool busy = x.row0 + wm * CFG::WTM < x.m;
     for (int kt = 0; kt + 1 < nk; ++kt) {
       // the last group of the stage before, whose fragments were read before the barrier
-      if (kt) mma_swapped<T, TM, TN>(fa, fb, acc);
+      if (kt && busy) mma_swapped<T, TM, TN>(fa, fb, acc);
       issue((kt + 1) * BK, (slot + kt + 1) & 1);
-      stage((slot + kt) & 1);
+      if (busy) stage((slot + kt) & 1);
       wait_vmcnt<0>();
       barrier_nofence();
-      pin_frags<T, TM, TN>(fa, fb);
+      if (busy) pin_frags<T, TM, TN>(fa, fb);
     }
-    if (nk > 1) mma_swapped<T, TM, TN>(fa, fb, acc);
+    if (nk > 1 && busy) mma_swapped<T, TM, TN>(fa, fb, acc);
     // the last stage, and the next tile's first one into the slot before it
     const ExpertTile now = x;
     const int last = slot + nk - 1;
     slot = (slot + nk) & 1;
     t += step;
-    const bool more = t < hi;
+    const bool more = t < l.n;
     if (more) {
-      x = expert_tile<MODE, T, CFG>(p, first, t);
+      x = expert_tile<MODE, T, CFG>(p, first, l, t);
       aim(x);
       if (x.k > 0) issue(0, slot);
     }
     if (nk) {
-      stage(last & 1);
+      if (busy) stage(last & 1);
       barrier_nofence();
-      pin_frags<T, TM, TN>(fa, fb);
-      mma_swapped<T, TM, TN>(fa, fb, acc);
+      if (busy) {
+        pin_frags<T, TM, TN>(fa, fb);
+        mma_swapped<T, TM, TN>(fa, fb, acc);
+      }
     }
     __builtin_amdgcn_sched_barrier(0);
     expert_store_direct<T, CFG>(p, now, acc, opaque(lane0), wm, wn);

@@ -11,6 +11,7 @@
 #include <initializer_list>
 
 #include "../host.hpp"
+#include "expert_few.hpp"
 #include "expert_gemm.hpp"
 #include "norm.hpp"
 #include "rows.hpp"
@@ -224,8 +225,8 @@ int check_product(const mns_tensor* in, const mns_tensor* w, const int32_t* offs
   return check_experts(offsets, (int32_t)w->batch);
 }
 
-// Persistent grid: enough workgroups for every tile the rows could make, at most those the chip
-// holds at once, the same number on each of the eight XCDs.
+// Persistent grid: enough workgroups for both halves of every tile the rows could make, at most
+// those the chip holds at once, the same number on each of the eight XCDs.
 template <class CFG>
 unsigned gemm_grid(int mode, const ExpertArgs& a, int64_t cols_n) {
   const int64_t tn = (cols_n + CFG::BN - 1) / CFG::BN;
@@ -233,7 +234,7 @@ unsigned gemm_grid(int mode, const ExpertArgs& a, int64_t cols_n) {
                                    : (a.rows + CFG::BM - 1) / CFG::BM + std::min<int64_t>(a.experts, a.rows) + 1;
   const int per_cu = std::max(1, std::min((160 * 1024) / (CFG::LDS + 8192), 4 * CFG::OCC / (CFG::NT / 64)));
   const int64_t most = (int64_t)device_cus() * per_cu;
-  return (unsigned)(8 * std::max<int64_t>(1, (std::min(tm * tn, most) + 7) / 8));
+  return (unsigned)(8 * std::max<int64_t>(1, (std::min(2 * tm * tn, most) + 7) / 8));
 }
 
 template <int MODE, class CFG>
@@ -259,12 +260,23 @@ int run_dma(ExpertArgs a, int dt, hipStream_t s) {
   });
 }
 
+// Few rows: a workgroup per 16 rows of each weight matrix that can have any.
+int run_few(const ExpertArgs& a, int dt, hipStream_t s) {
+  const dim3 g((a.n + 15) / 16, (unsigned)std::min<int64_t>(a.experts, a.rows) + 1);
+  return launch(K_EXPERT_GEMM, s, [&] {
+    if (dt == BF16) hipLaunchKernelGGL((expert_few_fwd<__bf16>), g, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((expert_few_fwd<_Float16>), g, dim3(256), 0, s, a);
+  });
+}
+
 // The kernel of a product. The 256 x 256 tiles need 16-bit types and whole 16-byte chunks
-// everywhere, and enough rows to fill them.
+// everywhere, and enough rows to fill them; the forward product of few rows has its own
+// (expert_few.hpp says from where to where).
 template <int MODE>
 int run_product(const ExpertArgs& a, int dt, bool vec, hipStream_t s) {
   const bool whole = vec && a.c_vec && a.n % 8 == 0 && dt != F32;
   const int64_t rows = a.rows / a.experts;
+  if (MODE == EX_FWD && vec && dt != F32 && a.rows <= 4 * a.experts) return run_few(a, dt, s);
   if (whole && (MODE == EX_DW ? a.m >= 256 && a.n >= 256 : rows >= 128)) return run_dma<MODE, Tile256>(a, dt, s);
   return run_staged<MODE, Tile128>(a, dt, vec, s);
 }
