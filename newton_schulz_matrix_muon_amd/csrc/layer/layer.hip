@@ -13,6 +13,7 @@
 #include "../host.hpp"
 #include "expert_few.hpp"
 #include "expert_gemm.hpp"
+#include "expert_pingpong.hpp"
 #include "norm.hpp"
 #include "rows.hpp"
 
@@ -225,8 +226,8 @@ int check_product(const mns_tensor* in, const mns_tensor* w, const int32_t* offs
   return check_experts(offsets, (int32_t)w->batch);
 }
 
-// Persistent grid: enough workgroups for both halves of every tile the rows could make, at most
-// those the chip holds at once, the same number on each of the eight XCDs.
+// Persistent grid: enough workgroups for every tile the rows could make, at most those the chip
+// holds at once, the same number on each of the eight XCDs.
 template <class CFG>
 unsigned gemm_grid(int mode, const ExpertArgs& a, int64_t cols_n) {
   const int64_t tn = (cols_n + CFG::BN - 1) / CFG::BN;
@@ -234,7 +235,7 @@ unsigned gemm_grid(int mode, const ExpertArgs& a, int64_t cols_n) {
                                    : (a.rows + CFG::BM - 1) / CFG::BM + std::min<int64_t>(a.experts, a.rows) + 1;
   const int per_cu = std::max(1, std::min((160 * 1024) / (CFG::LDS + 8192), 4 * CFG::OCC / (CFG::NT / 64)));
   const int64_t most = (int64_t)device_cus() * per_cu;
-  return (unsigned)(8 * std::max<int64_t>(1, (std::min(2 * tm * tn, most) + 7) / 8));
+  return (unsigned)(8 * std::max<int64_t>(1, (std::min(tm * tn, most) + 7) / 8));
 }
 
 template <int MODE, class CFG>
@@ -250,13 +251,13 @@ int run_staged(ExpertArgs a, int dt, bool vec, hipStream_t s) {
   });
 }
 
-template <int MODE, class CFG>
-int run_dma(ExpertArgs a, int dt, hipStream_t s) {
-  a.tiles_n = (a.n + CFG::BN - 1) / CFG::BN;
-  const unsigned g = gemm_grid<CFG>(MODE, a, a.n);
+template <int MODE>
+int run_pingpong(ExpertArgs a, int dt, hipStream_t s) {
+  a.tiles_n = (a.n + TilePP::BN - 1) / TilePP::BN;
+  const unsigned g = gemm_grid<TilePP>(MODE, a, a.n);
   return launch(K_EXPERT_GEMM, s, [&] {
-    if (dt == BF16) hipLaunchKernelGGL((expert_gemm_dma<MODE, __bf16, CFG>), dim3(g), dim3(CFG::NT), 0, s, a);
-    else hipLaunchKernelGGL((expert_gemm_dma<MODE, _Float16, CFG>), dim3(g), dim3(CFG::NT), 0, s, a);
+    if (dt == BF16) hipLaunchKernelGGL((expert_gemm_pp<MODE, __bf16>), dim3(g), dim3(TilePP::NT), 0, s, a);
+    else hipLaunchKernelGGL((expert_gemm_pp<MODE, _Float16>), dim3(g), dim3(TilePP::NT), 0, s, a);
   });
 }
 
@@ -274,10 +275,13 @@ int run_few(const ExpertArgs& a, int dt, hipStream_t s) {
 // (expert_few.hpp says from where to where).
 template <int MODE>
 int run_product(const ExpertArgs& a, int dt, bool vec, hipStream_t s) {
+  // the largest list of the smallest tiles
+  const int64_t tn = (a.n + 127) / 128, tm = MODE == EX_DW ? a.experts * ((a.m + 127) / 128) : a.rows / 128 + a.experts + 1;
+  if (tn * tm > INT32_MAX) return MNS_ERR_SHAPE;
   const bool whole = vec && a.c_vec && a.n % 8 == 0 && dt != F32;
   const int64_t rows = a.rows / a.experts;
   if (MODE == EX_FWD && vec && dt != F32 && a.rows <= 4 * a.experts) return run_few(a, dt, s);
-  if (whole && (MODE == EX_DW ? a.m >= 256 && a.n >= 256 : rows >= 128)) return run_dma<MODE, Tile256>(a, dt, s);
+  if (whole && (MODE == EX_DW ? a.m >= 256 && a.n >= 256 : rows >= 128)) return run_pingpong<MODE>(a, dt, s);
   return run_staged<MODE, Tile128>(a, dt, vec, s);
 }
 
