@@ -4,19 +4,28 @@
 // rows 0-127, waves 4-7 rows 128-255, 128 x 64 each (4 x 2 blocks of the 32x32x16 MFMA). The
 // contraction moves through LDS 64 values (128 bytes) at a time, DMA'd into a ring of two 64 KB
 // stages. Every stage is two steps of 16 MFMAs, and a step is two phases: a wave reads all the
-// step's fragments into registers, then computes from registers alone. The two waves of a SIMD
-// run half a step apart, so one always reads while the other computes; a barrier ends every phase.
+// step's fragments into registers (and, under the latency of the reads, issues its share of the
+// DMA), then computes from registers alone. The two waves of a SIMD run half a step apart, so one
+// always reads while the other computes; a barrier ends every phase.
 //
 // Because a step's reads come in one burst, its part of the stage is free for the stage after
-// next as soon as both halves have read it: the DMA runs one and a half stages ahead of its use in
-// a ring of two. The steps split a stage so that each has its own 1 KB pieces: by rows of A where
-// A is contraction-contiguous (step 1: all of B and rows 0-63 of either half; step 2: the other
-// rows), by the contraction where both operands are contraction-major.
+// next as soon as both halves have read it: the DMA runs one and a quarter to one and a half
+// stages ahead of its use in a ring of two. The steps split a stage so that each has its own 1 KB
+// pieces: by rows of A where A is contraction-contiguous (step 1: all of B and rows 0-63 of either
+// half; step 2: the other rows), by the contraction where both operands are contraction-major.
 //
 // The tiles of a workgroup form one stream of stages: the DMA goes on into the next tile while
 // this one's last stages and its stores run. Results leave the registers as 16-byte stores: the
 // MFMAs run with the operands swapped, so a lane holds runs of four columns of one row, and one
 // swap of lane halves makes them eight.
+//
+// Bound by the board's power and LDS. 4 x 2048 rows against 2048 x 7168, bf16, held for a second:
+// 177 us (1357 TFLOP/s) at 1.59 GHz and 1330 W, 2500 cycles a stage of 2048 MFMA cycles; on zeros
+// 129 us (1867 TFLOP/s) at 2.35 GHz. Without the DMA's waits 5 % less, without the LDS reads 30 %
+// less. What was slower on the same products (27 to 32 experts, 32768 rows): sixteen waves of 64 x
+// 64 at four a SIMD, a stage behind (840 against 745 us); eight or four waves that read the next
+// group under the current one's MFMAs with one barrier a stage (830, 920); the DMA issued before
+// the phase's reads (775).
 #pragma once
 
 #include "expert_gemm.hpp"
@@ -52,82 +61,20 @@ __device__ inline f32x16 mma32(const FragOf<T>& a, const FragOf<T>& b, const f32
   else return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
 
-// Fragment reads. Reads and their wait stand in one asm block: for reads it can see, the compiler
-// would wait for the whole DMA queue first, because the DMA writes the same array.
-//
-// Two blocks of 32 rows, four k-groups, from a contraction-contiguous stage: f[block][group]; at:
-// the lane's address of block 0 in each group (OFF: bytes from there to the first block
-// read).
-template <typename T, int OFF>
-__device__ inline void read_rows(const unsigned (&at)[4], FragOf<T> (&f)[2][4]) {
-  __asm__ __volatile__(
-      "ds_read_b128 %0, %8 offset:%12\n\t"
-      "ds_read_b128 %1, %8 offset:%13\n\t"
-      "ds_read_b128 %2, %9 offset:%12\n\t"
-      "ds_read_b128 %3, %9 offset:%13\n\t"
-      "ds_read_b128 %4, %10 offset:%12\n\t"
-      "ds_read_b128 %5, %10 offset:%13\n\t"
-      "ds_read_b128 %6, %11 offset:%12\n\t"
-      "ds_read_b128 %7, %11 offset:%13\n\t"
-      "s_waitcnt lgkmcnt(0)"
-      : "=&v"(f[0][0]), "=&v"(f[1][0]), "=&v"(f[0][1]), "=&v"(f[1][1]), "=&v"(f[0][2]), "=&v"(f[1][2]), "=&v"(f[0][3]), "=&v"(f[1][3])
-      : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "i"(OFF), "i"(OFF + 32 * 128)
-      : "memory");
+// dma16 from inline assembly: the compiler does not see that it writes LDS and does not wait for
+// the queue before reads of other pieces. The kernel's own waits and barriers order it.
+__device__ inline void dma16_unseen(u32x4 rs, uint32_t lds_at, uint32_t voff) {
+  __asm__ __volatile__("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds_at), "v"(voff), "s"(rs) : "memory");
 }
 
-// The same of both operands, in one burst.
-template <typename T, int OFF>
-__device__ inline void read_rows2(const unsigned (&a)[4], FragOf<T> (&fa)[2][4], const unsigned (&b)[4], FragOf<T> (&fb)[2][4]) {
-  __asm__ __volatile__(
-      "ds_read_b128 %0, %16 offset:%24\n\t"
-      "ds_read_b128 %8, %20 offset:%24\n\t"
-      "ds_read_b128 %9, %20 offset:%25\n\t"
-      "ds_read_b128 %1, %16 offset:%25\n\t"
-      "ds_read_b128 %2, %17 offset:%24\n\t"
-      "ds_read_b128 %10, %21 offset:%24\n\t"
-      "ds_read_b128 %11, %21 offset:%25\n\t"
-      "ds_read_b128 %3, %17 offset:%25\n\t"
-      "ds_read_b128 %4, %18 offset:%24\n\t"
-      "ds_read_b128 %12, %22 offset:%24\n\t"
-      "ds_read_b128 %13, %22 offset:%25\n\t"
-      "ds_read_b128 %5, %18 offset:%25\n\t"
-      "ds_read_b128 %6, %19 offset:%24\n\t"
-      "ds_read_b128 %14, %23 offset:%24\n\t"
-      "ds_read_b128 %15, %23 offset:%25\n\t"
-      "ds_read_b128 %7, %19 offset:%25\n\t"
-      "s_waitcnt lgkmcnt(0)"
-      : "=&v"(fa[0][0]), "=&v"(fa[1][0]), "=&v"(fa[0][1]), "=&v"(fa[1][1]), "=&v"(fa[0][2]), "=&v"(fa[1][2]), "=&v"(fa[0][3]), "=&v"(fa[1][3]),
-        "=&v"(fb[0][0]), "=&v"(fb[1][0]), "=&v"(fb[0][1]), "=&v"(fb[1][1]), "=&v"(fb[0][2]), "=&v"(fb[1][2]), "=&v"(fb[0][3]), "=&v"(fb[1][3])
-      : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "v"(b[0]), "v"(b[1]), "v"(b[2]), "v"(b[3]), "i"(OFF), "i"(OFF + 32 * 128)
-      : "memory");
-}
-
-// Two blocks of 32 columns, two k-groups from byte OFF on, from a contraction-major stage (rows of
-// 512 bytes): two transposing reads a fragment (see load_b_kmajor). at: the lane's address of
-// either block in group 0.
-template <typename T, int OFF>
-__device__ inline void read_major(unsigned at0, unsigned at1, FragOf<T>& f00, FragOf<T>& f01, FragOf<T>& f10, FragOf<T>& f11) {
-  s16x4 v[8];
-  __asm__ __volatile__(
-      "ds_read_b64_tr_b16 %0, %8 offset:%10\n\t"
-      "ds_read_b64_tr_b16 %1, %8 offset:%11\n\t"
-      "ds_read_b64_tr_b16 %2, %8 offset:%12\n\t"
-      "ds_read_b64_tr_b16 %3, %8 offset:%13\n\t"
-      "ds_read_b64_tr_b16 %4, %9 offset:%10\n\t"
-      "ds_read_b64_tr_b16 %5, %9 offset:%11\n\t"
-      "ds_read_b64_tr_b16 %6, %9 offset:%12\n\t"
-      "ds_read_b64_tr_b16 %7, %9 offset:%13\n\t"
-      "s_waitcnt lgkmcnt(0)"
-      : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(v[4]), "=&v"(v[5]), "=&v"(v[6]), "=&v"(v[7])
-      : "v"(at0), "v"(at1), "i"(OFF), "i"(OFF + 2048), "i"(OFF + 8192), "i"(OFF + 8192 + 2048)
-      : "memory");
-  auto join = [](s16x4 lo, s16x4 hi) {
-    return __builtin_bit_cast(FragOf<T>, (s16x8)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-  };
-  f00 = join(v[0], v[1]);
-  f01 = join(v[2], v[3]);
-  f10 = join(v[4], v[5]);
-  f11 = join(v[6], v[7]);
+// A fragment of 32 columns from a contraction-major stage (rows of 512 bytes): two transposing
+// reads (see kmajor_frag_off for their lanes); `at`: the lane's place for the group.
+template <typename T>
+__device__ inline FragOf<T> read_major(const char* at) {
+  typedef __attribute__((address_space(3))) s16x4* lds4;
+  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(char*)at);
+  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(char*)(at + 4 * 512));
+  return __builtin_bit_cast(FragOf<T>, (s16x8)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
 template <int MODE, typename T>
@@ -141,7 +88,6 @@ __global__ void __launch_bounds__(TilePP::NT, TilePP::OCC) expert_gemm_pp(const 
   __shared__ int2 rows[EXPERT_MAX + 1];
   __shared__ int wsum[NT / 64];
   typedef FragOf<T> F;
-  typedef __attribute__((address_space(3))) const char* lds_ptr;
   const int wave = wave_uniform(threadIdx.x >> 6), wm = wave >> 2, wn = wave & 3;
   const int lane = threadIdx.x & 63;
   expert_tiles<NT, TilePP::BM, true>(p, first, wsum, rows);
@@ -172,6 +118,7 @@ __global__ void __launch_bounds__(TilePP::NT, TilePP::OCC) expert_gemm_pp(const 
   int klen = 0, k0 = 0;              // its contraction length, the stage being issued
   int efrom = 0, islot = 1;
   bool live = true;
+  const uint32_t lds0 = (uint32_t)(size_t)(__attribute__((address_space(3))) char*)lds;
   auto offset = [&](int l0, bool km, int rb, int ext, int i) {
     if (km) {
       const int k = i * 2 + (l0 >> 5), c = ((l0 & 31) ^ kmajor_swizzle(k & 3)) * 8;
@@ -223,7 +170,9 @@ __global__ void __launch_bounds__(TilePP::NT, TilePP::OCC) expert_gemm_pp(const 
     uint32_t off = isa ? offa[j] : offb[j];
     // a chunk behind the end of its row would be the next row's
     if (!km) off = (i & 1 ? kin1 : kin0) < klen - k0 ? off : OOB;
-    dma16(make_rsrc(isa ? srca : srcb, isa ? lena : lenb), lds + (isa ? 0 : 2 * OPB) + islot * OPB + i * 1024, off);
+    const uint64_t v = reinterpret_cast<uint64_t>(isa ? srca : srcb);
+    const u32x4 rs = {(uint32_t)v, (uint32_t)(v >> 32) & 0xffffu, isa ? lena : lenb, 0x00020000u};
+    dma16_unseen(rs, lds0 + (isa ? 0 : 2 * OPB) + islot * OPB + i * 1024, off);
   };
   // the pieces of step `st` of the stage
   auto issue = [&](auto st_c) {
@@ -241,7 +190,7 @@ __global__ void __launch_bounds__(TilePP::NT, TilePP::OCC) expert_gemm_pp(const 
 
   // ------------------------------------------------------------------------------ the tiles
   f32x16 acc[4][2];
-  F fa[2][4], fb[2][4];              // AKM: fa[i / 2 .. ] holds block i, group g at [i >> 1][(i & 1) * 2 + g]
+  F fa[2][4], fb[2][4];              // [block][group]; AKM: block i, group g of A at [i >> 1][(i & 1) * 2 + g]
   auto clear = [&]() {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -250,30 +199,40 @@ __global__ void __launch_bounds__(TilePP::NT, TilePP::OCC) expert_gemm_pp(const 
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
   };
-  // the lane's addresses in the stage's slot: of the groups (contiguous) or blocks (major)
-  unsigned ata[4], atb[4];
+  // the lane's places in the stage's slot: of the groups (contiguous) or blocks (major)
+  int ata[4], atb[4];
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
-    const unsigned base = (unsigned)(size_t)(lds_ptr)lds;
-    const unsigned ck = ((2 * g + (lane >> 5)) ^ chunk_swizzle<8>(lane & 31)) << 4;
-    ata[g] = base + (AKM ? kmajor_frag_off<512>(lane, wm * 128 + g * 32) : (wm * 128 + (lane & 31)) * 128 + ck);
-    atb[g] = base + 2 * OPB + (BKM ? kmajor_frag_off<512>(lane, wn * 64 + (g & 1) * 32) : (wn * 64 + (lane & 31)) * 128 + ck);
+    const int ck = ((2 * g + (lane >> 5)) ^ chunk_swizzle<8>(lane & 31)) << 4;
+    ata[g] = AKM ? kmajor_frag_off<512>(lane, wm * 128 + g * 32) : (wm * 128 + (lane & 31)) * 128 + ck;
+    atb[g] = 2 * OPB + (BKM ? kmajor_frag_off<512>(lane, wn * 64 + (g & 1) * 32) : (wn * 64 + (lane & 31)) * 128 + ck);
   }
+  auto rowfrag = [&](int at) { return *reinterpret_cast<const F*>(lds + at); };
   auto read = [&](auto st_c) {
     constexpr int st = decltype(st_c)::value;
     if constexpr (AKM) {
-      read_major<T, st * 16384>(ata[0], ata[1], fa[0][0], fa[0][1], fa[0][2], fa[0][3]);
-      read_major<T, st * 16384>(ata[2], ata[3], fa[1][0], fa[1][1], fa[1][2], fa[1][3]);
-      read_major<T, st * 16384>(atb[0], atb[1], fb[0][0], fb[0][1], fb[1][0], fb[1][1]);
-    } else if constexpr (st == 1) {
-      read_rows<T, 64 * 128>(ata, fa);
-    } else if constexpr (BKM) {
-      read_major<T, 0>(atb[0], atb[1], fb[0][0], fb[0][1], fb[1][0], fb[1][1]);
-      read_major<T, 16384>(atb[0], atb[1], fb[0][2], fb[0][3], fb[1][2], fb[1][3]);
-      read_rows<T, 0>(ata, fa);
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) fb[j][g] = read_major<T>(lds + atb[j] + st * 16384 + g * 8192);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) fa[i >> 1][(i & 1) * 2 + g] = read_major<T>(lds + ata[i] + st * 16384 + g * 8192);
+      }
     } else {
-      read_rows2<T, 0>(ata, fa, atb, fb);
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        if constexpr (st == 0) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            if constexpr (BKM) fb[j][g] = read_major<T>(lds + atb[j] + g * 8192);
+            else fb[j][g] = rowfrag(atb[g] + j * 4096);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) fa[i][g] = rowfrag(ata[g] + st * 8192 + i * 4096);
+      }
     }
+    __builtin_amdgcn_sched_barrier(0);
   };
   auto compute = [&](auto st_c) {
     constexpr int st = decltype(st_c)::value;
@@ -357,15 +316,17 @@ __global__ void __launch_bounds__(TilePP::NT, TilePP::OCC) expert_gemm_pp(const 
       // In the queue at the end of either reading phase: eight pieces, and before the oldest of
       // them, in a tile's first stage, the stores of the tile before it.
       const bool stored = kt == 0 && !begin;
-      issue(S1{});                   // step 2 of the next stage
       if (busy0) read(S0{});
+      issue(S1{});                   // step 2 of the next stage
+      wait_lgkmcnt0();
       landed(stored);   // step 2 of this stage has landed
       phase_end();
       if (busy0) compute(S0{});
       phase_end();
+      if (busy1) read(S1{});
       advance();
       issue(S0{});                   // step 1 of the stage after next
-      if (busy1) read(S1{});
+      wait_lgkmcnt0();
       landed(stored);   // step 1 of the next stage has landed
       phase_end();
       if (busy1) compute(S1{});
