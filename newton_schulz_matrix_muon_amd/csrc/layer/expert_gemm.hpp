@@ -124,7 +124,7 @@ __device__ inline ExpertList expert_list(const ExpertArgs& p, const int* first) 
 
 // Tile t of an XCD's list. Tiles go expert by expert, within one in bands of EXPERT_BAND tile
 // rows, down a band, then one tile column right, so that the tiles that run together share panels
-// of both operands in L2. *from: an expert that is not behind the tile's; the tile's on return.
+// of both operands in L2. *from: the expert of the tile before, or 0.
 // rows (ROWS): as expert_tiles left them.
 constexpr int EXPERT_BAND = 8;
 template <int MODE, typename T, class CFG, bool ROWS = false>
@@ -139,9 +139,14 @@ __device__ inline ExpertTile expert_tile(const ExpertArgs& p, const int* first, 
     e = t / (tm * p.tiles_n);
     r = t - e * tm * p.tiles_n;
   } else {
-    // the expert whose tiles hold t: a few further than the last tile's
+    // the expert whose tiles hold t: the last tile's, or as many as end at or before t
     e = *from;
-    while (wave_uniform(first[e + 1]) * p.tiles_n <= t) ++e;
+    if (wave_uniform(first[e + 1]) * p.tiles_n <= t) {
+      const int lane = threadIdx.x & 63;
+      e = 0;
+      for (int i = lane; i - lane <= p.experts; i += 64)
+        e += __builtin_popcountll(__ballot(i <= p.experts && first[i + 1] * p.tiles_n <= t));
+    }
     *from = e;
     const int f = wave_uniform(first[e]);
     tm = wave_uniform(first[e + 1]) - f;

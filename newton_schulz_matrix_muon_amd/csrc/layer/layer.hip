@@ -270,18 +270,23 @@ int run_few(const ExpertArgs& a, int dt, hipStream_t s) {
   });
 }
 
-// The kernel of a product. The 256 x 256 tiles need 16-bit types and whole 16-byte chunks
-// everywhere, and enough rows to fill them; the forward product of few rows has its own
-// (expert_few.hpp says from where to where).
+// The kernel of a product. The 256 x 256 tiles need 16-bit types, whole 16-byte chunks everywhere,
+// extents that do not leave half of a tile empty, and enough tiles for half of the CUs. One
+// MI355X, bf16, 256 x 256 against 128 x 128 tiles: 27 experts of 2048 x 7168, 8 rows each, forward
+// 143 against 176 us, weight gradient 189 against 249; 256 rows 314 against 446, 441 against 652;
+// 128 experts of 512 x 512 (264 tiles), 32 rows 19 against 18 us, 64 rows 21 against 27, 512 rows
+// 54 against 73; 8 experts of 1000 x 776 (64 tiles), 320 rows 23 against 19 us, weight gradient (128
+// tiles) 20 against 20. The forward product of few rows has its own kernel (expert_few.hpp says from
+// where to where).
 template <int MODE>
 int run_product(const ExpertArgs& a, int dt, bool vec, hipStream_t s) {
   // the largest list of the smallest tiles
   const int64_t tn = (a.n + 127) / 128, tm = MODE == EX_DW ? a.experts * ((a.m + 127) / 128) : a.rows / 128 + a.experts + 1;
   if (tn * tm > INT32_MAX) return MNS_ERR_SHAPE;
-  const bool whole = vec && a.c_vec && a.n % 8 == 0 && dt != F32;
-  const int64_t rows = a.rows / a.experts;
   if (MODE == EX_FWD && vec && dt != F32 && a.rows <= 4 * a.experts) return run_few(a, dt, s);
-  if (whole && (MODE == EX_DW ? a.m >= 256 && a.n >= 256 : rows >= 128)) return run_pingpong<MODE>(a, dt, s);
+  const bool whole = vec && a.c_vec && a.n % 8 == 0 && dt != F32 && a.n > 128 && (MODE != EX_DW || a.m > 128);
+  const int64_t high = MODE == EX_DW ? a.experts * ((a.m + 255) / 256) : a.rows / 256 + std::min<int64_t>(a.experts, a.rows);
+  if (whole && 2 * high * ((a.n + 255) / 256) >= device_cus()) return run_pingpong<MODE>(a, dt, s);
   return run_staged<MODE, Tile128>(a, dt, vec, s);
 }
 
