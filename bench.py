@@ -103,6 +103,71 @@ def bench_adamw(args):
     print(json.dumps(out), flush=True)
 
 
+def bench_moe_layer(args):
+    """One training step of a mixture-of-experts layer whose matrices Muon updates: layer norm,
+    tokens sorted by expert, up and down products with a squared ReLU between them, weighted sum
+    back, the whole backward pass, then the hybrid optimizer step on its gradients. 4096 tokens of
+    2048, top 6 of 64 experts of 1408 x 2048 (up) and 2048 x 1408 (down), bf16."""
+    import torch
+    from newton_schulz_matrix_muon_amd import ops
+    dev = torch.device("cuda:0")
+    T, K, E, D, H = 4096, 6, 64, 2048, 1408
+    gen = torch.Generator(device=dev).manual_seed(77)
+    rnd = lambda *shape: torch.randn(*shape, generator=gen, device=dev)
+    up, down = (rnd(E, H, D) * D ** -0.5).bfloat16(), (rnd(E, D, H) * H ** -0.5).bfloat16()
+    nw, nb = torch.ones(D, device=dev), torch.zeros(D, device=dev)
+    x, dy = rnd(T, D).bfloat16(), (1e-3 * rnd(T, D)).bfloat16()
+    picks = torch.topk(rnd(T, E), K, dim=1)
+    ids, weights = picks.indices, torch.softmax(picks.values, dim=1)
+    mom = [torch.zeros(E, H, D, device=dev), torch.zeros(E, D, H, device=dev)]
+    adam = [(p, torch.zeros(D, device=dev), torch.zeros(D, device=dev)) for p in (nw, nb)]
+    variant = ops.GRAM if args.variant == "gram" else ops.STANDARD
+
+    def step():
+        h, mean, rstd = ops.layer_norm(x, nw, nb)
+        offsets, rank = ops.expert_sort(ids, E)
+        xs = ops.expert_dispatch(h, rank, offsets)
+        pre = ops.expert_matmul(xs, up, offsets)
+        pos = pre.clamp(min=0)
+        act = pos.square()
+        ys = ops.expert_matmul(act, down, offsets)
+        ops.expert_combine(ys, weights, rank)
+        dys, _ = ops.expert_combine_backward(dy, ys, weights, rank, offsets)
+        dact, ddown = ops.expert_matmul_backward(dys, act, down, offsets)
+        dxs, dup = ops.expert_matmul_backward(dact.mul_(pos).mul_(2), xs, up, offsets)
+        dh = ops.expert_dispatch_backward(dxs, rank)
+        _, dnw, dnb = ops.layer_norm_backward(dh, x, mean, rstd, nw)
+        ops.hybrid_step([(up, dup, mom[0]), (down, ddown, mom[1])],
+                        [(p, g, m, v) for (p, m, v), g in zip(adam, (dnw, dnb))],
+                        muon=dict(lr=2e-4, momentum=0.95, weight_decay=0.1, nesterov=True, variant=variant), adamw=ADAMW_KW)
+
+    for _ in range(max(1, args.warmup)):
+        step()
+    torch.cuda.synchronize()
+    ops.timing_reset()
+    ops.timing_enable(True)
+    t0 = time.perf_counter()
+    for _ in range(args.steps):
+        step()
+    torch.cuda.synchronize()
+    sec = (time.perf_counter() - t0) / args.steps
+    ops.timing_enable(False)
+    kinds = {k: {"ms_per_step": ms / args.steps, "launches_per_step": n / args.steps}
+             for k, (ms, n) in ops.timing_query().items() if n}
+    flop = 12 * T * K * D * H          # six products of 2 T K D H
+    gemm_s = kinds["expert_gemm"]["ms_per_step"] / 1e3
+    print(json.dumps({
+        "metric": "mixture-of-experts layer training tokens/sec (forward, backward, Muon + AdamW step)",
+        "value": T / sec, "unit": "tokens/s", "n_gpus": 1, "steps": args.steps, "warmup": args.warmup,
+        "ms_per_step": sec * 1e3, "higher_is_better": True, "scaling": "weak", "vs_baseline": None, "dtype": "bf16",
+        "data": "synthetic",
+        "config": {"workload": "moe_layer_4096x2048_top6_of_64x1408x2048_bf16", "tokens": T, "k": K, "experts": E,
+                   "hidden": D, "inner": H, "variant": args.variant},
+        "roofline": {"bound": "mfma", "achieved": flop / gemm_s / 1e12, "peak": PEAK_MFMA_TFLOPS, "unit": "TFLOP/s",
+                     "frac": flop / gemm_s / 1e12 / PEAK_MFMA_TFLOPS, "traffic": None, "kernel": "expert_gemm"},
+        "kinds": kinds, "cpu_baseline": None}), flush=True)
+
+
 class ClockSampler:
     """Samples the GPU's reported graphics clock (sysfs pp_dpm_sclk, the line marked '*') and
     board power (hwmon power1_average or power1_input, with the power1_cap limit) every
@@ -291,14 +356,15 @@ def main():
     ap.add_argument("--warmup", type=int, default=3)
     ap.add_argument("--variant", choices=["gram", "standard"], default="gram")
     ap.add_argument("--workload", choices=["experts", "experts_1408", "dense_ffn", "k2_full", "k2_hybrid",
-                                           "adamw"], default="experts",
+                                           "adamw", "moe_layer"], default="experts",
                     help="experts: the Kimi-K2 expert batch, --batch x --rows x --cols (default 648 x "
                          "2048 x 7168) Gaussian plus a rank-32 spike; experts_1408: 64 x 1408 x 2048 "
                          "low-rank (s_i = i^-0.7) plus 0.05 noise, lr 2e-4, wd 0.1; dense_ffn: 3 x 7168 x "
                          "18432 low-rank (s_i = i^-0.5) plus 0.05 noise; k2_full: the whole Kimi-K2 Muon "
                          "step in one grouped call (432 x 2048 x 7168 up/gate, 216 x 7168 x 2048 down, "
                          "3 x 7168 x 18432 dense); k2_hybrid: k2_full plus AdamW on the 1-D / embedding "
-                         "parameters; adamw: the AdamW side alone")
+                         "parameters; adamw: the AdamW side alone; moe_layer: a training step of one "
+                         "mixture-of-experts layer, forward, backward and optimizer")
     ap.add_argument("--batch", type=int, default=648)
     ap.add_argument("--rows", type=int, default=2048)
     ap.add_argument("--cols", type=int, default=7168)
@@ -328,6 +394,8 @@ def main():
         copy_probe(args.copy_probe_mib)
     if args.workload == "adamw":
         return bench_adamw(args)
+    if args.workload == "moe_layer":
+        return bench_moe_layer(args)
     if args.vendor_gemm:
         return vendor_gemm(args)
     # inputs: (generator name, workload index of the seeds) per preset

@@ -100,9 +100,14 @@ constexpr int held(int nt, int vpt) { return nt * vpt * 8; }
 constexpr int kNormHeld = held(1024, 2);   // longer rows take the kernels that read them again
 
 // Workgroups that share the rows of a backward pass, each with a part of dweight and dbias: enough
-// to fill the chip (two of 512 threads a CU, or four of 256 where rows are short).
+// to fill the chip (two of 512 threads a CU, or four of 256 where rows are short), but at least
+// four turns of rows each once every CU has one, because each part costs as much traffic as two
+// fp32 rows (1021 x 2047 fp32 with a part a row: 12 us and 8 for the parts' sum; four rows a part:
+// 12 and 4).
 int norm_parts(int64_t rows, int64_t cols) {
-  return (int)std::max<int64_t>(1, cols <= held(64, 2) ? std::min<int64_t>((rows + 3) / 4, 1024) : std::min<int64_t>(rows, cols <= held(256, 1) ? 1024 : 512));
+  const int64_t turns = cols <= held(64, 2) ? (rows + 3) / 4 : rows;   // four rows at a time where a wave holds one
+  const int64_t most = cols <= held(256, 1) ? 1024 : 512;
+  return (int)std::max<int64_t>(1, turns <= 256 ? turns : std::min(most, std::max<int64_t>(256, turns / 4)));
 }
 
 template <typename T, typename WT, bool VEC>

@@ -141,9 +141,15 @@ def _check(code: int, what: str):
         raise MnsError(code, what)
 
 
+_TORCH = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
 
 
 _DTYPE_CODES = {}
@@ -210,10 +216,9 @@ def _check_device(what, ref, **named):
     """Every named tensor (None skipped) is a device tensor on ref's device."""
     if not ref.is_cuda:
         raise ValueError(f"{what}: tensors must be device tensors (got {ref.device})")
+    device = ref.device
     for name, t in named.items():
-        if t is None:
-            continue
-        if not t.is_cuda or t.device != ref.device:
+        if t is not None and t.device != device:
             raise ValueError(f"{what}: {name} is on {t.device}, expected {ref.device}")
 
 
@@ -544,7 +549,7 @@ def _check_rows(what, ref, **named):
 
 
 def _check_shape(what, name, t, shape):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:   # a torch.Size compares with a tuple
         raise ValueError(f"{what}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
@@ -576,19 +581,27 @@ def _check_offsets(what, offsets):
 
 
 def _ptr(t):
-    return None if t is None or t.numel() == 0 else t.data_ptr()
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(index):
+    """The current stream's handle (torch.cuda.current_stream builds an object for it, 1.5 us)."""
+    torch = _torch()
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(index) if get else torch.cuda.current_stream(index).cuda_stream
 
 
 def _launch(what, ref, *args):
     """Call the C function `what` on ref's device and its current stream there."""
-    torch = _torch()
+    index = ref.device.index
     fn = getattr(_lib(), what)
-    if ref.device.index == torch.cuda.current_device():
-        code = fn(*args, torch.cuda.current_stream().cuda_stream)
+    if index == _torch().cuda.current_device():
+        code = fn(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(ref.device):
-            code = fn(*args, torch.cuda.current_stream().cuda_stream)
-    _check(code, what)
+        with _torch().cuda.device(index):
+            code = fn(*args, _raw_stream(index))
+    if code:
+        raise MnsError(code, what)
 
 
 def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, out=None):
@@ -599,12 +612,15 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, out=None):
     what = "layer_norm"
     _check_recorded(what, x, weight, bias)
     xd = describe(x)
-    params = [t for t in (weight, bias) if t is not None]
     _check_flat(what, x, (x.dtype, torch.float32), weight=weight, bias=bias)
+    lead, cols = x.shape[:-1], x.shape[-1:]
+    wcode = F32
     for name, t in (("weight", weight), ("bias", bias)):
         if t is not None:
-            _check_shape(what, name, t, x.shape[-1:])
-    if len(params) == 2 and weight.dtype != bias.dtype:
+            if t.shape != cols:
+                _check_shape(what, name, t, cols)
+            wcode = dtype_code(t)
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
         raise TypeError(f"{what}: weight is {weight.dtype}, bias is {bias.dtype}")
     if out is not None:
         _check_same_shape(what, x, out=out)
@@ -612,10 +628,9 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, out=None):
             raise TypeError(f"{what}: out must have x's dtype {x.dtype}, got {out.dtype}")
     _check_device(what, x, weight=weight, bias=bias, out=out)
     y = x.new_empty(x.shape) if out is None else out
-    lead = x.shape[:-1]
     mean = torch.empty(lead, dtype=torch.float32, device=x.device)
     rstd = torch.empty(lead, dtype=torch.float32, device=x.device)
-    _launch(what, x, xd, _ptr(weight), _ptr(bias), dtype_code(params[0]) if params else F32, eps, describe(y),
+    _launch(what, x, xd, _ptr(weight), _ptr(bias), wcode, eps, describe(y),
             _ptr(mean), _ptr(rstd))
     return y, mean, rstd
 
@@ -819,9 +834,17 @@ def expert_matmul_grad_weight(dy, x, offsets, *, out=None):
 
 
 def expert_matmul_backward(dy, x, w, offsets):
-    """(dx, dw) of expert_matmul."""
-    _check_product("expert_matmul_backward", w, offsets, dy=dy, x=x)
-    return expert_matmul_grad_input(dy, w, offsets), expert_matmul_grad_weight(dy, x, offsets)
+    """(dx, dw) of expert_matmul: expert_matmul_grad_input and expert_matmul_grad_weight."""
+    what = "expert_matmul_backward"
+    _check_product(what, w, offsets, dy=dy, x=x)
+    _check_shape(what, "x", x, (x.shape[0], w.shape[2]))
+    _check_shape(what, "dy", dy, (x.shape[0], w.shape[1]))
+    _check_device(what, dy, x=x, w=w, offsets=offsets)
+    dyd, xd, at = describe(dy), describe(x), offsets.data_ptr()
+    dx, dw = x.new_empty(x.shape), w.new_empty(w.shape)
+    _launch("expert_matmul_grad_input", dy, dyd, describe(w), at, describe(dx))
+    _launch("expert_matmul_grad_weight", dy, dyd, xd, at, describe(dw))
+    return dx, dw
 
 
 def gram_trace(G, *, steps: int = DEFAULT_STEPS, coeffs=None, eps: float = DEFAULT_EPS,

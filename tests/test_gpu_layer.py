@@ -336,6 +336,64 @@ def test_expert_products(torch, ops, case, dtype):
     check_product(torch, ops, x, dy, w, counts, offsets)
 
 
+def uneven(experts, most, seed, empty=5):
+    """Row counts 0 .. most, every empty-th expert without rows."""
+    import torch
+    c = torch.randint(0, most + 1, (experts,), generator=torch.Generator().manual_seed(seed))
+    c[::empty] = 0
+    return c.tolist()
+
+
+# many experts: half a chip of 256 x 256 tiles and more, several a workgroup; contractions of one
+# chunk, one stage, a stage and a bit, an odd and an even number of stages
+MANY = [
+    (uneven(70, 600, 1), 3, 264, 8), (uneven(70, 300, 2), 0, 520, 64), (uneven(90, 300, 3), 300, 392, 72), (uneven(40, 500, 4), 5, 1032, 200),
+    (uneven(33, 200, 5), 0, 2048, 256), (uneven(200, 40, 6), 1, 136, 1096), (uneven(1024, 3, 7), 2, 264, 136), ([0] * 20 + [9000] + [0] * 19, 9, 256, 328),
+    ([256] * 130, 0, 256, 320), ([0] * 150, 700, 144, 160), (uneven(150, 130, 8, 2), 0, 144, 160),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+@pytest.mark.parametrize("case", MANY, ids=lambda c: f"{len(c[0])}x{sum(c[0])}+{c[1]}_{c[2]}x{c[3]}")
+def test_expert_products_of_many_experts(torch, ops, case, dtype):
+    counts, rest, n, k = case
+    gen = gen_for(torch, n + k)
+    x, dy, w, offsets = make_product(torch, gen, getattr(torch, dtype), counts, rest, n, k, pad=8)
+    x[sum(counts):] = float("nan")
+    dy[sum(counts):] = float("nan")
+    check_product(torch, ops, x, dy, w, counts, offsets)
+
+
+def test_expert_products_write_nothing_outside(torch, ops):
+    """Strided results: the columns behind each row and the rows around stay as they were."""
+    gen = gen_for(torch, 12)
+    for counts, n, k in (([40, 0, 70], 72, 136), (uneven(60, 300, 9), 264, 328)):
+        rows = sum(counts)
+        x, dy, w, offsets = make_product(torch, gen, torch.bfloat16, counts, 0, n, k)
+        for call, r, c in ((lambda o: ops.expert_matmul(x, w, offsets, out=o), rows, n),
+                           (lambda o: ops.expert_matmul_grad_input(dy, w, offsets, out=o), rows, k)):
+            full = torch.full((r + 4, c + 16), 7.0, dtype=torch.bfloat16, device="cuda")
+            got = call(full[2:-2, 8:-8]).clone()
+            full[2:-2, 8:-8] = 7.0
+            assert (full == 7.0).all() and torch.equal(got, call(None))
+        full = torch.full((len(counts), n + 4, k + 16), 7.0, dtype=torch.bfloat16, device="cuda")
+        got = ops.expert_matmul_grad_weight(dy, x, offsets, out=full[:, 2:-2, 8:-8]).clone()
+        full[:, 2:-2, 8:-8] = 7.0
+        assert (full == 7.0).all() and torch.equal(got, ops.expert_matmul_grad_weight(dy, x, offsets))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_no_rows_at_all(torch, ops, dtype):
+    dt = getattr(torch, dtype)
+    for experts in (3, 200):
+        w = torch.randn(experts, 136, 264, device="cuda").to(dt)
+        off = torch.zeros(experts + 1, dtype=torch.int32, device="cuda")
+        x, dy = torch.empty(0, 264, dtype=dt, device="cuda"), torch.empty(0, 136, dtype=dt, device="cuda")
+        assert ops.expert_matmul(x, w, off).shape == (0, 136)
+        dx, dw = ops.expert_matmul_backward(dy, x, w, off)
+        assert dx.shape == (0, 264) and dw.shape == w.shape and not dw.any()
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("pad,shift", [(8, 0), (3, 0), (8, 1), (0, 8), (1, 3)])
 def test_expert_products_strided_and_unaligned(torch, ops, dtype, pad, shift):
