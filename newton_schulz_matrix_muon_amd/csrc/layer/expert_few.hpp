@@ -48,6 +48,7 @@ __device__ inline f32x4 mma16(const typename Frag<T>::type& a, const typename Fr
 template <typename T>
 __global__ void __launch_bounds__(256) expert_few_fwd(const ExpertArgs p) {
   typedef typename Frag<T>::type F;
+  constexpr int U = 8;               // pieces of a wave in flight
   __shared__ f32x4 part[3][64];
   const int lane = threadIdx.x & 63, wave = wave_uniform(threadIdx.x >> 6);
   const int n0 = blockIdx.x * 16, l16 = lane & 15, q = lane >> 4;
@@ -61,10 +62,10 @@ __global__ void __launch_bounds__(256) expert_few_fwd(const ExpertArgs p) {
     if (e < p.experts) {
       const T* X = reinterpret_cast<const T*>(p.A) + (int64_t)min(r, hi - 1) * p.lda;
       const F zero = {};
-      for (int k0 = wave * 64; k0 < p.k; k0 += 4 * 4 * 64) {
-        F a[4][2], b[4][2];
+      for (int k0 = wave * 64; k0 < p.k; k0 += 4 * U * 64) {
+        F a[U][2], b[U][2];
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
           for (int v = 0; v < 2; ++v) {
             const int k = k0 + u * 256 + q * 16 + v * 8;
@@ -73,7 +74,7 @@ __global__ void __launch_bounds__(256) expert_few_fwd(const ExpertArgs p) {
             b[u][v] = in && r < hi ? *reinterpret_cast<const F*>(X + k) : zero;
           }
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
           for (int v = 0; v < 2; ++v) acc = mma16<T>(a[u][v], b[u][v], acc);
       }
