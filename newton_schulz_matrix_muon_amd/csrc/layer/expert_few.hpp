@@ -2,11 +2,10 @@
 // time is that of reading the weights of the experts that have rows, once, so the work is cut
 // along the weights, 16 of their rows a workgroup, until every CU reads.
 //
-// One MI355X, bf16, weights from HBM: 64 experts of 1408 x 2048, 6 rows 14.6 us (128 x 128 tiles:
-// 33.4), 64 rows 51 us at 4.8 TB/s (60), 256 rows 77 us (103), 1024 rows 126 us (104); 27 experts
-// of 2048 x 7168, 27 rows 93 us at 5.7 TB/s (146), 108 rows 145 us (156), 216 rows 174 us (158).
-// So it serves up to four rows an expert. The input gradient stays on the tiles: they read W by
-// whole rows, 5.2 TB/s from one row an expert on.
+// One MI355X, bf16, weights from HBM (128 x 128 tiles in brackets): 64 experts of 1408 x 2048, 6 rows
+// 9.7 us, 64 rows 50 us at 5.0 TB/s (56), 256 rows 73 us (94); 27 experts of 2048 x 7168, 27 rows
+// 92 us at 5.7 TB/s (134), 108 rows 144 us (142). The input gradient stays on the tiles: they read
+// W by whole rows, 5.2 TB/s from one row an expert on.
 #pragma once
 
 #include "expert_gemm.hpp"
@@ -35,20 +34,33 @@ __device__ inline int nth_expert(const ExpertArgs& p, int slot, int* lo, int* hi
   return -1;
 }
 
+// acc += the products of one 16-byte chunk of each operand's row: chunks of lanes q = 0..3 of a row
+// are four parts of the contraction.
 template <typename T>
-__device__ inline f32x4 mma16(const typename Frag<T>::type& a, const typename Frag<T>::type& b, f32x4 c) {
-  if constexpr (__is_same(T, __bf16)) return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-  else return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+__device__ inline f32x4 mma16(const u32x4& a, const u32x4& b, f32x4 c) {
+  typedef typename Frag<T>::type F;
+  const F x = __builtin_bit_cast(F, a), y = __builtin_bit_cast(F, b);
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(x[e], y[e], c, 0, 0, 0);
+    return c;
+  } else if constexpr (__is_same(T, __bf16)) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, y, c, 0, 0, 0);
+  } else {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(x, y, c, 0, 0, 0);
+  }
 }
 
 // Forward: a workgroup takes 16 rows of one expert's W against 16 rows of X at a time; its four
-// waves take every fourth 64-wide piece of K, whose 128 bytes four lanes of a row read whole (the
-// order of the contraction within a piece does not matter as long as both operands agree), and
-// their sums meet in LDS. One wave's pieces are loaded four at a time.
-template <typename T>
-__global__ void __launch_bounds__(256) expert_few_fwd(const ExpertArgs p) {
-  typedef typename Frag<T>::type F;
+// waves take every fourth piece of K, whose 128 bytes four lanes of a row read whole (the order of
+// the contraction within a piece does not matter as long as both operands agree), and their sums
+// meet in LDS. One wave's pieces are loaded eight at a time.
+// (Two workgroups a CU at least, so that the sums stay out of the accumulation registers: there the
+// compiler read one behind a branch without the wait that the last product needs.)
+template <typename T, int FIT>
+__global__ void __launch_bounds__(256, 2) expert_few_fwd(const ExpertArgs p) {
   constexpr int U = 8;               // pieces of a wave in flight
+  constexpr int N = 16 / sizeof(T), PIECE = 8 * N;
   __shared__ f32x4 part[3][64];
   const int lane = threadIdx.x & 63, wave = wave_uniform(threadIdx.x >> 6);
   const int n0 = blockIdx.x * 16, l16 = lane & 15, q = lane >> 4;
@@ -61,23 +73,34 @@ __global__ void __launch_bounds__(256) expert_few_fwd(const ExpertArgs p) {
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
     if (e < p.experts) {
       const T* X = reinterpret_cast<const T*>(p.A) + (int64_t)min(r, hi - 1) * p.lda;
-      const F zero = {};
-      for (int k0 = wave * 64; k0 < p.k; k0 += 4 * U * 64) {
-        F a[U][2], b[U][2];
+      auto pieces = [&](int k0, auto cut_c) {
+        constexpr bool cut = decltype(cut_c)::value, shift = cut && FIT == CHUNK_ANY;
+        const u32x4 zero = {0, 0, 0, 0};
+        u32x4 a[U][2], b[U][2];
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
           for (int v = 0; v < 2; ++v) {
-            const int k = k0 + u * 256 + q * 16 + v * 8;
-            const bool in = k < p.k;
-            a[u][v] = in ? *reinterpret_cast<const F*>(W + k) : zero;
-            b[u][v] = in && r < hi ? *reinterpret_cast<const F*>(X + k) : zero;
+            const int k = k0 + u * 4 * PIECE + (q * 2 + v) * N, at = shift ? min(k, p.k - N) : k;
+            const bool in = !cut || k < p.k;
+            a[u][v] = in ? load_chunk<T, FIT>(W, at, p.k) : zero;
+            b[u][v] = in && r < hi ? load_chunk<T, FIT>(X, at, p.k) : zero;
           }
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-          for (int v = 0; v < 2; ++v) acc = mma16<T>(a[u][v], b[u][v], acc);
-      }
+          for (int v = 0; v < 2; ++v) {
+            if constexpr (shift) {
+              const int k = k0 + u * 4 * PIECE + (q * 2 + v) * N, by = k - min(k, p.k - N);
+              a[u][v] = drop_first<T>(a[u][v], by);
+              b[u][v] = drop_first<T>(b[u][v], by);
+            }
+            acc = mma16<T>(a[u][v], b[u][v], acc);
+          }
+      };
+      int k0 = wave * PIECE;
+      for (; k0 + (4 * U - 3) * PIECE <= p.k; k0 += 4 * U * PIECE) pieces(k0, std::false_type{});
+      if (k0 < p.k) pieces(k0, std::true_type{});
     }
     if (wave) part[wave - 1][lane] = acc;
     __syncthreads();

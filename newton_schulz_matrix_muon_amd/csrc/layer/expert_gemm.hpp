@@ -20,6 +20,8 @@
 // outside 0 .. S are cut to it, and an expert whose end lies before its beginning has no rows.
 #pragma once
 
+#include <type_traits>
+
 #include "norm.hpp"
 
 namespace mns {
@@ -94,12 +96,23 @@ struct ExpertTile {
   char* c;
 };
 
-// 16 bytes of an operand row: elements e0 .. of a row `len` long, zero past the end.
-template <typename T, bool VEC>
+// 16 bytes at any element's address
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+
+// How the 16-byte chunks of an operand's rows are loaded: rows of whole aligned chunks; rows of any
+// length from a chunk on, at any address, which the hardware's loads take as it is; rows shorter
+// than a chunk, element by element.
+enum { CHUNK_TINY, CHUNK_ANY, CHUNK_ALIGNED };
+
+// Elements e0 .. of a row `len` long. The row has the whole chunk, but for CHUNK_TINY, which gives
+// zeros past the end.
+template <typename T, int FIT>
 __device__ inline u32x4 load_chunk(const T* row, int e0, int len) {
   constexpr int N = 16 / (int)sizeof(T);
-  if constexpr (VEC) {
-    return e0 < len ? *reinterpret_cast<const u32x4*>(row + e0) : u32x4{0, 0, 0, 0};
+  if constexpr (FIT == CHUNK_ALIGNED) {
+    return *reinterpret_cast<const u32x4*>(row + e0);
+  } else if constexpr (FIT == CHUNK_ANY) {
+    return *reinterpret_cast<const u32x4_any*>(row + e0);
   } else {
     typedef T TN __attribute__((ext_vector_type(N)));
     TN v;
@@ -108,6 +121,15 @@ __device__ inline u32x4 load_chunk(const T* row, int e0, int len) {
     return __builtin_bit_cast(u32x4, v);
   }
 }
+
+// v without its first `by` elements, zeros behind.
+template <typename T>
+__device__ inline u32x4 drop_first(u32x4 v, int by) {
+  constexpr int N = 16 / (int)sizeof(T);
+  const unsigned __int128 w = __builtin_bit_cast(unsigned __int128, v);
+  return by < N ? __builtin_bit_cast(u32x4, w >> (by * (int)sizeof(T) * 8)) : u32x4{0, 0, 0, 0};
+}
+
 
 // The part of the launch's tile list that one XCD takes (an eighth, so that neighbouring tiles
 // share an L2), for the workgroups on it to walk side by side.
@@ -201,8 +223,14 @@ __device__ inline void expert_store(const ExpertArgs& p, const ExpertTile& x, ch
         const f32x4 b = *reinterpret_cast<const f32x4*>(Cs + lr * CP + lc + 4);
         const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
         T* out = reinterpret_cast<T*>(x.c) + (int64_t)r * p.ldc;
-        if (p.c_vec && c + 8 <= p.n) {
-          VecIO<T>::store(out, c, v);
+        if (c + 8 <= p.n) {
+          u32x4_any* o = reinterpret_cast<u32x4_any*>(out + c);
+          if constexpr (sizeof(T) == 4) {
+            o[0] = __builtin_bit_cast(u32x4, a);
+            o[1] = __builtin_bit_cast(u32x4, b);
+          } else {
+            o[0] = u32x4{pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7])};
+          }
         } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
@@ -214,9 +242,16 @@ __device__ inline void expert_store(const ExpertArgs& p, const ExpertTile& x, ch
   }
 }
 
-// Operands staged through registers: every type and any alignment (VEC: rows of whole 16-byte
-// chunks). 128 x 128 tiles of 4 waves.
-template <int MODE, typename T, bool VEC, class CFG>
+// Operands staged through registers: every type, any alignment and length (FIT). 128 x 128 tiles of
+// 4 waves, one stage of K ahead in registers (two ahead gained 1 % at 50 registers more), 64 KB of
+// LDS and two workgroups a CU, so that one computes while the other waits.
+//
+// One MI355X, bf16, 64 experts with 64 rows each: 1408 x 2048 forward 102 us, input gradient 96,
+// weight gradient 146; 1405 x 2045, whose rows begin anywhere, 124, 122, 195. Loads element by
+// element for such rows took 3.5 times as long (3056 x 1466, 135 rows each, forward 393 us, now
+// 134), loads under a condition per lane 1.3 to 2 times (the compiler waits for one before the
+// next). fp32 is bound by its MFMAs, so blocks of 32 rows that have none are left out.
+template <int MODE, typename T, int FIT, class CFG>
 __global__ void __launch_bounds__(CFG::NT, CFG::OCC) expert_gemm_staged(const ExpertArgs p) {
   constexpr int ES = sizeof(T), BM = CFG::BM, BN = CFG::BN, NT = CFG::NT, KB = CFG::KB, ROWB = CFG::ROWB;
   constexpr int EPC = 16 / ES, BK = KB / ES, CPR = CFG::CPR, TM = CFG::TM, TN = CFG::TN;
@@ -241,35 +276,71 @@ __global__ void __launch_bounds__(CFG::NT, CFG::OCC) expert_gemm_staged(const Ex
         for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
     const T* A = reinterpret_cast<const T*>(x.a);
     const T* B = reinterpret_cast<const T*>(x.b);
+    // A thread's chunks of a stage: loaded without a branch from places clamped into the operand,
+    // so that the loads of a stage are all in flight together; what the clamps moved is put right
+    // when the registers go to LDS, in the stages and tiles that have an edge. Only the contraction
+    // needs its zeros: rows and columns past C's are not stored.
     u32x4 ra[CFG::CA], rb[CFG::CB];
-    const u32x4 zero = {0, 0, 0, 0};
-    auto load_stage = [&](int k0) {
+    constexpr int RPQ = NT / CPR;       // rows that one chunk of every thread covers
+    constexpr bool CLAMP = FIT != CHUNK_TINY;
+    auto load_rows = [&](const T* src, int64_t ld, int row0, int rows, int k0, auto& r) {
+      const int e0 = k0 + (tid % CPR) * EPC, row = tid / CPR;
 #pragma unroll
-      for (int q = 0; q < CFG::CA; ++q) {
-        const int c = tid + NT * q;
-        if constexpr (AKM) {
-          const int k = k0 + c / CPM, i = x.row0 + (c % CPM) * EPC;
-          ra[q] = k < x.k ? load_chunk<T, VEC>(A + (int64_t)k * p.lda, i, x.m) : zero;
-        } else {
-          const int i = x.row0 + c / CPR;
-          ra[q] = i < x.m ? load_chunk<T, VEC>(A + (int64_t)i * p.lda, k0 + (c % CPR) * EPC, x.k) : zero;
-        }
-      }
-#pragma unroll
-      for (int q = 0; q < CFG::CB; ++q) {
-        const int c = tid + NT * q;
-        if constexpr (BKM) {
-          const int k = k0 + c / CPN, j = x.col0 + (c % CPN) * EPC;
-          rb[q] = k < x.k ? load_chunk<T, VEC>(B + (int64_t)k * p.ldb, j, p.n) : zero;
-        } else {
-          const int j = x.col0 + c / CPR;
-          rb[q] = j < p.n ? load_chunk<T, VEC>(B + (int64_t)j * p.ldb, k0 + (c % CPR) * EPC, x.k) : zero;
-        }
+      for (int q = 0; q < (int)(sizeof(r) / 16); ++q) {
+        const int first = row0 + RPQ * q;
+        if (first >= rows) break;       // equal in every lane
+        const T* at = src + (int64_t)min(first + row, rows - 1) * ld;
+        r[q] = load_chunk<T, FIT>(at, CLAMP ? min(e0, x.k - EPC) : e0, x.k);
       }
     };
-    auto store_stage = [&](int buf) {
+    auto load_deep = [&](const T* src, int64_t ld, int col0, int cols, int k0, auto& r, auto cpr_c) {
+      constexpr int C = decltype(cpr_c)::value;
+      const int c0 = col0 + (tid % C) * EPC;
+#pragma unroll
+      for (int q = 0; q < (int)(sizeof(r) / 16); ++q) {
+        const T* at = src + (int64_t)min(k0 + tid / C + NT / C * q, x.k - 1) * ld;
+        r[q] = load_chunk<T, FIT>(at, CLAMP ? min(c0, cols - EPC) : c0, cols);
+      }
+    };
+    auto mend_rows = [&](int k0, auto& r) {
+      const int e0 = k0 + (tid % CPR) * EPC;
+#pragma unroll
+      for (int q = 0; q < (int)(sizeof(r) / 16); ++q) {
+        if constexpr (FIT == CHUNK_ALIGNED) r[q] = e0 < x.k ? r[q] : u32x4{0, 0, 0, 0};
+        else if constexpr (CLAMP) r[q] = drop_first<T>(r[q], e0 - min(e0, x.k - EPC));
+      }
+    };
+    auto mend_deep = [&](int col0, int cols, int k0, auto& r, auto cpr_c) {
+      constexpr int C = decltype(cpr_c)::value;
+      const int c0 = col0 + (tid % C) * EPC;
+#pragma unroll
+      for (int q = 0; q < (int)(sizeof(r) / 16); ++q) {
+        if constexpr (FIT == CHUNK_ANY) r[q] = drop_first<T>(r[q], c0 - min(c0, cols - EPC));
+        r[q] = k0 + tid / C + NT / C * q < x.k ? r[q] : u32x4{0, 0, 0, 0};
+      }
+    };
+    using CM = std::integral_constant<int, CPM>;
+    using CN = std::integral_constant<int, CPN>;
+    auto load_stage = [&](int k0) {
+      if constexpr (AKM) load_deep(A, p.lda, x.row0, x.m, k0, ra, CM{});
+      else load_rows(A, p.lda, x.row0, x.m, k0, ra);
+      if constexpr (BKM) load_deep(B, p.ldb, x.col0, p.n, k0, rb, CN{});
+      else load_rows(B, p.ldb, x.col0, p.n, k0, rb);
+    };
+    auto store_stage = [&](int buf, int k0) {
       char* As = lds + buf * CFG::STAGE;
       char* Bs = As + BM * ROWB;
+      const bool cut = k0 + BK > x.k;
+      if constexpr (AKM) {
+        if (cut || (FIT == CHUNK_ANY && x.row0 + BM > x.m)) mend_deep(x.row0, x.m, k0, ra, CM{});
+      } else {
+        if (cut) mend_rows(k0, ra);
+      }
+      if constexpr (BKM) {
+        if (cut || (FIT == CHUNK_ANY && x.col0 + BN > p.n)) mend_deep(x.col0, p.n, k0, rb, CN{});
+      } else {
+        if (cut) mend_rows(k0, rb);
+      }
 #pragma unroll
       for (int q = 0; q < CFG::CA; ++q) {
         const int c = tid + NT * q;
@@ -288,37 +359,49 @@ __global__ void __launch_bounds__(CFG::NT, CFG::OCC) expert_gemm_staged(const Ex
       }
     };
     typedef typename Frag<T>::type F;
-    F fa[TM], fb[TN];
     int aoff[TM], boff[TN];
 #pragma unroll
     for (int i = 0; i < TM; ++i) aoff[i] = AKM ? kmajor_frag_off<BM * ES>(lane, wm * CFG::WTM + i * 32) : 0;
 #pragma unroll
     for (int j = 0; j < TN; ++j) boff[j] = BKM ? kmajor_frag_off<BN * ES>(lane, wn * CFG::WTN + j * 32) : 0;
     const int nk = (x.k + BK - 1) / BK;
-    if (nk) {
-      load_stage(0);
-      store_stage(0);
-      __syncthreads();
-    }
-    for (int kt = 0; kt < nk; ++kt) {
-      if (kt + 1 < nk) load_stage((kt + 1) * BK);
-      const char* As = lds + (kt & 1) * CFG::STAGE;
+    // A stage's products of the wave's first R row blocks.
+    auto compute = [&](int buf, auto r_c) {
+      constexpr int R = decltype(r_c)::value;
+      F fa[R], fb[TN];
+      const char* As = lds + buf * CFG::STAGE;
       const char* Bs = As + BM * ROWB;
 #pragma unroll
       for (int g = 0; g < CFG::NG; ++g) {
         if constexpr (!AKM)
-          load_frags<T, TM, TN, ROWB, !BKM>(As + (wm * CFG::WTM) * ROWB, Bs + (wn * CFG::WTN) * ROWB, lane, g, fa, fb);
+          load_frags<T, R, TN, ROWB, !BKM>(As + (wm * CFG::WTM) * ROWB, Bs + (wn * CFG::WTN) * ROWB, lane, g, fa, fb);
         else if constexpr (ES == 2)
-          load_b_kmajor<T, TM, BM * ES>(As, aoff, g, fa);
+          load_b_kmajor<T, R, BM * ES>(As, aoff, g, fa);
         else
-          load_b_kmajor_f32<TM, BM * ES>(As, lane, wm * CFG::WTM, g, fa);
+          load_b_kmajor_f32<R, BM * ES>(As, lane, wm * CFG::WTM, g, fa);
         if constexpr (BKM && ES == 2)
           load_b_kmajor<T, TN, BN * ES>(Bs, boff, g, fb);
         else if constexpr (BKM)
           load_b_kmajor_f32<TN, BN * ES>(Bs, lane, wn * CFG::WTN, g, fb);
-        mma<T, TM, TN>(fa, fb, acc);
+        mma<T, R, TN>(fa, fb, reinterpret_cast<f32x16(&)[R][TN]>(acc));
       }
-      if (kt + 1 < nk) store_stage((kt & 1) ^ 1);
+    };
+    // the wave's row blocks that hold any row: fp32 products of few rows are bound by MFMAs
+    const int nb = (x.m - x.row0 - wm * CFG::WTM + 31) / 32;
+    if (nk) {
+      load_stage(0);
+      store_stage(0, 0);
+      __syncthreads();
+    }
+    for (int kt = 0; kt < nk; ++kt) {
+      if (kt + 1 < nk) load_stage((kt + 1) * BK);
+      if constexpr (AKM && ES == 2) {
+        if (nb > 0) compute(kt & 1, std::integral_constant<int, TM>{});
+      } else {
+        if (nb >= TM) compute(kt & 1, std::integral_constant<int, TM>{});
+        else if (nb > 0) compute(kt & 1, std::integral_constant<int, 1>{});
+      }
+      if (kt + 1 < nk) store_stage((kt & 1) ^ 1, (kt + 1) * BK);
       __syncthreads();
     }
     expert_store<T, CFG>(p, x, lds, acc, lane);

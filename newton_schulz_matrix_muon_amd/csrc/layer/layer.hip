@@ -243,15 +243,26 @@ unsigned gemm_grid(int mode, const ExpertArgs& a, int64_t cols_n) {
   return (unsigned)(8 * std::max<int64_t>(1, (std::min(tm * tn, most) + 7) / 8));
 }
 
+// CHUNK_*: how a product's operand rows are loaded (the row operands' and W's widths, but for the
+// contraction of a weight gradient, which runs along the rows).
+template <int MODE>
+int chunk_fit(const ExpertArgs& a, int dt, bool vec) {
+  const int chunk = 16 / (int)dtype_size(dt);
+  if (vec) return CHUNK_ALIGNED;
+  return (MODE == EX_DW ? a.m : a.k) < chunk || (MODE != EX_FWD && a.n < chunk) ? CHUNK_TINY : CHUNK_ANY;
+}
+
 template <int MODE, class CFG>
 int run_staged(ExpertArgs a, int dt, bool vec, hipStream_t s) {
   a.tiles_n = (a.n + CFG::BN - 1) / CFG::BN;
   const unsigned g = gemm_grid<CFG>(MODE, a, a.n);
+  const int fit = chunk_fit<MODE>(a, dt, vec);
   return by_type(dt, [&](auto x) {
     using T = decltype(x);
     return launch(K_EXPERT_GEMM, s, [&] {
-      if (vec) hipLaunchKernelGGL((expert_gemm_staged<MODE, T, true, CFG>), dim3(g), dim3(CFG::NT), 0, s, a);
-      else hipLaunchKernelGGL((expert_gemm_staged<MODE, T, false, CFG>), dim3(g), dim3(CFG::NT), 0, s, a);
+      if (fit == CHUNK_ALIGNED) hipLaunchKernelGGL((expert_gemm_staged<MODE, T, CHUNK_ALIGNED, CFG>), dim3(g), dim3(CFG::NT), 0, s, a);
+      else if (fit == CHUNK_ANY) hipLaunchKernelGGL((expert_gemm_staged<MODE, T, CHUNK_ANY, CFG>), dim3(g), dim3(CFG::NT), 0, s, a);
+      else hipLaunchKernelGGL((expert_gemm_staged<MODE, T, CHUNK_TINY, CFG>), dim3(g), dim3(CFG::NT), 0, s, a);
     });
   });
 }
@@ -267,28 +278,51 @@ int run_pingpong(ExpertArgs a, int dt, hipStream_t s) {
 }
 
 // Few rows: a workgroup per 16 rows of each weight matrix that can have any.
-int run_few(const ExpertArgs& a, int dt, hipStream_t s) {
+int run_few(const ExpertArgs& a, int dt, bool vec, hipStream_t s) {
   const dim3 g((a.n + 15) / 16, (unsigned)std::min<int64_t>(a.experts, a.rows) + 1);
-  return launch(K_EXPERT_GEMM, s, [&] {
-    if (dt == BF16) hipLaunchKernelGGL((expert_few_fwd<__bf16>), g, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((expert_few_fwd<_Float16>), g, dim3(256), 0, s, a);
+  const int fit = chunk_fit<EX_FWD>(a, dt, vec);
+  return by_type(dt, [&](auto x) {
+    using T = decltype(x);
+    return launch(K_EXPERT_GEMM, s, [&] {
+      if (fit == CHUNK_ALIGNED) hipLaunchKernelGGL((expert_few_fwd<T, CHUNK_ALIGNED>), g, dim3(256), 0, s, a);
+      else if (fit == CHUNK_ANY) hipLaunchKernelGGL((expert_few_fwd<T, CHUNK_ANY>), g, dim3(256), 0, s, a);
+      else hipLaunchKernelGGL((expert_few_fwd<T, CHUNK_TINY>), g, dim3(256), 0, s, a);
+    });
   });
+}
+
+// Whether the forward product has few enough rows for the kernel that reads the weights once
+// (expert_few.hpp). One MI355X, its time against the 128 x 128 tiles', rows per expert:
+//   64 x 1408 x 2048, bf16: 4 rows 71 to 94 us, 8 rows 86 to 96; 27 x 2048 x 7168: 4 rows 133 to 142,
+//   8 rows 169 to 147; fp32, 64 x 1408 x 2048: 8 rows 192 to 241, 32 rows 465 to 389. Rows that begin
+//   anywhere, 64 x 1405 x 2045: bf16 1 row 81 to 59, fp32 4 rows 194 to 243, 16 rows 334 to 293.
+//   16-bit with short rows of W, 0.2 rows: 131 x 3432 x 440 20 to 29, 98 x 5872 x 296 19 to 24, 244 x
+//   4112 x 112 (224 bytes) 56 to 34, 260 x 5088 x 80 149 to 61.
+// Tiles for less than half of the CUs are bound by the latency of their stages, so it takes four
+// times the rows: 8 x 1000 x 776, bf16: 16 rows 6 to 14 us, 64 rows 14 to 15; fp32 32 rows 24 to 58;
+// 8 x 1001 x 777, bf16: 8 rows 9 to 15, 16 rows 16 to 15; fp32 16 rows 17 to 41. (Not more, for rows
+// that all go to one expert read its weights again for every 16.)
+bool few_rows(const ExpertArgs& a, int dt, int fit) {
+  const int64_t tiles = std::min<int64_t>(a.experts, a.rows) * ((a.n + 127) / 128);
+  const int64_t most = (fit == CHUNK_ALIGNED ? 4 : 2) * (dt == F32 ? 2 : 1) * (int64_t)a.experts;
+  if (2 * tiles <= device_cus()) return a.rows <= 4 * most;
+  return a.rows <= most && a.k * dtype_size(dt) >= 512 && (fit == CHUNK_ALIGNED || dt == F32);
 }
 
 // The kernel of a product. The 256 x 256 tiles need 16-bit types, whole 16-byte chunks everywhere,
 // extents that do not leave half of a tile empty, and enough tiles for half of the CUs. One
 // MI355X, bf16, 256 x 256 against 128 x 128 tiles: 27 experts of 2048 x 7168, 8 rows each, forward
-// 143 against 176 us, weight gradient 189 against 249; 256 rows 314 against 446, 441 against 652;
-// 128 experts of 512 x 512 (264 tiles), 32 rows 19 against 18 us, 64 rows 21 against 27, 512 rows
-// 54 against 73; 8 experts of 1000 x 776 (64 tiles), 320 rows 23 against 19 us, weight gradient (128
-// tiles) 20 against 20. The forward product of few rows has its own kernel (expert_few.hpp says from
-// where to where).
+// 139 against 147 us, weight gradient 174 against 237; 256 rows 315 against 405, 435 against 604;
+// 64 experts of 1408 x 2048, 16 rows 103 against 97 us, weight gradient 86 against 112; 128 rows 116
+// against 137; 128 experts of 512 x 512 (264 tiles), 32 rows 19 against 17 us, 64 rows 21 against 25,
+// 512 rows 58 against 73; 8 experts of 1000 x 776 (64 tiles), 320 rows 23 against 18 us, weight
+// gradient (128 tiles) 20 against 20.
 template <int MODE>
 int run_product(const ExpertArgs& a, int dt, bool vec, hipStream_t s) {
   // the largest list of the smallest tiles
   const int64_t tn = (a.n + 127) / 128, tm = MODE == EX_DW ? a.experts * ((a.m + 127) / 128) : a.rows / 128 + a.experts + 1;
   if (tn * tm > INT32_MAX) return MNS_ERR_SHAPE;
-  if (MODE == EX_FWD && vec && dt != F32 && a.rows <= 4 * a.experts) return run_few(a, dt, s);
+  if (MODE == EX_FWD && few_rows(a, dt, chunk_fit<EX_FWD>(a, dt, vec))) return run_few(a, dt, vec, s);
   const bool whole = vec && a.c_vec && a.n % 8 == 0 && dt != F32 && a.n > 128 && (MODE != EX_DW || a.m > 128);
   const int64_t high = MODE == EX_DW ? a.experts * ((a.m + 255) / 256) : a.rows / 256 + std::min<int64_t>(a.experts, a.rows);
   if (whole && 2 * high * ((a.n + 255) / 256) >= device_cus()) return run_pingpong<MODE>(a, dt, s);

@@ -403,6 +403,29 @@ def test_expert_products_strided_and_unaligned(torch, ops, dtype, pad, shift):
     check_product(torch, ops, x, dy, w, counts, offsets)
 
 
+NARROW = [(1, 9), (3, 8), (4, 4), (5, 7), (7, 5), (8, 3), (9, 1), (9, 17), (12, 31), (130, 15), (15, 130), (257, 33), (33, 2067)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("counts,rest", [([2, 0, 1], 1), ([17, 0, 3, 40], 0), ([70, 0, 130], 2)], ids=str)
+@pytest.mark.parametrize("n,k", NARROW)
+def test_expert_products_of_rows_shorter_than_a_load(torch, ops, n, k, counts, rest, dtype):
+    """Widths around 16 bytes and rows that begin at any element, their neighbours not finite."""
+    dt = getattr(torch, dtype)
+    gen = gen_for(torch, 31 * n + k)
+
+    def rows(r, c):                    # a base one element into the storage, one column behind each row
+        flat = torch.full((r * (c + 1) + 2,), float("nan"), device="cuda", dtype=dt)
+        out = flat[1:1 + r * (c + 1)].view(r, c + 1)[:, :c]
+        out.copy_(normal(torch, gen, r, c))
+        return out
+    total = sum(counts) + rest
+    x, dy, w = rows(total, k), rows(total, n), rows(len(counts) * n, k)
+    w = w.as_strided((len(counts), n, k), (n * w.stride(0), w.stride(0), 1), w.storage_offset())
+    offsets = torch.tensor([0] + counts, device="cuda").cumsum(0).to(torch.int32)
+    check_product(torch, ops, x, dy, w, counts, offsets)
+
+
 @pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
 def test_expert_products_at_model_widths(torch, ops, dtype):
     """27 experts of 2048 x 7168, skewed, with one empty: the sizes a card of the 216-expert layer holds."""
