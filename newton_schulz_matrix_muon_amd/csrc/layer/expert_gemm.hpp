@@ -138,9 +138,11 @@ struct ExpertList {
 };
 template <int MODE, class CFG>
 __device__ inline ExpertList expert_list(const ExpertArgs& p, const int* first) {
-  const int64_t total = (int64_t)p.tiles_n * (MODE == EX_DW ? p.experts * ((p.m + CFG::BM - 1) / CFG::BM) : wave_uniform(first[p.experts + 1]));
+  const int64_t tiles = (int64_t)p.tiles_n * (MODE == EX_DW ? p.experts * ((p.m + CFG::BM - 1) / CFG::BM) : wave_uniform(first[p.experts + 1]));
+  // the host keeps a launch's tiles below 2^31; offsets that fall and rise again can make more
+  const int64_t total = min(tiles, (int64_t)0x7fffffff);
   const int xcd = blockIdx.x & 7;
-  const int lo = (int)(total * xcd / 8);   // the host keeps a launch's tiles below 2^31
+  const int lo = (int)(total * xcd / 8);
   return {wave_uniform(lo), wave_uniform((int)(total * (xcd + 1) / 8) - lo)};
 }
 

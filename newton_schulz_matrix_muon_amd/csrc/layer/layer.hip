@@ -83,6 +83,12 @@ int by_type(int dt, F&& f) {
   return f(_Float16{});
 }
 
+// At least n workgroups of up to 1024 threads, numbered by block_id().
+dim3 grid_of(int64_t n) {
+  const int64_t x = std::min<int64_t>(n, 1 << 21);
+  return dim3((unsigned)x, (unsigned)((n + x - 1) / x));
+}
+
 hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
 
 // ------------------------------------------------------------------------------- layer norm
@@ -112,7 +118,7 @@ int norm_parts(int64_t rows, int64_t cols) {
 
 template <typename T, typename WT, bool VEC>
 void launch_norm_fwd(const NormArgs& a, hipStream_t s) {
-  const dim3 one((unsigned)a.rows), four((unsigned)((a.rows + 3) / 4));
+  const dim3 one = grid_of(a.rows), four = grid_of((a.rows + 3) / 4);
   if (a.cols <= held(64, 1)) hipLaunchKernelGGL((norm_fwd_row<T, WT, 64, 1, VEC>), four, dim3(256), 0, s, a);
   else if (a.cols <= held(64, 2)) hipLaunchKernelGGL((norm_fwd_row<T, WT, 64, 2, VEC>), four, dim3(256), 0, s, a);
   else if (a.cols <= held(64, 4)) hipLaunchKernelGGL((norm_fwd_row<T, WT, 64, 4, VEC>), four, dim3(256), 0, s, a);
@@ -184,12 +190,8 @@ RowsArgs rows_args(const mns_tensor* tok, const int32_t* rank, int32_t k) {
   return a;
 }
 
-// Workgroups of the (token, unit) kernels.
-bool rows_grid(const RowsArgs& a, unsigned* g) {
-  const int64_t n = (a.tokens * a.units + ROWS_NT - 1) / ROWS_NT;
-  *g = (unsigned)n;
-  return n <= INT32_MAX;
-}
+// Workgroups of the (token, unit) kernels: at most 2^24 x 2^20 / 256, two dimensions hold them.
+dim3 rows_grid(const RowsArgs& a) { return grid_of((a.tokens * a.units + ROWS_NT - 1) / ROWS_NT); }
 
 template <bool WEIGHTED>
 int gather(RowsArgs a, const mns_tensor* row, const mns_tensor* tok, hipStream_t s) {
@@ -199,13 +201,12 @@ int gather(RowsArgs a, const mns_tensor* row, const mns_tensor* tok, hipStream_t
   a.out_ld = row_bytes(tok);
   const bool vec = vec_rows(row) && vec_rows(tok) && tok->cols % 8 == 0;
   a.units = (int)(vec ? tok->cols / 8 : tok->cols);
-  unsigned g;
-  if (!rows_grid(a, &g)) return MNS_ERR_SHAPE;
+  const dim3 g = rows_grid(a);
   return by_type(tok->dtype, [&](auto x) {
     using T = decltype(x);
     return launch(K_ROUTE, s, [&] {
-      if (vec) hipLaunchKernelGGL((rows_gather<T, 8, WEIGHTED>), dim3(g), dim3(ROWS_NT), 0, s, a);
-      else hipLaunchKernelGGL((rows_gather<T, 1, WEIGHTED>), dim3(g), dim3(ROWS_NT), 0, s, a);
+      if (vec) hipLaunchKernelGGL((rows_gather<T, 8, WEIGHTED>), g, dim3(ROWS_NT), 0, s, a);
+      else hipLaunchKernelGGL((rows_gather<T, 1, WEIGHTED>), g, dim3(ROWS_NT), 0, s, a);
     });
   });
 }
@@ -444,7 +445,7 @@ int layer_norm_backward(const mns_tensor* dY, const mns_tensor* X, const float* 
           }))
         return st;
     } else if (rows) {
-      if (int st = launch(K_LAYER_NORM, s, [&] { hipLaunchKernelGGL((norm_dx_any<T, WT>), dim3((unsigned)rows), dim3(256), 0, s, a); })) return st;
+      if (int st = launch(K_LAYER_NORM, s, [&] { hipLaunchKernelGGL((norm_dx_any<T, WT>), grid_of(rows), dim3(256), 0, s, a); })) return st;
       if (grads)
         if (int st = launch(K_LAYER_NORM, s, [&] {
               hipLaunchKernelGGL((norm_dw_any<T>), dim3((a.cols + 255) / 256, a.nparts), dim3(256), 0, s, a);
@@ -503,13 +504,12 @@ int expert_dispatch(const mns_tensor* X, const int32_t* rank, int32_t k, const i
   const bool vec = vec_rows(X) && vec_rows(XS);
   const int es = dtype_size(X->dtype);
   a.units = (int)(vec ? X->cols * es / 16 : X->cols);
-  unsigned g;
-  if (!rows_grid(a, &g)) return MNS_ERR_SHAPE;
+  const dim3 g = rows_grid(a);
   const hipStream_t s = as_stream(stream);
   return launch(K_ROUTE, s, [&] {
-    if (vec) hipLaunchKernelGGL((rows_dispatch<u32x4>), dim3(g), dim3(ROWS_NT), 0, s, a);
-    else if (es == 4) hipLaunchKernelGGL((rows_dispatch<uint32_t>), dim3(g), dim3(ROWS_NT), 0, s, a);
-    else hipLaunchKernelGGL((rows_dispatch<uint16_t>), dim3(g), dim3(ROWS_NT), 0, s, a);
+    if (vec) hipLaunchKernelGGL((rows_dispatch<u32x4>), g, dim3(ROWS_NT), 0, s, a);
+    else if (es == 4) hipLaunchKernelGGL((rows_dispatch<uint32_t>), g, dim3(ROWS_NT), 0, s, a);
+    else hipLaunchKernelGGL((rows_dispatch<uint16_t>), g, dim3(ROWS_NT), 0, s, a);
   });
 }
 
@@ -561,12 +561,12 @@ int expert_combine_backward(const mns_tensor* dY, const mns_tensor* YS, const vo
   const bool vec = vec_rows(dY) && vec_rows(YS) && vec_rows(dYS) && dY->cols % 8 == 0;
   a.units = (int)(vec ? dY->cols / 8 : dY->cols);
   const hipStream_t s = as_stream(stream);
-  const dim3 g((unsigned)a.tokens);
+  const dim3 g = grid_of(a.tokens);
   return by_type(dY->dtype, [&](auto x) {
     using T = decltype(x);
     return launch(K_ROUTE, s, [&] {
-      if (vec) hipLaunchKernelGGL((rows_combine_bwd<T, 8, 256>), g, dim3(256), 0, s, a);
-      else hipLaunchKernelGGL((rows_combine_bwd<T, 1, 256>), g, dim3(256), 0, s, a);
+      if (vec) hipLaunchKernelGGL((rows_combine_bwd<T, 8>), g, dim3(ROWS_NT), 0, s, a);
+      else hipLaunchKernelGGL((rows_combine_bwd<T, 1>), g, dim3(ROWS_NT), 0, s, a);
     });
   });
 }

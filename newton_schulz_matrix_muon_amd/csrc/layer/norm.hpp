@@ -9,12 +9,17 @@
 // fixed order (no atomics), so a call's results are the same every time.
 //
 // Bound by HBM: the forward pass reads x and writes y, the backward pass reads x and dy and
-// writes dx; a few flops per byte.
+// writes dx; a few flops per byte. One MI355X, 16384 x 7168 bf16: forward 88 us, 5.3 TB/s (a large
+// copy reaches 5.0 to 5.3); backward with dw and db 147 us, 4.8 TB/s.
 #pragma once
 
 #include "../gemm.hpp"
 
 namespace mns {
+
+// The workgroup's number in a grid of up to two dimensions: a dimension holds fewer than 2^32
+// threads, which a workgroup per row can pass.
+__device__ inline int64_t block_id() { return blockIdx.x + (int64_t)blockIdx.y * gridDim.x; }
 
 // A strided [batch][rows][cols] buffer seen as batch * rows rows.
 struct RowsRef {
@@ -81,7 +86,8 @@ __device__ inline void block_sum2(float& a, float& b, float* red) {
 template <typename T, typename WT>
 __global__ void __launch_bounds__(256) norm_fwd_any(const NormArgs p) {
   __shared__ float red[3][32];
-  const int64_t r = blockIdx.x;
+  const int64_t r = block_id();
+  if (r >= p.rows) return;
   const T* x = row_ptr<T>(p.x, r);
   T* y = row_ptr<T>(p.y, r);
   const WT* w = reinterpret_cast<const WT*>(p.w);
@@ -112,7 +118,8 @@ __global__ void __launch_bounds__(256) norm_fwd_any(const NormArgs p) {
 template <typename T, typename WT>
 __global__ void __launch_bounds__(256) norm_dx_any(const NormArgs p) {
   __shared__ float red[32];
-  const int64_t r = blockIdx.x;
+  const int64_t r = block_id();
+  if (r >= p.rows) return;
   const T* x = row_ptr<T>(p.x, r);
   const T* dy = row_ptr<T>(p.dy, r);
   T* dx = row_ptr<T>(p.dx, r);
@@ -181,13 +188,14 @@ __device__ inline void piece_store(T* row, int i, int nt, int tid, int cols, con
 }
 
 // Forward: NT threads hold a row, VPT pieces each; x is read once, the mean and then the variance
-// come from the registers. NT = 64: four rows a workgroup, no barrier.
+// come from the registers. NT = 64: four rows a workgroup, no barrier. 16384 x 7168 bf16: 390 us
+// when a row is read three times (twice from cache), 88 so; one row 3.3 us.
 template <typename T, typename WT, int NT, int VPT, bool VEC>
 __global__ void __launch_bounds__(NT < 256 ? 256 : NT) norm_fwd_row(const NormArgs p) {
   __shared__ float red[2][32];
   const int tid = threadIdx.x % NT;
-  const int64_t r = (int64_t)blockIdx.x * (NT < 256 ? 256 / NT : 1) + threadIdx.x / NT;
-  if (NT == 64 && r >= p.rows) return;
+  const int64_t r = block_id() * (NT < 256 ? 256 / NT : 1) + threadIdx.x / NT;
+  if (r >= p.rows) return;   // whole waves (NT = 64), else the whole workgroup
   const T* x = row_ptr<T>(p.x, r);
   Piece<T, VEC> px[VPT];
 #pragma unroll
@@ -248,7 +256,9 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT) norm_fwd_row(const NormAr
 
 // Backward: a workgroup walks every gridDim.x-th row (or four of them, NT = 64) with the next
 // row's x and dy already on their way, and keeps its columns' dw and db in registers; they leave
-// once, as one part, for norm_dw_sum to add up.
+// once, as one part, for norm_dw_sum to add up. 16384 x 7168 bf16: 345 us with a barrier that waits
+// for the loads on their way as well, 141 with one that waits for LDS only and w in LDS, not in
+// registers (which spilled); 1021 x 2047 fp32, any alignment, 11 us.
 template <typename T, typename WT, int NT, int VPT, bool VEC>
 __global__ void __launch_bounds__(NT < 256 ? 256 : NT, NT >= 512 ? 4 : 1) norm_bwd_row(const NormArgs p) {
   constexpr int RPW = NT < 256 ? 256 / NT : 1;
@@ -369,7 +379,7 @@ __global__ void __launch_bounds__(256) norm_dw_any(const NormArgs p) {
 }
 
 // dw (blockIdx.y = 0) or db (1) from the parts: 64 columns a workgroup, its 16 waves each take
-// every 16th part, eight at a time.
+// every 16th part, eight at a time: 6.4 us for 7168 columns of 512 parts.
 template <typename WT>
 __global__ void __launch_bounds__(1024) norm_dw_sum(const NormArgs p) {
   __shared__ float red[16][64];

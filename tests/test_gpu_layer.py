@@ -501,6 +501,38 @@ def test_row_buffers_past_32_bits(torch, ops):
         close(dx[s], g @ m, 74 * 2.0 ** -23 * (g.abs() @ m.abs()), f"dx row {s}")
 
 
+def test_more_threads_than_a_grid_dimension_holds(torch, ops):
+    """A workgroup per token of 2^24 tokens, and a thread per element of 2^22 x 1025 that begin anywhere."""
+    gen = gen_for(torch, 8)
+    tokens, experts = 1 << 24, 5
+    x = normal(torch, gen, tokens, 1)
+    ids = torch.randint(-1, experts, (tokens, 1), generator=gen, device="cuda", dtype=torch.int32)
+    offsets, rank = ops.expert_sort(ids, experts)
+    some = (ids >= 0).view(-1)
+    at = rank.view(-1).long()[some]
+    xs = ops.expert_dispatch(x, rank, offsets)
+    assert torch.equal(xs[at], x[some]) and not xs[int(offsets[-1]):].any()
+    w = normal(torch, gen, tokens, 1)
+    y = ops.expert_combine(xs, w, rank)
+    assert torch.equal(y[some], (w * x)[some]) and not y[~some].any()
+    dys, dw = ops.expert_combine_backward(x, xs, w, rank, offsets)
+    assert torch.equal(dys[at], (w * x)[some]) and not dys[int(offsets[-1]):].any()
+    assert torch.equal(dw[some], (x * x)[some]) and not dw[~some].any()
+    del x, xs, w, y, dys, dw
+
+    tokens, cols = 1 << 22, 1025
+    x = torch.arange(tokens, device="cuda", dtype=torch.int32).to(torch.bfloat16).view(-1, 1).expand(tokens, cols).contiguous()
+    offsets, rank = ops.expert_sort(ids[:tokens], experts)
+    xs = ops.expert_dispatch(x, rank, offsets)
+    some = (ids[:tokens] >= 0).view(-1)
+    at = rank.view(-1).long()[some]
+    for c in (0, cols - 1):
+        assert torch.equal(xs[:, c][at], x[:, c][some]) and not xs[int(offsets[-1]):, c].any()
+    dx = ops.expert_dispatch_backward(xs, rank)
+    for c in (0, cols - 1):
+        assert torch.equal(dx[:, c][some], x[:, c][some]) and not dx[:, c][~some].any()
+
+
 def test_layer_norm_past_32_bits(torch, ops):
     rows, cols = 300000, 7168
     x = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
