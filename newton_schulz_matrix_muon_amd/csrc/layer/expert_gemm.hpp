@@ -204,6 +204,26 @@ __device__ inline ExpertTile expert_tile(const ExpertArgs& p, const int* first, 
   return x;
 }
 
+// Elements c .. c + 7 of a row of n, at any address.
+template <typename T>
+__device__ inline void store_eight(T* out, int c, int n, const f32x4& a, const f32x4& b) {
+  constexpr int DT = sizeof(T) == 4 ? F32 : (__is_same(T, __bf16) ? BF16 : F16);
+  const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  if (c + 8 <= n) {
+    u32x4_any* o = reinterpret_cast<u32x4_any*>(out + c);
+    if constexpr (sizeof(T) == 4) {
+      o[0] = __builtin_bit_cast(u32x4, a);
+      o[1] = __builtin_bit_cast(u32x4, b);
+    } else {
+      o[0] = u32x4{pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7])};
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (c + e < n) store_elem(out, DT, c + e, v[e]);
+  }
+}
+
 // Accumulators to C: through an fp32 slab in LDS, whole rows of 16-byte vectors out.
 template <typename T, class CFG>
 __device__ inline void expert_store(const ExpertArgs& p, const ExpertTile& x, char* lds, const f32x16 (&acc)[CFG::TM][CFG::TN], int lane) {
@@ -211,7 +231,6 @@ __device__ inline void expert_store(const ExpertArgs& p, const ExpertTile& x, ch
   constexpr int SR = CFG::SR, SROWS = SR * WTM, VPR = BN / 8;
   const int wave = wave_uniform(threadIdx.x >> 6), tid = wave * 64 + lane;
   const int wm = wave / CFG::WVN, wn = wave % CFG::WVN;
-  constexpr int DT = sizeof(T) == 4 ? F32 : (__is_same(T, __bf16) ? BF16 : F16);
   float* Cs = reinterpret_cast<float*>(lds);
   for (int sl = 0; sl < CFG::WVM / SR; ++sl) {
     if (wm / SR == sl) acc_to_slab<CFG>(Cs, acc, lane, wn, (wm % SR) * WTM);
@@ -223,25 +242,46 @@ __device__ inline void expert_store(const ExpertArgs& p, const ExpertTile& x, ch
       if (r < x.m && c < p.n) {
         const f32x4 a = *reinterpret_cast<const f32x4*>(Cs + lr * CP + lc);
         const f32x4 b = *reinterpret_cast<const f32x4*>(Cs + lr * CP + lc + 4);
-        const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-        T* out = reinterpret_cast<T*>(x.c) + (int64_t)r * p.ldc;
-        if (c + 8 <= p.n) {
-          u32x4_any* o = reinterpret_cast<u32x4_any*>(out + c);
-          if constexpr (sizeof(T) == 4) {
-            o[0] = __builtin_bit_cast(u32x4, a);
-            o[1] = __builtin_bit_cast(u32x4, b);
-          } else {
-            o[0] = u32x4{pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7])};
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (c + e < p.n) store_elem(out, DT, c + e, v[e]);
-        }
+        store_eight(reinterpret_cast<T*>(x.c) + (int64_t)r * p.ldc, c, p.n, a, b);
       }
     }
     lds_barrier();
   }
+}
+
+// kmajor_swizzle and kmajor_frag_off of gemm.hpp for rows of C chunks, 8 as well as 16.
+template <int C>
+__device__ constexpr int stage_swizzle(int s) { return kmajor_swizzle(s) & (C - 1); }
+template <int RB>
+__device__ inline int stage_frag_off(int lane, int n0) {
+  const int j16 = lane & 15, qo = (lane >> 4) & 1, hi = lane >> 5;
+  const int n = n0 + 16 * qo + 4 * (j16 & 3);
+  return (8 * hi + (j16 >> 2)) * RB + (((n >> 3) ^ stage_swizzle<RB / 16>(j16 >> 2)) << 4) + 8 * (j16 & 1);
+}
+
+// G waves' sums of one tile to C, added up in the waves' order.
+template <typename T, class CFG, int G>
+__device__ inline void expert_store_split(const ExpertArgs& p, const ExpertTile& x, char* lds, const f32x16 (&acc)[CFG::TM][CFG::TN], int lane) {
+  constexpr int BM = CFG::BM, BN = CFG::BN, CP = CFG::CP, VPR = BN / 8;
+  const int wave = wave_uniform(threadIdx.x >> 6);
+  acc_to_slab<CFG>(reinterpret_cast<float*>(lds + wave * CFG::STAGE), acc, lane, 0, 0);
+  lds_barrier();
+#pragma unroll 1
+  for (int idx = wave * 64 + lane; idx < BM * VPR; idx += 64 * G) {
+    const int lr = idx / VPR, lc = (idx - lr * VPR) * 8;
+    const int r = x.row0 + lr, c = x.col0 + lc;
+    if (r < x.m && c < p.n) {
+      f32x4 a = {0.f, 0.f, 0.f, 0.f}, b = a;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const float* Cs = reinterpret_cast<const float*>(lds + g * CFG::STAGE) + lr * CP + lc;
+        a += *reinterpret_cast<const f32x4*>(Cs);
+        b += *reinterpret_cast<const f32x4*>(Cs + 4);
+      }
+      store_eight(reinterpret_cast<T*>(x.c) + (int64_t)r * p.ldc, c, p.n, a, b);
+    }
+  }
+  lds_barrier();
 }
 
 // Operands staged through registers: every type, any alignment and length (FIT). 128 x 128 tiles of
@@ -253,18 +293,27 @@ __device__ inline void expert_store(const ExpertArgs& p, const ExpertTile& x, ch
 // element for such rows took 3.5 times as long (3056 x 1466, 135 rows each, forward 393 us, now
 // 134), loads under a condition per lane 1.3 to 2 times (the compiler waits for one before the
 // next). fp32 is bound by its MFMAs, so blocks of 32 rows that have none are left out.
-template <int MODE, typename T, int FIT, class CFG>
-__global__ void __launch_bounds__(CFG::NT, CFG::OCC) expert_gemm_staged(const ExpertArgs p) {
+//
+// G > 1 (few tiles): 64 x 64 tiles whose G waves take every G-th stage each, on their own: a wave
+// stages into its own piece of LDS, where its reads and writes keep their order without a barrier,
+// and the sums meet at the end. A stage of a 128 x 128 tile alone on its CU takes about 1 us (loads,
+// LDS, barrier, MFMAs one after the other; fp32 1.8), so eight waves side by side cut the time of a
+// long contraction to a third: 3 experts of 504 x 4000 bf16, 256 rows each, 54 us to 19.
+template <int MODE, typename T, int FIT, class CFG, int G = 1>
+__global__ void __launch_bounds__(CFG::NT * G, CFG::OCC) expert_gemm_staged(const ExpertArgs p) {
   constexpr int ES = sizeof(T), BM = CFG::BM, BN = CFG::BN, NT = CFG::NT, KB = CFG::KB, ROWB = CFG::ROWB;
   constexpr int EPC = 16 / ES, BK = KB / ES, CPR = CFG::CPR, TM = CFG::TM, TN = CFG::TN;
   constexpr bool AKM = MODE == EX_DW, BKM = MODE != EX_FWD;
   constexpr int CPM = BM * ES / 16, CPN = BN * ES / 16;   // chunks per contraction-major row
-  __shared__ __align__(16) char lds[CFG::LDS];
+  static_assert(G == 1 || (CFG::NT == 64 && CFG::STAGE >= CFG::SLAB), "the parts of a split tile are waves");
+  __shared__ __align__(16) char lds_all[G > 1 ? G * CFG::STAGE : CFG::LDS];
   __shared__ int first[EXPERT_MAX + 2];
-  __shared__ int wsum[NT / 64];
-  const int tid = threadIdx.x, lane = tid & 63, wave = wave_uniform(tid >> 6);
+  __shared__ int wsum[NT * G / 64];
+  const int part = G > 1 ? wave_uniform(threadIdx.x >> 6) : 0;
+  char* lds = lds_all + part * CFG::STAGE;
+  const int tid = G > 1 ? threadIdx.x & 63 : threadIdx.x, lane = tid & 63, wave = G > 1 ? 0 : wave_uniform(tid >> 6);
   const int wm = wave / CFG::WVN, wn = wave % CFG::WVN;
-  if constexpr (MODE != EX_DW) expert_tiles<NT, BM>(p, first, wsum);
+  if constexpr (MODE != EX_DW) expert_tiles<NT * G, BM>(p, first, wsum);
   const ExpertList l = expert_list<MODE, CFG>(p, first);
   int from = 0;
   for (int t = blockIdx.x >> 3; t < l.n; t += gridDim.x >> 3) {
@@ -347,7 +396,7 @@ __global__ void __launch_bounds__(CFG::NT, CFG::OCC) expert_gemm_staged(const Ex
       for (int q = 0; q < CFG::CA; ++q) {
         const int c = tid + NT * q;
         if constexpr (AKM)
-          *reinterpret_cast<u32x4*>(As + (c / CPM) * (BM * ES) + (((c % CPM) ^ kmajor_swizzle((c / CPM) & 3)) << 4)) = ra[q];
+          *reinterpret_cast<u32x4*>(As + (c / CPM) * (BM * ES) + (((c % CPM) ^ stage_swizzle<CPM>((c / CPM) & 3)) << 4)) = ra[q];
         else
           *reinterpret_cast<u32x4*>(As + (c / CPR) * ROWB + (c % CPR) * 16) = ra[q];
       }
@@ -355,7 +404,7 @@ __global__ void __launch_bounds__(CFG::NT, CFG::OCC) expert_gemm_staged(const Ex
       for (int q = 0; q < CFG::CB; ++q) {
         const int c = tid + NT * q;
         if constexpr (BKM)
-          *reinterpret_cast<u32x4*>(Bs + (c / CPN) * (BN * ES) + (((c % CPN) ^ kmajor_swizzle((c / CPN) & 3)) << 4)) = rb[q];
+          *reinterpret_cast<u32x4*>(Bs + (c / CPN) * (BN * ES) + (((c % CPN) ^ stage_swizzle<CPN>((c / CPN) & 3)) << 4)) = rb[q];
         else
           *reinterpret_cast<u32x4*>(Bs + (c / CPR) * ROWB + (c % CPR) * 16) = rb[q];
       }
@@ -363,9 +412,9 @@ __global__ void __launch_bounds__(CFG::NT, CFG::OCC) expert_gemm_staged(const Ex
     typedef typename Frag<T>::type F;
     int aoff[TM], boff[TN];
 #pragma unroll
-    for (int i = 0; i < TM; ++i) aoff[i] = AKM ? kmajor_frag_off<BM * ES>(lane, wm * CFG::WTM + i * 32) : 0;
+    for (int i = 0; i < TM; ++i) aoff[i] = AKM ? stage_frag_off<BM * ES>(lane, wm * CFG::WTM + i * 32) : 0;
 #pragma unroll
-    for (int j = 0; j < TN; ++j) boff[j] = BKM ? kmajor_frag_off<BN * ES>(lane, wn * CFG::WTN + j * 32) : 0;
+    for (int j = 0; j < TN; ++j) boff[j] = BKM ? stage_frag_off<BN * ES>(lane, wn * CFG::WTN + j * 32) : 0;
     const int nk = (x.k + BK - 1) / BK;
     // A stage's products of the wave's first R row blocks.
     auto compute = [&](int buf, auto r_c) {
@@ -390,6 +439,26 @@ __global__ void __launch_bounds__(CFG::NT, CFG::OCC) expert_gemm_staged(const Ex
     };
     // the wave's row blocks that hold any row: fp32 products of few rows are bound by MFMAs
     const int nb = (x.m - x.row0 - wm * CFG::WTM + 31) / 32;
+    auto products = [&](int buf) {
+      if constexpr (AKM && ES == 2) {
+        if (nb > 0) compute(buf, std::integral_constant<int, TM>{});
+      } else {
+        if (nb >= TM) compute(buf, std::integral_constant<int, TM>{});
+        else if (nb > 0) compute(buf, std::integral_constant<int, 1>{});
+      }
+    };
+    if constexpr (G > 1) {
+      if (part < nk) load_stage(part * BK);
+      for (int kt = part; kt < nk; kt += G) {
+        store_stage(0, kt * BK);
+        __builtin_amdgcn_wave_barrier();
+        if (kt + G < nk) load_stage((kt + G) * BK);
+        products(0);
+        __builtin_amdgcn_wave_barrier();
+      }
+      expert_store_split<T, CFG, G>(p, x, lds_all, acc, lane);
+      continue;
+    }
     if (nk) {
       load_stage(0);
       store_stage(0, 0);
@@ -397,12 +466,7 @@ __global__ void __launch_bounds__(CFG::NT, CFG::OCC) expert_gemm_staged(const Ex
     }
     for (int kt = 0; kt < nk; ++kt) {
       if (kt + 1 < nk) load_stage((kt + 1) * BK);
-      if constexpr (AKM && ES == 2) {
-        if (nb > 0) compute(kt & 1, std::integral_constant<int, TM>{});
-      } else {
-        if (nb >= TM) compute(kt & 1, std::integral_constant<int, TM>{});
-        else if (nb > 0) compute(kt & 1, std::integral_constant<int, 1>{});
-      }
+      products(kt & 1);
       if (kt + 1 < nk) store_stage((kt & 1) ^ 1, (kt + 1) * BK);
       __syncthreads();
     }

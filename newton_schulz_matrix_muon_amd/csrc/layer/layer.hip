@@ -268,6 +268,26 @@ int run_staged(ExpertArgs a, int dt, bool vec, hipStream_t s) {
   });
 }
 
+using Tile64 = TileCfg<64, 64, 1, 1, 128, 1, 2>;
+
+// Few tiles: 64 x 64 ones, each split over eight waves, one workgroup a CU.
+template <int MODE>
+int run_split(ExpertArgs a, int dt, bool vec, hipStream_t s) {
+  constexpr int G = 8;
+  a.tiles_n = (a.n + 63) / 64;
+  const int64_t tm = MODE == EX_DW ? a.experts * ((a.m + 63) / 64) : a.rows / 64 + std::min<int64_t>(a.experts, a.rows) + 1;
+  const dim3 g((unsigned)(8 * ((std::min<int64_t>(tm * a.tiles_n, device_cus()) + 7) / 8)));
+  const int fit = chunk_fit<MODE>(a, dt, vec);
+  return by_type(dt, [&](auto x) {
+    using T = decltype(x);
+    return launch(K_EXPERT_GEMM, s, [&] {
+      if (fit == CHUNK_ALIGNED) hipLaunchKernelGGL((expert_gemm_staged<MODE, T, CHUNK_ALIGNED, Tile64, G>), g, dim3(64 * G), 0, s, a);
+      else if (fit == CHUNK_ANY) hipLaunchKernelGGL((expert_gemm_staged<MODE, T, CHUNK_ANY, Tile64, G>), g, dim3(64 * G), 0, s, a);
+      else hipLaunchKernelGGL((expert_gemm_staged<MODE, T, CHUNK_TINY, Tile64, G>), g, dim3(64 * G), 0, s, a);
+    });
+  });
+}
+
 template <int MODE>
 int run_pingpong(ExpertArgs a, int dt, hipStream_t s) {
   a.tiles_n = (a.n + TilePP::BN - 1) / TilePP::BN;
@@ -300,14 +320,32 @@ int run_few(const ExpertArgs& a, int dt, bool vec, hipStream_t s) {
 //   16-bit with short rows of W, 0.2 rows: 131 x 3432 x 440 20 to 29, 98 x 5872 x 296 19 to 24, 244 x
 //   4112 x 112 (224 bytes) 56 to 34, 260 x 5088 x 80 149 to 61.
 // Tiles for less than half of the CUs are bound by the latency of their stages, so it takes four
-// times the rows: 8 x 1000 x 776, bf16: 16 rows 6 to 14 us, 64 rows 14 to 15; fp32 32 rows 24 to 58;
-// 8 x 1001 x 777, bf16: 8 rows 9 to 15, 16 rows 16 to 15; fp32 16 rows 17 to 41. (Not more, for rows
-// that all go to one expert read its weights again for every 16.)
+// times the rows, but for 16-bit rows that begin anywhere; against split tiles, 8 x 1000 x 776, bf16:
+// 16 rows 5.6 to 7.4 us, 32 rows 10 to 8; fp32 (1001 x 777) 16 rows 17 to 19; bf16 8 x 1001 x 777: 8
+// rows 8.8 to 8.1; 3 x 505 x 4001: 1 row 15 to 17, 8 rows 20 to 18.
 bool few_rows(const ExpertArgs& a, int dt, int fit) {
   const int64_t tiles = std::min<int64_t>(a.experts, a.rows) * ((a.n + 127) / 128);
   const int64_t most = (fit == CHUNK_ALIGNED ? 4 : 2) * (dt == F32 ? 2 : 1) * (int64_t)a.experts;
-  if (2 * tiles <= device_cus()) return a.rows <= 4 * most;
-  return a.rows <= most && a.k * dtype_size(dt) >= 512 && (fit == CHUNK_ALIGNED || dt == F32);
+  const bool whole = fit == CHUNK_ALIGNED || dt == F32;
+  if (2 * tiles <= device_cus()) return a.rows <= (whole ? 4 * most : most);
+  return a.rows <= most && a.k * dtype_size(dt) >= 512 && whole;
+}
+
+// Whether a product takes 64 x 64 tiles, each split along the contraction over eight waves: where
+// they fit the CUs at once (fp32, whose MFMAs bound it: nine times that) and the contraction has
+// four stages or more. One MI355X, 128 x 128 against split tiles, bf16: 8 experts of 1000 x 776,
+// forward 64 rows (192 tiles) 15.2 to 8.6 us, 256 rows (576) 17 to 21; 3 of 504 x 4000, forward 256
+// rows (108) 54 to 19, input gradient 32 rows (189) 11.1 to 6.6, 256 rows (850) 13 to 20; 12 of 5361 x
+// 2944, 26 rows (1008) 192 to 230. fp32, 64 of 1405 x 2045, forward 16 rows (1408) 294 to 210, 64 rows
+// (2112) 407 to 419, input gradient 1 row (2112) 204 to 121. Weight gradients: 6 of 152 x 88 fp32, 1093
+// rows (36 tiles) 420 to 130 with the input's; 8 of 1001 x 777 fp32 (1664) 14 to 39.
+template <int MODE>
+bool split_tiles(const ExpertArgs& a, int dt) {
+  const int64_t stage = 128 / dtype_size(dt);
+  const int64_t some = std::min<int64_t>(a.experts, a.rows);   // experts that can have rows
+  const int64_t high = MODE == EX_DW ? a.experts * ((a.m + 63) / 64) : std::max(some, a.rows / 64 + some / 2);
+  const int64_t tiles = high * ((a.n + 63) / 64), deep = MODE == EX_DW ? a.rows / a.experts : a.k;
+  return deep >= 4 * stage && tiles <= (dt == F32 && MODE != EX_DW ? 9 : 1) * (int64_t)device_cus();
 }
 
 // The kernel of a product. The 256 x 256 tiles need 16-bit types, whole 16-byte chunks everywhere,
@@ -327,6 +365,7 @@ int run_product(const ExpertArgs& a, int dt, bool vec, hipStream_t s) {
   const bool whole = vec && a.c_vec && a.n % 8 == 0 && dt != F32 && a.n > 128 && (MODE != EX_DW || a.m > 128);
   const int64_t high = MODE == EX_DW ? a.experts * ((a.m + 255) / 256) : a.rows / 256 + std::min<int64_t>(a.experts, a.rows);
   if (whole && 2 * high * ((a.n + 255) / 256) >= device_cus()) return run_pingpong<MODE>(a, dt, s);
+  if (split_tiles<MODE>(a, dt)) return run_split<MODE>(a, dt, vec, s);
   return run_staged<MODE, Tile128>(a, dt, vec, s);
 }
 

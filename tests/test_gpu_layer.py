@@ -403,11 +403,12 @@ def test_expert_products_strided_and_unaligned(torch, ops, dtype, pad, shift):
     check_product(torch, ops, x, dy, w, counts, offsets)
 
 
-NARROW = [(1, 9), (3, 8), (4, 4), (5, 7), (7, 5), (8, 3), (9, 1), (9, 17), (12, 31), (130, 15), (15, 130), (257, 33), (33, 2067)]
+NARROW = [(1, 9), (3, 8), (4, 4), (5, 7), (7, 5), (8, 3), (9, 1), (9, 17), (12, 31), (130, 15), (15, 130), (257, 33), (33, 2067),
+          (300, 5), (301, 261)]
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("counts,rest", [([2, 0, 1], 1), ([17, 0, 3, 40], 0), ([70, 0, 130], 2)], ids=str)
+@pytest.mark.parametrize("counts,rest", [([2, 0, 1], 1), ([17, 0, 3, 40], 0), ([70, 0, 130], 2), ([400, 0, 390], 1)], ids=str)
 @pytest.mark.parametrize("n,k", NARROW)
 def test_expert_products_of_rows_shorter_than_a_load(torch, ops, n, k, counts, rest, dtype):
     """Widths around 16 bytes and rows that begin at any element, their neighbours not finite."""
