@@ -283,7 +283,8 @@ int run_split(ExpertArgs a, int dt, bool vec, hipStream_t s) {
     return launch(K_EXPERT_GEMM, s, [&] {
       if (fit == CHUNK_ALIGNED) hipLaunchKernelGGL((expert_gemm_staged<MODE, T, CHUNK_ALIGNED, Tile64, G>), g, dim3(64 * G), 0, s, a);
       else if (fit == CHUNK_ANY) hipLaunchKernelGGL((expert_gemm_staged<MODE, T, CHUNK_ANY, Tile64, G>), g, dim3(64 * G), 0, s, a);
-      else hipLaunchKernelGGL((expert_gemm_staged<MODE, T, CHUNK_TINY, Tile64, G>), g, dim3(64 * G), 0, s, a);
+      else if constexpr (MODE != EX_FWD)   // whose contraction would be one short row
+        hipLaunchKernelGGL((expert_gemm_staged<MODE, T, CHUNK_TINY, Tile64, G>), g, dim3(64 * G), 0, s, a);
     });
   });
 }
