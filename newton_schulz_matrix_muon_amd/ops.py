@@ -525,16 +525,25 @@ def hybrid_step(matrix_groups, vector_params, *, muon: dict, adamw: dict):
 # ------------------------------------------------------------------ the layer around the experts
 # Layer norm and a mixture of experts, forward and backward, next to the optimizer that takes
 # their gradients: expert_matmul_backward's dW is muon_step's G, the norm's are adamw_step's.
-# Gradients are explicit calls; a call that autograd would have to record is refused.
+# Gradients are explicit calls; a call that autograd would have to record, or whose forward-mode
+# tangent would be lost, is refused.
 
 MAX_EXPERTS = 1024
 
 
 def _check_recorded(what, *ts):
+    torch = _torch()
     for t in ts:
-        if t is not None and t.requires_grad and _torch().is_grad_enabled():
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
             raise RuntimeError(f"{what}: not recorded by autograd; call it under torch.no_grad() (or in an "
                                "autograd.Function) and its gradient explicitly")
+    # a dual tensor does not require grad; duals exist inside a dual level only (0.3 us a tensor to ask)
+    fwad = torch.autograd.forward_ad
+    if getattr(fwad, "_current_level", 0) >= 0:
+        for t in ts:
+            if t is not None and fwad.unpack_dual(t).tangent is not None:
+                raise RuntimeError(f"{what}: no forward-mode derivative; pass the primal (forward_ad.unpack_dual) and take "
+                                   "the tangent through the explicit formulas")
 
 
 def _check_rows(what, ref, **named):

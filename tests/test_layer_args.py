@@ -242,3 +242,28 @@ def test_binding_refuses_what_autograd_would_have_to_record(torch, ops):
         ops.layer_norm(torch.zeros(8, 64, requires_grad=True))
     with torch.no_grad(), pytest.raises(ValueError, match="device tensors"):
         ops.expert_matmul(torch.zeros(8, 64), w, off)
+
+
+def test_binding_refuses_forward_mode_tangents(torch, ops):
+    """A dual tensor's tangent would be lost: refused, with gradients enabled or not."""
+    from torch.autograd import forward_ad as fwad
+    x, w, off = torch.zeros(8, 64), torch.zeros(3, 32, 64), torch.zeros(4, dtype=torch.int32)
+    stat, rank, picks = torch.zeros(8), torch.zeros(8, 1, dtype=torch.int32), torch.ones(8, 1)
+    with fwad.dual_level():
+        dual = lambda t: fwad.make_dual(t, torch.ones_like(t))
+        calls = [lambda: ops.layer_norm(dual(x)), lambda: ops.layer_norm(x, dual(torch.ones(64))),
+                 lambda: ops.layer_norm_backward(dual(x), x, stat, stat), lambda: ops.expert_dispatch(dual(x), rank, off),
+                 lambda: ops.expert_dispatch_backward(dual(x), rank), lambda: ops.expert_combine(x, dual(picks), rank),
+                 lambda: ops.expert_combine_backward(x, dual(x), picks, rank, off), lambda: ops.expert_matmul(x, dual(w), off),
+                 lambda: ops.expert_matmul_grad_input(dual(x[:, :32].contiguous()), w, off),
+                 lambda: ops.expert_matmul_grad_weight(x[:, :32], dual(x), off), lambda: ops.expert_matmul_backward(x[:, :32], dual(x), w, off)]
+        for call in calls:
+            with pytest.raises(RuntimeError, match="forward-mode"):
+                call()
+            with torch.no_grad(), pytest.raises(RuntimeError, match="forward-mode"):
+                call()
+        # a tensor without a tangent passes this check, and so does a dual where torch itself drops tangents
+        with pytest.raises(ValueError, match="device tensors"):
+            ops.layer_norm(x)
+        with fwad._set_fwd_grad_enabled(False), pytest.raises(ValueError, match="device tensors"):
+            ops.layer_norm(dual(x))
