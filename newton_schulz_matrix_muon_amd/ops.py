@@ -619,7 +619,7 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, out=None):
     row, for the backward pass."""
     torch = _torch()
     what = "layer_norm"
-    _check_recorded(what, x, weight, bias)
+    _check_recorded(what, x, weight, bias, out)
     xd = describe(x)
     _check_flat(what, x, (x.dtype, torch.float32), weight=weight, bias=bias)
     lead, cols = x.shape[:-1], x.shape[-1:]
@@ -655,7 +655,7 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, *, param_grads: bool = T
     weight's dtype; they are None without weight or with param_grads=False."""
     torch = _torch()
     what = "layer_norm_backward"
-    _check_recorded(what, dy, x, weight)
+    _check_recorded(what, dy, x, mean, rstd, weight, out)
     _check_same_shape(what, x, dy=dy, out=out)
     for name, t in (("dy", dy), ("out", out)):
         if t is not None and t.dtype != x.dtype:
@@ -714,7 +714,7 @@ def expert_dispatch(x, rank, offsets, *, out=None):
     ([tokens * k, dim]; C ABI ``expert_dispatch``)."""
     torch = _torch()
     what = "expert_dispatch"
-    _check_recorded(what, x)
+    _check_recorded(what, x, out)
     _check_rank(what, rank, offsets)
     _check_rows(what, x, x=x, out=out)
     _check_shape(what, "rank", rank, (x.shape[0], rank.shape[1]))
@@ -730,7 +730,7 @@ def expert_dispatch_backward(dxs, rank, *, out=None):
     """dx[t] = sum_j dxs[rank[t, j]] (C ABI ``expert_dispatch_backward``)."""
     torch = _torch()
     what = "expert_dispatch_backward"
-    _check_recorded(what, dxs)
+    _check_recorded(what, dxs, out)
     _check_rank(what, rank)
     _check_rows(what, dxs, dxs=dxs, out=out)
     _check_shape(what, "dxs", dxs, (rank.numel(), dxs.shape[1]))
@@ -747,7 +747,7 @@ def expert_combine(ys, weights, rank, *, out=None):
     dtype or float32; a slot without a row adds nothing, whatever its weight."""
     torch = _torch()
     what = "expert_combine"
-    _check_recorded(what, ys, weights)
+    _check_recorded(what, ys, weights, out)
     _check_rank(what, rank)
     _check_rows(what, ys, ys=ys, out=out)
     _check_flat(what, ys, (ys.dtype, torch.float32), weights=weights)
@@ -766,7 +766,7 @@ def expert_combine_backward(dy, ys, weights, rank, offsets, *, out=None):
     dtype, 0 for a slot without a row."""
     torch = _torch()
     what = "expert_combine_backward"
-    _check_recorded(what, dy, ys, weights)
+    _check_recorded(what, dy, ys, weights, out)
     _check_rank(what, rank, offsets)
     _check_rows(what, ys, dy=dy, ys=ys, out=out)
     _check_flat(what, ys, (ys.dtype, torch.float32), weights=weights)

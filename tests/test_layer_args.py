@@ -267,3 +267,23 @@ def test_binding_refuses_forward_mode_tangents(torch, ops):
             ops.layer_norm(x)
         with fwad._set_fwd_grad_enabled(False), pytest.raises(ValueError, match="device tensors"):
             ops.layer_norm(dual(x))
+
+
+def test_binding_refuses_results_and_statistics_that_autograd_tracks(torch, ops):
+    """`out` that requires grad would be overwritten behind autograd's back, kept statistics lose their gradient."""
+    leaf = lambda *shape: torch.zeros(*shape, requires_grad=True)
+    x, w, off = torch.zeros(8, 64), torch.zeros(3, 32, 64), torch.zeros(4, dtype=torch.int32)
+    y, stat, rank, picks = torch.zeros(8, 32), torch.zeros(8), torch.zeros(8, 1, dtype=torch.int32), torch.ones(8, 1)
+    calls = [lambda: ops.layer_norm(x, out=leaf(8, 64)), lambda: ops.layer_norm_backward(x, x, stat, stat, out=leaf(8, 64)),
+             lambda: ops.layer_norm_backward(x, x, leaf(8), stat), lambda: ops.layer_norm_backward(x, x, stat, leaf(8)),
+             lambda: ops.expert_dispatch(x, rank, off, out=leaf(8, 64)), lambda: ops.expert_dispatch_backward(x, rank, out=leaf(8, 64)),
+             lambda: ops.expert_combine(x, picks, rank, out=leaf(8, 64)),
+             lambda: ops.expert_combine_backward(x, x, picks, rank, off, out=leaf(8, 64)),
+             lambda: ops.expert_matmul(x, w, off, out=leaf(8, 32)), lambda: ops.expert_matmul_grad_input(y, w, off, out=leaf(8, 64)),
+             lambda: ops.expert_matmul_grad_weight(y, x, off, out=leaf(3, 32, 64))]
+    for i, call in enumerate(calls):
+        with pytest.raises(RuntimeError, match="autograd"):
+            call()
+            pytest.fail(f"call {i}")
+        with torch.no_grad(), pytest.raises(ValueError, match="device tensors"):
+            call()
