@@ -270,7 +270,8 @@ MNS_API int gram_ns_trace(const mns_tensor* G, const mns_tensor* O, const mns_ns
  * lives on another GPU. Rows from offsets[E] to S - 1 belong to no expert and are written as
  * zeros. E is at most 1024. offsets and rank stay on the device and are not read on the host: a
  * rank outside 0 .. S - 1 counts as -1, offsets are cut to 0 .. S and an expert whose end lies
- * before its beginning has no rows, so no buffer contents lead to an access out of range.
+ * before its beginning has no rows, so no buffer contents lead to an access out of range. (Rows
+ * that offsets in no order give to several experts, or to none, have unspecified results.)
  */
 
 /*

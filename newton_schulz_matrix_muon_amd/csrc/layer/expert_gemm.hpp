@@ -45,14 +45,38 @@ struct ExpertArgs {
 };
 
 // Beginning and end of expert e's rows; e = E: the rows of nobody.
-__device__ inline void expert_rows(const ExpertArgs& p, int e, int* lo, int* hi) {
+__host__ __device__ inline void expert_rows(const ExpertArgs& p, int e, int* lo, int* hi) {
   const int rows = (int)p.rows, a = p.offsets[e], b = e < p.experts ? p.offsets[e + 1] : rows;
   *lo = min(max(a, 0), rows);
   *hi = min(max(b, *lo), rows);
 }
 
-// first[e] = tile rows (of BM) of the experts before e, e = 0 .. E + 1: entry E begins the tile
-// rows over the rows of nobody, entry E + 1 is the total. rows (ROWS): beginning and number of each
+// The arithmetic of the tile list in plain functions, which a test compiles for the host.
+//
+// Tile rows before an expert, cut so that their number of tiles fits 32 bits. The host keeps a
+// call's tiles below 2^31, so nothing is cut but what offsets that fall and rise again make: experts
+// that share rows have up to E / 2 times the tile rows that S rows have.
+__host__ __device__ inline int list_rows(int64_t tile_rows, int tiles_n) {
+  return (int)min(tile_rows, (int64_t)(0x7fffffff / tiles_n));
+}
+
+// Whether all tiles up to expert i's last lie before or at tile t of the list.
+__host__ __device__ inline bool ends_by(const int* first, int i, int tiles_n, int t) { return first[i + 1] * tiles_n <= t; }
+
+// Tile r of an expert with tm x tiles_n of them: in bands of EXPERT_BAND tile rows, down a band,
+// then one tile column right.
+constexpr int EXPERT_BAND = 8;
+struct TileAt {
+  int row, col;
+};
+__host__ __device__ inline TileAt tile_at(int r, int tm, int tiles_n) {
+  const int band = r / (EXPERT_BAND * tiles_n), high = min(tm - band * EXPERT_BAND, EXPERT_BAND);
+  r -= band * EXPERT_BAND * tiles_n;
+  return {band * EXPERT_BAND + r % high, r / high};
+}
+
+// first[e] = tile rows (of BM) of the experts before e, as list_rows cuts them, e = 0 .. E + 1: entry
+// E begins the tile rows over the rows of nobody, entry E + 1 is the total. rows (ROWS): beginning and number of each
 // expert's rows. Ends with a barrier.
 template <int NT, int BM, bool ROWS = false>
 __device__ inline void expert_tiles(const ExpertArgs& p, int* first, int* wsum, int2* rows = nullptr) {
@@ -81,8 +105,8 @@ __device__ inline void expert_tiles(const ExpertArgs& p, int* first, int* wsum, 
       all += wsum[w];
     }
     base += all;
-    if (e <= p.experts) first[e] = before + run - n;
-    if (e == p.experts) first[e + 1] = before + run;
+    if (e <= p.experts) first[e] = list_rows(before + run - n, p.tiles_n);
+    if (e == p.experts) first[e + 1] = list_rows(before + run, p.tiles_n);
     __syncthreads();
   }
 }
@@ -138,19 +162,16 @@ struct ExpertList {
 };
 template <int MODE, class CFG>
 __device__ inline ExpertList expert_list(const ExpertArgs& p, const int* first) {
-  const int64_t tiles = (int64_t)p.tiles_n * (MODE == EX_DW ? p.experts * ((p.m + CFG::BM - 1) / CFG::BM) : wave_uniform(first[p.experts + 1]));
-  // the host keeps a launch's tiles below 2^31; offsets that fall and rise again can make more
-  const int64_t total = min(tiles, (int64_t)0x7fffffff);
+  // below 2^31: a weight gradient's by the host's check, the others' also by list_rows
+  const int64_t total = (int64_t)p.tiles_n * (MODE == EX_DW ? p.experts * ((p.m + CFG::BM - 1) / CFG::BM) : wave_uniform(first[p.experts + 1]));
   const int xcd = blockIdx.x & 7;
   const int lo = (int)(total * xcd / 8);
   return {wave_uniform(lo), wave_uniform((int)(total * (xcd + 1) / 8) - lo)};
 }
 
-// Tile t of an XCD's list. Tiles go expert by expert, within one in bands of EXPERT_BAND tile
-// rows, down a band, then one tile column right, so that the tiles that run together share panels
-// of both operands in L2. *from: the expert of the tile before, or 0.
-// rows (ROWS): as expert_tiles left them.
-constexpr int EXPERT_BAND = 8;
+// Tile t of an XCD's list. Tiles go expert by expert, within one in bands (tile_at), so that the
+// tiles that run together share panels of both operands in L2. *from: the expert of the tile
+// before, or 0. rows (ROWS): as expert_tiles left them.
 template <int MODE, typename T, class CFG, bool ROWS = false>
 __device__ inline ExpertTile expert_tile(const ExpertArgs& p, const int* first, const ExpertList& l, int t, int* from,
                                          const int2* rows = nullptr) {
@@ -169,7 +190,7 @@ __device__ inline ExpertTile expert_tile(const ExpertArgs& p, const int* first, 
       const int lane = threadIdx.x & 63;
       e = 0;
       for (int i = lane; i - lane <= p.experts; i += 64)
-        e += __builtin_popcountll(__ballot(i <= p.experts && first[i + 1] * p.tiles_n <= t));
+        e += __builtin_popcountll(__ballot(i <= p.experts && ends_by(first, i, p.tiles_n, t)));
     }
     *from = e;
     const int f = wave_uniform(first[e]);
@@ -185,10 +206,9 @@ __device__ inline ExpertTile expert_tile(const ExpertArgs& p, const int* first, 
   }
   lo = wave_uniform(lo);
   hi = wave_uniform(hi);
-  const int band = r / (EXPERT_BAND * p.tiles_n), high = min(tm - band * EXPERT_BAND, EXPERT_BAND);
-  r -= band * EXPERT_BAND * p.tiles_n;
-  x.row0 = (band * EXPERT_BAND + r % high) * CFG::BM;
-  x.col0 = (r / high) * CFG::BN;
+  const TileAt at = tile_at(r, tm, p.tiles_n);
+  x.row0 = at.row * CFG::BM;
+  x.col0 = at.col * CFG::BN;
   x.a = p.A + (int64_t)lo * p.lda * ES;
   if constexpr (MODE == EX_DW) {
     x.m = p.m;

@@ -463,6 +463,28 @@ def test_offsets_out_of_range_are_cut(torch, ops):
     assert not xs.any()
 
 
+def test_offsets_in_no_order_write_nothing_outside(torch, ops):
+    """Experts that share rows: the results are unspecified, what lies around them stays."""
+    gen = gen_for(torch, 14)
+    for rows, n, k, dt in ((10, 64, 64, torch.float32), (300, 264, 328, torch.bfloat16), (700, 520, 136, torch.float16), (900, 130, 70, torch.bfloat16)):
+        for raw in ([0, rows] * 9, [rows // 2, rows, 3, -5, rows + 9, 0, rows], [2 ** 31 - 1, -2 ** 31, 5, 4, 3, 2 ** 31 - 1, 0, 7]):
+            off = torch.tensor(raw, dtype=torch.int32, device="cuda")
+            w = normal(torch, gen, len(raw) - 1, n, k).to(dt)
+            x, dy = normal(torch, gen, rows, k).to(dt), normal(torch, gen, rows, n).to(dt)
+            for call, r, c in ((lambda o: ops.expert_matmul(x, w, off, out=o), rows, n),
+                               (lambda o: ops.expert_matmul_grad_input(dy, w, off, out=o), rows, k)):
+                full = torch.full((r + 4, c + 16), 7.0, dtype=dt, device="cuda")
+                call(full[2:-2, 8:-8])
+                full[2:-2, 8:-8] = 7.0
+                assert (full == 7.0).all()
+            dw = ops.expert_matmul_grad_weight(dy, x, off)   # each expert's own rows, shared or not
+            for e, (lo, hi) in enumerate(zip(raw, raw[1:])):
+                lo = min(max(lo, 0), rows)
+                hi = min(max(hi, lo), rows)
+                g, a = dy[lo:hi].double(), x[lo:hi].double()
+                close(dw[e], g.T @ a, (hi - lo + 2) * 2.0 ** -23 * (g.abs().T @ a.abs()), f"dw of expert {e}")
+
+
 def test_row_buffers_past_32_bits(torch, ops):
     """40000 tokens of 7168 with 8 picks: the row side holds 2.3e9 elements."""
     gen = gen_for(torch, 6)
