@@ -5,6 +5,7 @@ Usage: python -m newton_schulz_matrix_muon_amd.build [-v] [--hostsan]
 from __future__ import annotations
 
 import os
+import re
 import subprocess
 import sys
 
@@ -33,18 +34,36 @@ BUILD = os.path.join(ROOT, "_build")
 HOSTSAN_LIB = os.path.join(BUILD, "libmuon_ns_hostsan.so")
 
 
-def _run(cmds, verbose: bool, what: str) -> None:
-    """Run the commands side by side; raise with the compiler's messages if one fails."""
+RESOURCES = "-Rpass-analysis=kernel-resource-usage"
+
+
+def check_registers(remarks: str) -> int:
+    """Raise if a kernel of the compiler's resource remarks (RESOURCES) uses accumulation registers; returns the
+    number of kernels. The compiler moves an MFMA's result out of them (v_accvgpr_read) behind a branch without
+    the wait states that the MFMA needs, so a kernel whose sums live there reads them too early. Kernels of at
+    least two waves a SIMD (__launch_bounds__) keep their sums in vector registers, where it does wait."""
+    used = re.findall(r"Function Name: (\S+).*?AGPRs: (\d+)", remarks, re.S)
+    bad = [name for name, n in used if int(n)]
+    if bad:
+        raise RuntimeError("kernels with sums in accumulation registers: " + ", ".join(bad))
+    return len(used)
+
+
+def _run(cmds, verbose: bool, what: str) -> str:
+    """Run the commands side by side; raise with the compiler's messages if one fails. Returns the remarks."""
+    remarks = ""
     if verbose:
         for cmd in cmds:
             print(" ".join(cmd), flush=True)
     procs = [subprocess.Popen(c, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True) for c in cmds]
     for p, (_, err) in zip(procs, [p.communicate() for p in procs]):
-        errs = [l for l in err.splitlines() if "packed-fp32-ops" not in l]
+        remarks += "".join(l + "\n" for l in err.splitlines() if RESOURCES in l)
+        errs = [l for l in err.splitlines() if "packed-fp32-ops" not in l and RESOURCES not in l]
         if p.returncode != 0:
             raise RuntimeError(f"{what} failed:\n" + "\n".join(errs))
         if verbose and errs:
             print("\n".join(errs))
+    return remarks
 
 
 def _object(source: str, suffix: str) -> str:
@@ -56,8 +75,10 @@ def build(verbose: bool = False) -> str:
     tmp = LIB + ".tmp"
     objs = [_object(s, ".o") for s in SOURCES]
     flags = [f for f in HIPCC_FLAGS if f != "-shared"]
-    _run([[hipcc(), *flags, "-I", os.path.join(ROOT, "include"), "-I", CSRC, "-c", os.path.join(CSRC, s), "-o", o]
-          for s, o in zip(SOURCES, objs)], verbose, "hipcc")
+    remarks = _run([[hipcc(), *flags, RESOURCES, "-I", os.path.join(ROOT, "include"), "-I", CSRC, "-c", os.path.join(CSRC, s), "-o", o]
+                    for s, o in zip(SOURCES, objs)], verbose, "hipcc")
+    if not check_registers(remarks):
+        raise RuntimeError("hipcc printed no resource remarks")
     _run([[hipcc(), *HIPCC_FLAGS, *objs, "-o", tmp]], verbose, "hipcc (link)")
     os.replace(tmp, LIB)
     return LIB

@@ -55,8 +55,9 @@ __device__ inline f32x4 mma16(const u32x4& a, const u32x4& b, f32x4 c) {
 // waves take every fourth piece of K, whose 128 bytes four lanes of a row read whole (the order of
 // the contraction within a piece does not matter as long as both operands agree), and their sums
 // meet in LDS. One wave's pieces are loaded eight at a time.
-// (Two workgroups a CU at least, so that the sums stay out of the accumulation registers: there the
-// compiler read one behind a branch without the wait that the last product needs.)
+// (Two waves a SIMD at least: up to 256 registers a lane the compiler takes the MFMAs whose sums are in
+// vector registers. In accumulation registers it moves them out behind the loop's branch without the
+// wait that the last product needs; build.py refuses a library with a kernel that has any.)
 template <typename T, int FIT>
 __global__ void __launch_bounds__(256, 2) expert_few_fwd(const ExpertArgs p) {
   constexpr int U = 8;               // pieces of a wave in flight

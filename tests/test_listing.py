@@ -1,6 +1,7 @@
 """Rules that the compiler cannot keep for the kernels, checked on the listings it makes of them (gfx950, no GPU needed)."""
 import os
 import re
+import shutil
 import subprocess
 
 import pytest
@@ -10,15 +11,15 @@ from newton_schulz_matrix_muon_amd import build as b
 pytestmark = pytest.mark.skipif(not os.path.exists("/opt/rocm/bin/hipcc"), reason="no compiler")
 
 
-def listing(tmp_path, include, kernel):
-    """The gfx950 assembly of one kernel's instantiation."""
+def listing(tmp_path, include, kernel, csrc=b.CSRC, flags=()):
+    """The gfx950 assembly of one kernel's instantiation, and what the compiler said."""
     src, out = tmp_path / "one.hip", tmp_path / "one.s"
     src.write_text(f'#include <hip/hip_runtime.h>\n#include "{include}"\nnamespace mns {{ template __global__ void {kernel}; }}\n')
-    flags = [f for f in b.HIPCC_FLAGS if f not in ("-shared",)]
-    r = subprocess.run([b.hipcc(), *flags, "--cuda-device-only", "-S", "-I", os.path.join(b.ROOT, "include"), "-I", b.CSRC,
+    flags = [f for f in b.HIPCC_FLAGS if f != "-shared"] + list(flags)
+    r = subprocess.run([b.hipcc(), *flags, "--cuda-device-only", "-S", "-I", os.path.join(b.ROOT, "include"), "-I", csrc,
                         str(src), "-o", str(out)], capture_output=True, text=True)
     assert r.returncode == 0, r.stderr[-3000:]
-    return out.read_text()
+    return out.read_text(), r.stderr
 
 
 def instructions(text):
@@ -69,7 +70,7 @@ def test_the_dma_waits_for_the_scalars_it_reads(tmp_path, mode, dtype):
     """A vector memory instruction may read a scalar register five wait states after a vector instruction wrote it,
     at the earliest. The compiler does not look into the asm statement that issues the DMA: a wait has to follow
     the last of the scalars' writes (and the compiler must not write them again on the way)."""
-    ins, follow = instructions(listing(tmp_path, "layer/expert_pingpong.hpp", f"expert_gemm_pp<{mode}, {dtype}>(ExpertArgs)"))
+    ins, follow = instructions(listing(tmp_path, "layer/expert_pingpong.hpp", f"expert_gemm_pp<{mode}, {dtype}>(ExpertArgs)")[0])
     assert sum(name.startswith("buffer_load") and ops[-1] == "0" for name, ops in ins) >= 16
     reads = lambda name, ops: set().union(*(registers("s", o) for o in ops)) if name.startswith("buffer_") else set()
     writes = lambda name, ops: registers("s", ops[0]) if name.startswith("s_") else set()
@@ -80,3 +81,21 @@ def test_the_dma_waits_for_the_scalars_it_reads(tmp_path, mode, dtype):
             assert states_before_read(ins, follow, i, registers("s", ops[0]), reads, writes, 5) >= 5, (name, ops)
     # the statement sets m0 without the compiler's knowledge, so nothing else may live in it
     assert not [(name, ops) for name, ops in ins if "m0" in ops and not (name == "s_mov_b32" and ops[0] == "m0")]
+
+
+@pytest.mark.parametrize("dtype", ["float", "__bf16", "_Float16"])
+def test_sums_in_accumulation_registers_are_refused(tmp_path, dtype):
+    """The few rows' kernel as it is passes the build's check; built for one wave a SIMD, where the compiler puts its sums
+    into accumulation registers, it does not."""
+    kernel = f"expert_few_fwd<{dtype}, CHUNK_ALIGNED>(ExpertArgs)"
+    assert b.check_registers(listing(tmp_path, "layer/expert_few.hpp", kernel, flags=[b.RESOURCES])[1]) == 1
+    one = tmp_path / "csrc"
+    shutil.copytree(b.CSRC, one)
+    path = one / "layer" / "expert_few.hpp"
+    text = path.read_text()
+    assert text.count("__launch_bounds__(256, 2) expert_few_fwd") == 1
+    path.write_text(text.replace("__launch_bounds__(256, 2) expert_few_fwd", "__launch_bounds__(256) expert_few_fwd"))
+    asm, said = listing(tmp_path, "layer/expert_few.hpp", kernel, csrc=str(one), flags=[b.RESOURCES])
+    assert "v_accvgpr_read" in asm
+    with pytest.raises(RuntimeError, match="expert_few_fwd"):
+        b.check_registers(said)
