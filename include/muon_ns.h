@@ -258,7 +258,9 @@ MNS_API int gram_ns_trace(const mns_tensor* G, const mns_tensor* O, const mns_ns
  *    element offsets may pass 32 bits. At most 2^24 rows, 2^20 columns, ld <= 2^20; more is
  *    MNS_ERR_SHAPE. Any alignment of the element size and any ld is accepted; rows of whole
  *    16-byte chunks at 16-byte aligned addresses run the fast kernels.
- *  - Outputs must not overlap inputs or each other (MNS_ERR_ARG).
+ *  - Outputs must not overlap inputs or each other (MNS_ERR_ARG). Parts of one larger buffer may be
+ *    an input and an output where they share no byte and lie at one distance: ranges of columns of
+ *    rows with the same ld, or matrices of batches with the same stride.
  *  - Sums are fp32 in a fixed order; each result is rounded once to its buffer's dtype, so equal
  *    calls give equal bits.
  *  - Workspaces are device memory aligned to 16 bytes.

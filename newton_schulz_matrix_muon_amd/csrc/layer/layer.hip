@@ -8,13 +8,13 @@
 
 #include <algorithm>
 #include <cmath>
-#include <initializer_list>
 
 #include "../host.hpp"
 #include "expert_few.hpp"
 #include "expert_gemm.hpp"
 #include "expert_pingpong.hpp"
 #include "norm.hpp"
+#include "overlap.hpp"
 #include "rows.hpp"
 
 using namespace mns;
@@ -37,31 +37,8 @@ int check_rows(const mns_tensor* t) {
   return MNS_OK;
 }
 
-struct Span {
-  uintptr_t lo, hi;
-};
-Span span(const mns_tensor* t) {
-  const uintptr_t lo = reinterpret_cast<uintptr_t>(t->ptr);
-  if (!t->rows) return {lo, lo};
-  const int64_t last = (t->batch - 1) * (t->batch > 1 ? t->stride : 0) + (t->rows - 1) * t->ld + t->cols;
-  return {lo, lo + (uintptr_t)(last * dtype_size(t->dtype))};
-}
-Span span(const void* p, int64_t bytes) {
-  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-  return {lo, p ? lo + (uintptr_t)bytes : lo};
-}
-
-// An output that shares bytes with an input or another output: each of `out` against all.
-bool clash(std::initializer_list<Span> out, std::initializer_list<Span> in) {
-  for (auto a = out.begin(); a != out.end(); ++a) {
-    if (a->lo == a->hi) continue;
-    for (auto b = out.begin(); b != a; ++b)
-      if (a->lo < b->hi && b->lo < a->hi) return true;
-    for (const Span& b : in)
-      if (a->lo < b.hi && b.lo < a->hi) return true;
-  }
-  return false;
-}
+Span span(const mns_tensor* t) { return mns::span(t, dtype_size(t->dtype)); }
+using mns::span;
 
 bool same_rows(const mns_tensor* a, const mns_tensor* b) {
   return a->batch == b->batch && a->rows == b->rows && a->cols == b->cols;

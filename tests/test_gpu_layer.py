@@ -568,6 +568,38 @@ def test_layer_norm_past_32_bits(torch, ops):
     assert torch.equal(dx[5], dx[-1]) and torch.equal(db, 2 * y[5].float())
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_halves_of_one_buffer_as_input_and_output(torch, ops, dtype):
+    """Columns of one wider buffer, and every other matrix of one batch, on both sides of a call."""
+    dt = getattr(torch, dtype)
+    gen = gen_for(torch, 15)
+    for rows, cols, e in ((70, 64, 3), (301, 33, 2), (2000, 264, 5)):
+        both = lambda r: normal(torch, gen, r, 2 * cols).to(dt)
+        buf = both(rows)
+        x = buf[:, :cols].clone()
+        y, mean, rstd = ops.layer_norm(buf[:, :cols], out=buf[:, cols:])
+        assert torch.equal(y, ops.layer_norm(x)[0]) and torch.equal(buf[:, :cols], x)
+        buf = both(rows)
+        dy, want = buf[:, cols:].clone(), ops.layer_norm_backward(buf[:, cols:].clone(), x, mean, rstd)[0]
+        assert torch.equal(ops.layer_norm_backward(buf[:, cols:], x, mean, rstd, out=buf[:, :cols])[0], want) and torch.equal(buf[:, cols:], dy)
+        off = torch.linspace(0, rows, e + 1, device="cuda").to(torch.int32)
+        w = normal(torch, gen, e, cols, cols).to(dt)
+        buf = both(rows)
+        x, want = buf[:, :cols].clone(), ops.expert_matmul(buf[:, :cols].clone(), w, off)
+        assert torch.equal(ops.expert_matmul(buf[:, :cols], w, off, out=buf[:, cols:]), want) and torch.equal(buf[:, :cols], x)
+        want = ops.expert_matmul_grad_input(x, w, off)
+        assert torch.equal(ops.expert_matmul_grad_input(buf[:, :cols], w, off, out=buf[:, cols:]), want) and torch.equal(buf[:, :cols], x)
+        with pytest.raises(RuntimeError, match="MNS_ERR_ARG"):
+            ops.expert_matmul(buf[:, :cols], w, off, out=buf[:, cols - 1:-1])
+        ids = torch.randint(-1, e, (rows, 1), generator=gen, device="cuda", dtype=torch.int32)
+        offsets, rank = ops.expert_sort(ids, e)
+        want = ops.expert_dispatch(x, rank, offsets)
+        assert torch.equal(ops.expert_dispatch(buf[:, :cols], rank, offsets, out=buf[:, cols:]), want) and torch.equal(buf[:, :cols], x)
+        pairs = normal(torch, gen, 3, 2, rows, cols).to(dt)
+        x = pairs[:, 0].clone()
+        assert torch.equal(ops.layer_norm(pairs[:, 0], out=pairs[:, 1])[0], ops.layer_norm(x)[0]) and torch.equal(pairs[:, 0], x)
+
+
 # ------------------------------------------------------------------------- streams, graphs
 
 def layer_inputs(torch, dt, seed=2, tokens=200, k=4, experts=10, dim=256, inner=192):
