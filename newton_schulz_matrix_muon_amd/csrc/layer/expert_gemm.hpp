@@ -32,8 +32,8 @@ constexpr int EXPERT_MAX = 1024;
 enum { EX_FWD = 0, EX_DX = 1, EX_DW = 2 };
 
 struct ExpertArgs {
-  const char* A; int64_t lda, sA;   // elements; s: matrix stride of W, unused for row operands
-  const char* B; int64_t ldb, sB;
+  const char* A; int64_t lda;       // elements
+  const char* B; int64_t ldb, sB;   // sB, sC: from matrix to matrix, where there is one per expert
   char* C; int64_t ldc, sC;
   const int32_t* offsets;
   int experts;

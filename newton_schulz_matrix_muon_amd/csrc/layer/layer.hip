@@ -163,7 +163,6 @@ RowsArgs rows_args(const mns_tensor* tok, const int32_t* rank, int32_t k) {
   a.k = k;
   a.tokens = tok->rows;
   a.slots = tok->rows * k;
-  a.cols = (int)tok->cols;
   return a;
 }
 
@@ -351,7 +350,6 @@ ExpertArgs product_args(const mns_tensor* A, const mns_tensor* B, const mns_tens
   ExpertArgs a{};
   a.A = reinterpret_cast<const char*>(A->ptr);
   a.lda = A->ld;
-  a.sA = A->stride;
   a.B = reinterpret_cast<const char*>(B->ptr);
   a.ldb = B->ld;
   a.sB = B->batch > 1 ? B->stride : 0;

@@ -156,7 +156,6 @@ struct RowsArgs {
   int64_t tokens, slots;
   int k, experts;
   int units;                         // accesses per row
-  int cols;
 };
 
 constexpr int ROWS_NT = 256;
