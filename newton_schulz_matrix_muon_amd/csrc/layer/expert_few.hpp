@@ -2,9 +2,9 @@
 // time is that of reading the weights of the experts that have rows, once, so the work is cut
 // along the weights, 16 of their rows a workgroup, until every CU reads.
 //
-// One MI355X, bf16, weights from HBM (128 x 128 tiles in brackets): 64 experts of 1408 x 2048, 6 rows
-// 9.7 us, 64 rows 50 us at 5.0 TB/s (56), 256 rows 73 us (94); 27 experts of 2048 x 7168, 27 rows
-// 92 us at 5.7 TB/s (134), 108 rows 144 us (142). The input gradient stays on the tiles: they read
+// One MI355X, bf16, weights from HBM (128 x 128 tiles in brackets), rows in all, each of an expert at
+// random: 64 experts of 1408 x 2048, 6 rows 10.2 us (28), 64 rows 48 us at 4.9 TB/s (61), 256 rows 75 us
+// (97); 27 experts of 2048 x 7168, 27 rows 96 us at 5.2 TB/s (147), 108 rows 150 us (153). The input gradient stays on the tiles: they read
 // W by whole rows, 5.2 TB/s from one row an expert on.
 #pragma once
 

@@ -308,17 +308,16 @@ __device__ inline void expert_store_split(const ExpertArgs& p, const ExpertTile&
 // 4 waves, one stage of K ahead in registers (two ahead gained 1 % at 50 registers more), 64 KB of
 // LDS and two workgroups a CU, so that one computes while the other waits.
 //
-// One MI355X, bf16, 64 experts with 64 rows each: 1408 x 2048 forward 102 us, input gradient 96,
-// weight gradient 146; 1405 x 2045, whose rows begin anywhere, 124, 122, 195. Loads element by
-// element for such rows took 3.5 times as long (3056 x 1466, 135 rows each, forward 393 us, now
-// 134), loads under a condition per lane 1.3 to 2 times (the compiler waits for one before the
-// next). fp32 is bound by its MFMAs, so blocks of 32 rows that have none are left out.
+// One MI355X, bf16, 64 experts with 64 rows on average: 1408 x 2048 forward 108 us, input gradient 82,
+// weight gradient 147; 1405 x 2045, whose rows begin anywhere, 122, 95, 189. Loads element by
+// element for such rows took 3 times as long, loads under a condition per lane 1.3 to 2 times (the
+// compiler waits for one before the next). fp32 is bound by its MFMAs, so blocks of 32 rows that have none are left out.
 //
 // G > 1 (few tiles): 64 x 64 tiles whose G waves take every G-th stage each, on their own: a wave
 // stages into its own piece of LDS, where its reads and writes keep their order without a barrier,
 // and the sums meet at the end. A stage of a 128 x 128 tile alone on its CU takes about 1 us (loads,
 // LDS, barrier, MFMAs one after the other; fp32 1.8), so eight waves side by side cut the time of a
-// long contraction to a third: 3 experts of 504 x 4000 bf16, 256 rows each, 54 us to 19.
+// long contraction to a third: 3 experts of 504 x 4000 bf16, 256 rows each, 61 us to 20.
 template <int MODE, typename T, int FIT, class CFG, int G = 1>
 __global__ void __launch_bounds__(CFG::NT * G, CFG::OCC) expert_gemm_staged(const ExpertArgs p) {
   constexpr int ES = sizeof(T), BM = CFG::BM, BN = CFG::BN, NT = CFG::NT, KB = CFG::KB, ROWB = CFG::ROWB;

@@ -290,16 +290,17 @@ int run_few(const ExpertArgs& a, int dt, bool vec, hipStream_t s) {
 }
 
 // Whether the forward product has few enough rows for the kernel that reads the weights once
-// (expert_few.hpp). One MI355X, its time against the 128 x 128 tiles', rows per expert:
-//   64 x 1408 x 2048, bf16: 4 rows 71 to 94 us, 8 rows 86 to 96; 27 x 2048 x 7168: 4 rows 133 to 142,
-//   8 rows 169 to 147; fp32, 64 x 1408 x 2048: 8 rows 192 to 241, 32 rows 465 to 389. Rows that begin
-//   anywhere, 64 x 1405 x 2045: bf16 1 row 81 to 59, fp32 4 rows 194 to 243, 16 rows 334 to 293.
-//   16-bit with short rows of W, 0.2 rows: 131 x 3432 x 440 20 to 29, 98 x 5872 x 296 19 to 24, 244 x
-//   4112 x 112 (224 bytes) 56 to 34, 260 x 5088 x 80 149 to 61.
+// (expert_few.hpp). One MI355X, rows per expert on average (a router's picks), its time against the
+// 128 x 128 tiles':
+//   64 x 1408 x 2048, bf16: 4 rows 75 to 94 us, 8 rows 85 to 99; 27 x 2048 x 7168: 4 rows 150 to 153,
+//   8 rows 178 to 154; fp32, 64 x 1408 x 2048: 8 rows 184 to 241 (split tiles 160), 32 rows 460 to 390
+//   (229). Rows that begin anywhere, 64 x 1405 x 2045: bf16 1 row 84 to 60, fp32 4 rows 203 to 244, 16
+//   rows 332 to 245 (181). 16-bit with short rows of W, 0.2 rows: 131 x 3432 x 440 18 to 25, 98 x 5872 x
+//   296 20 to 21, 244 x 4112 x 112 (224 bytes) 36 to 21, 260 x 5088 x 80 47 to 25.
 // Tiles for less than half of the CUs are bound by the latency of their stages, so it takes four
 // times the rows, but for 16-bit rows that begin anywhere; against split tiles, 8 x 1000 x 776, bf16:
-// 16 rows 5.6 to 7.4 us, 32 rows 10 to 8; fp32 (1001 x 777) 16 rows 17 to 19; bf16 8 x 1001 x 777: 8
-// rows 8.8 to 8.1; 3 x 505 x 4001: 1 row 15 to 17, 8 rows 20 to 18.
+// 16 rows 7.1 to 8.4 us, 32 rows 9.5 to 8.9; fp32 (1001 x 777) 16 rows 16.2 to 16.4; bf16 8 x 1001 x 777: 8
+// rows 9.8 to 8.9; 3 x 505 x 4001: 1 row 15 to 17, 8 rows 19 to 18.
 bool few_rows(const ExpertArgs& a, int dt, int fit) {
   const int64_t tiles = std::min<int64_t>(a.experts, a.rows) * ((a.n + 127) / 128);
   const int64_t most = (fit == CHUNK_ALIGNED ? 4 : 2) * (dt == F32 ? 2 : 1) * (int64_t)a.experts;
@@ -311,11 +312,11 @@ bool few_rows(const ExpertArgs& a, int dt, int fit) {
 // Whether a product takes 64 x 64 tiles, each split along the contraction over eight waves: where
 // they fit the CUs at once (fp32, whose MFMAs bound it: nine times that) and the contraction has
 // four stages or more. One MI355X, 128 x 128 against split tiles, bf16: 8 experts of 1000 x 776,
-// forward 64 rows (192 tiles) 15.2 to 8.6 us, 256 rows (576) 17 to 21; 3 of 504 x 4000, forward 256
-// rows (108) 54 to 19, input gradient 32 rows (189) 11.1 to 6.6, 256 rows (850) 13 to 20; 12 of 5361 x
-// 2944, 26 rows (1008) 192 to 230. fp32, 64 of 1405 x 2045, forward 16 rows (1408) 294 to 210, 64 rows
-// (2112) 407 to 419, input gradient 1 row (2112) 204 to 121. Weight gradients: 6 of 152 x 88 fp32, 1093
-// rows (36 tiles) 420 to 130 with the input's; 8 of 1001 x 777 fp32 (1664) 14 to 39.
+// forward 64 rows (192 tiles) 17.3 to 9.7 us, 256 rows (576) 20 to 22; 3 of 504 x 4000, forward 256
+// rows (108) 61 to 20, input gradient 32 rows (189) 11.7 to 7.6, 256 rows (850) 14 to 21; 12 of 5361 x
+// 2944, 26 rows (1008) 75 to 79. fp32, 64 of 1405 x 2045, forward 16 rows (1408) 245 to 183, 64 rows
+// (2112) 399 to 380, input gradient 1 row (2112) 206 to 131. Weight gradients: 6 of 152 x 88 fp32, 1093
+// rows (36 tiles) 99 to 27; 8 of 1001 x 777 fp32 (1664) 17 to 40.
 template <int MODE>
 bool split_tiles(const ExpertArgs& a, int dt) {
   const int64_t stage = 128 / dtype_size(dt);
@@ -327,12 +328,13 @@ bool split_tiles(const ExpertArgs& a, int dt) {
 
 // The kernel of a product. The 256 x 256 tiles need 16-bit types, whole 16-byte chunks everywhere,
 // extents that do not leave half of a tile empty, and enough tiles for half of the CUs. One
-// MI355X, bf16, 256 x 256 against 128 x 128 tiles: 27 experts of 2048 x 7168, 8 rows each, forward
-// 139 against 147 us, weight gradient 174 against 237; 256 rows 315 against 405, 435 against 604;
-// 64 experts of 1408 x 2048, 16 rows 103 against 97 us, weight gradient 86 against 112; 128 rows 116
-// against 137; 128 experts of 512 x 512 (264 tiles), 32 rows 19 against 17 us, 64 rows 21 against 25,
-// 512 rows 58 against 73; 8 experts of 1000 x 776 (64 tiles), 320 rows 23 against 18 us, weight
-// gradient (128 tiles) 20 against 20.
+// MI355X, bf16, rows per expert on average (a router's picks), 256 x 256 against 128 x 128 tiles: 27
+// experts of 2048 x 7168, 8 rows, forward 144 against 154 us, weight gradient 173 against 237; 256
+// rows 317 against 417, 380 against 496 (exactly 256 rows each: 218 against 318, 362 against 449); 64
+// experts of 1408 x 2048, 16 rows 100 against 100 us, weight gradient 83 against 115; 128 rows 115
+// against 132, 138 against 183; 128 experts of 512 x 512 (264 tiles), 32 rows 22 against 20 us, weight
+// gradient 20 against 22; 64 rows 24 against 22, 22 against 25; 512 rows 63 against 75; 8 experts of
+// 1000 x 776 (64 tiles), 320 rows 23 against 19 us, weight gradient (128 tiles) 17 against 15.
 template <int MODE>
 int run_product(const ExpertArgs& a, int dt, bool vec, hipStream_t s) {
   // the largest list of the smallest tiles
