@@ -342,6 +342,80 @@ MNS_API int expert_matmul_grad_input(const mns_tensor* dY, const mns_tensor* W, 
 MNS_API int expert_matmul_grad_weight(const mns_tensor* dY, const mns_tensor* X, const int32_t* offsets, const mns_tensor* dW,
                                       void* stream);
 
+/*
+ * ------------------------------------------------------------------------------------------
+ * Around the layer: the norm whose scales the hybrid optimizer's AdamW side takes, token embeddings, and that
+ * side with its states in 8 bits. The conventions of the layer's calls hold.
+ *
+ * 8-bit values: e4m3 codes (OCP FP8: largest value 448, smallest 2^-9) in blocks of 32 consecutive
+ * elements, the last one of a row or tensor shorter where its length is no multiple, and per block a byte
+ * b that stands for 2^(b - 127) (e8m0): value = code * 2^(b - 127). A block's power is the smallest
+ * that brings its largest finite magnitude to 448 or less (b = 0 for a block of zeros); infinities and
+ * NaN become NaN codes. Codes and bytes may begin at any address.
+ */
+
+/*
+ * Root-mean-square norm of every row of X (any batch), behind the residual stream's addition:
+ * H = X + R, rounded to X's dtype (R = H = NULL: H is X); rstd = 1 / sqrt(mean_cols(H^2) + eps);
+ * Y = H rstd weight. weight: device [cols] of wdtype, X's dtype or F32; NULL = 1. R, H, Y: X's batch,
+ * rows, cols and dtype. rstd: device float [batch * rows], written (the backward pass reads it, and H).
+ * H may be R's own buffer (the same address and strides): the stream is then updated in place.
+ */
+MNS_API int rms_norm(const mns_tensor* X, const mns_tensor* R, const void* weight, int32_t wdtype, float eps, const mns_tensor* Y,
+                     const mns_tensor* H, float* rstd, void* stream);
+
+/*
+ * The same with Y in 8 bits, rounded to nearest even from fp32: q: contiguous codes [batch * rows, cols],
+ * scales: contiguous bytes [batch * rows, ceil(cols / 32)]; blocks run along the columns.
+ */
+MNS_API int rms_norm_mx8(const mns_tensor* X, const mns_tensor* R, const void* weight, int32_t wdtype, float eps, uint8_t* q,
+                         uint8_t* scales, const mns_tensor* H, float* rstd, void* stream);
+
+/* Workspace bytes of rms_norm_backward for this X (host-only; only its shape is read). */
+MNS_API int mns_rms_norm_workspace_bytes(const mns_tensor* X, size_t* bytes);
+
+/*
+ * Gradients of rms_norm: with xh = H rstd and g = dY weight,
+ * dX = rstd (g - xh mean_cols(g xh)) + dH, the gradient of X and of R, and dweight = sum_rows(dY xh).
+ * dH: the gradient that reaches H along the stream, or NULL; dX may be its own buffer (the same
+ * address and strides). dweight: device [cols] of wdtype, or NULL where not wanted (the workspace is
+ * then not needed). Zero rows give dweight = 0.
+ */
+MNS_API int rms_norm_backward(const mns_tensor* dY, const mns_tensor* H, const float* rstd, const void* weight, int32_t wdtype,
+                              const mns_tensor* dH, const mns_tensor* dX, void* dweight, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Token embeddings: Y[t] = scale table[tokens[t]]; a token outside 0 .. rows - 1 (padding) gives a row of
+ * zeros. tokens: contiguous int32 or int64 (id_bytes 4 or 8), one per row of Y. table: at least one row;
+ * Y: table's cols and dtype. scale: finite.
+ */
+MNS_API int embed(const void* tokens, int32_t id_bytes, const mns_tensor* table, float scale, const mns_tensor* Y, void* stream);
+
+/* Workspace bytes of embed_backward (host-only). */
+MNS_API int mns_embed_workspace_bytes(int64_t tokens, int64_t vocab, int64_t cols, size_t* bytes);
+
+/*
+ * Its gradient, dense: dtable[v] = scale * (sum of dY[t] over the t with tokens[t] = v), zero for a token
+ * that does not occur. Sums are fp32 in an order that depends on the tokens alone.
+ */
+MNS_API int embed_backward(const mns_tensor* dY, const void* tokens, int32_t id_bytes, float scale, const mns_tensor* dtable, void* ws,
+                           size_t ws_bytes, void* stream);
+
+/*
+ * AdamW with its moments in 8 bits: exp_avg holds m, root holds r = sqrt(v), each numels[i] codes with
+ * ceil(numels[i] / 32) bytes (exp_avg_scale, root_scale); zeroed memory is the state before the first step.
+ *   m <- beta1 m + (1 - beta1) g;  r <- sqrt(beta2 r^2 + (1 - beta2) g^2);
+ *   p <- (1 - lr weight_decay) p - lr m^ / (r^ + eps),
+ * m^ = m and r^ = r, or m / (1 - beta1^step) and r / sqrt(1 - beta2^step) with bias_correction. The
+ * update takes the fp32 m and r; the states are then rounded up or down at random, in proportion, a
+ * root that is not zero to the smallest code (2^-9) at least. The random numbers depend on seed,
+ * ap->step (>= 1: count it up), the tensor's place in the list and the element's in the tensor.
+ * params and grads as for adamw_step, at most 2^34 elements a tensor; no two buffers may overlap.
+ */
+MNS_API int adamw8_step(int ntensors, void* const* params, const void* const* grads, uint8_t* const* exp_avg,
+                        uint8_t* const* exp_avg_scale, uint8_t* const* root, uint8_t* const* root_scale, const int64_t* numels,
+                        int32_t dtype, const mns_adamw_params* ap, uint64_t seed, void* stream);
+
 /* Static English text for a status code (never NULL). */
 MNS_API const char* mns_status_string(int code);
 

@@ -1,0 +1,211 @@
+// AdamW whose moments are held in 8 bits (mx8.hpp): m, and r = sqrt(v), whose range is half of v's in
+// powers of two, each as codes and one power of two per 32 elements of the flat tensor.
+//
+//   m <- beta1 m + (1 - beta1) g;  r <- sqrt(beta2 r^2 + (1 - beta2) g^2);
+//   p <- (1 - lr wd) p - lr m^ / (r^ + eps)
+//
+// The update takes m and r in fp32, before they are rounded to their codes. They are rounded up or
+// down at random, in proportion, so that a moment's mean is right: with the nearest code a change
+// below half a code's step is lost every time, and a step of e4m3 is 6 to 12 % where g = 0 moves r
+// by (1 - beta2) / 2, so moments that should decay would stand still. A root that is not zero keeps
+// the smallest code at least, so that an element that has seen a gradient never divides by eps
+// alone; m / r stays within its block's range.
+//
+// Bound by HBM: 3 elements, 4 bytes of codes and an eighth of a byte of powers per parameter (10.1 bytes
+// in bf16, 22 with moments in fp32).
+#pragma once
+
+#include "../adamw.hpp"
+#include "mx8.hpp"
+
+namespace mns {
+
+constexpr int ADAM8_MAXT = 48;                // tensors per launch (kernel-argument table)
+constexpr int ADAM8_BLOCK = 256, ADAM8_ITERS = 2;
+constexpr int ADAM8_CHUNK = ADAM8_BLOCK * 8 * ADAM8_ITERS;   // elements per workgroup
+
+struct Adam8Table {
+  void* p[ADAM8_MAXT];
+  const void* g[ADAM8_MAXT];
+  uint8_t* m[ADAM8_MAXT];
+  uint8_t* ms[ADAM8_MAXT];
+  uint8_t* r[ADAM8_MAXT];
+  uint8_t* rs[ADAM8_MAXT];
+  int64_t numel[ADAM8_MAXT];
+  int blk_start[ADAM8_MAXT + 1];              // first workgroup of each tensor
+  uint32_t key[ADAM8_MAXT];                   // of the tensor's random numbers
+  int nt;
+  float lr, beta1, beta2, eps, wd_mul;        // wd_mul = 1 - lr * weight_decay
+  float one_beta1, one_beta2;                 // 1 - beta1, 1 - beta2, rounded once
+  float bc1, bc2;                             // bias correction of m and of r (1 when off)
+};
+
+// Random bits: a number's bits mixed, which the tensor's key and an element's place go through.
+constexpr uint32_t ADAM8_MIX0 = 0xdf50e7c3u, ADAM8_MIX1 = 0x3dd219bfu, ADAM8_MIX2 = 0xafd7c8e5u;
+__host__ __device__ inline uint32_t adam8_mix(uint32_t x) {
+  x ^= x >> 16;
+  x *= ADAM8_MIX1;
+  x ^= x >> 15;
+  x *= ADAM8_MIX2;
+  return x ^ (x >> 16);
+}
+// 16 bits for m (low) and 16 for r (high) of element i.
+__device__ inline uint32_t adam8_bits(uint32_t key, int64_t i) {
+  if (i >> 32) key = adam8_mix(key ^ (uint32_t)(i >> 32));
+  return adam8_mix((uint32_t)i * ADAM8_MIX0 + key);
+}
+
+// A magnitude of at most 448 to a multiple of e4m3's step below or above it, above by the chance
+// that rnd / 2^16 is under the rest: fp32 keeps 20 bits more than e4m3, and below 2^-6 the step is 2^-9.
+__device__ inline float adam8_round(float x, uint32_t rnd) {
+  const float high = __uint_as_float((__float_as_uint(x) + (rnd << 4)) & 0xfff00000u);
+  const float low = floorf(x * 512.f + (float)rnd * 0x1p-16f) * 0x1p-9f;
+  return x < 0x1p-6f ? low : high;
+}
+
+// Eight elements' new states as codes with their block's byte: adam8_round of the scaled magnitudes.
+template <bool ROOT>
+__device__ inline u32x2 adam8_codes(const float (&v)[8], const uint32_t (&rnd)[8], int* byte) {
+  float top = 0.f, q[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) top = fmaxf(top, finite_size(v[e]));
+  *byte = mx_byte(quad_max(top));
+  const float d = mx_divisor(*byte);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float a = __builtin_fabsf(v[e]);
+    float s = adam8_round(a * d, ROOT ? rnd[e] >> 16 : rnd[e] & 0xffffu);
+    if (ROOT && a > 0.f) s = fmaxf(s, 0x1p-9f);
+    q[e] = a < __builtin_inff() ? __builtin_copysignf(s, v[e]) : __builtin_nanf("");
+  }
+  return u32x2{mx_pack(q[0], q[1], q[2], q[3]), mx_pack(q[4], q[5], q[6], q[7])};
+}
+
+__device__ inline u32x2 adam8_load(const uint8_t* p, int64_t i, int64_t n) {
+  if (i + 8 <= n) return *reinterpret_cast<const u32x2_any*>(p + i);
+  u32x2 v = {0, 0};
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (i + e < n) v[e >> 2] |= (uint32_t)p[i + e] << (8 * (e & 3));
+  return v;
+}
+__device__ inline void adam8_store(uint8_t* p, int64_t i, int64_t n, const u32x2& v) {
+  if (i + 8 <= n) {
+    *reinterpret_cast<u32x2_any*>(p + i) = v;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (i + e < n) p[i + e] = (uint8_t)(v[e >> 2] >> (8 * (e & 3)));
+  }
+}
+
+// Eight elements at any element's address.
+template <typename T>
+struct Adam8Vec {
+  static constexpr int N = 16 / (int)sizeof(T), L = 8 / N;
+  u32x4 v[L];
+  __device__ inline void load(const T* p, int64_t i, int64_t n) {
+    if (i + 8 <= n) {
+#pragma unroll
+      for (int l = 0; l < L; ++l) v[l] = *reinterpret_cast<const u32x4_any*>(p + i + l * N);
+    } else {
+      typedef T TN __attribute__((ext_vector_type(N)));
+#pragma unroll
+      for (int l = 0; l < L; ++l) {
+        TN s;
+#pragma unroll
+        for (int e = 0; e < N; ++e) s[e] = i + l * N + e < n ? p[i + l * N + e] : (T)0.f;
+        v[l] = __builtin_bit_cast(u32x4, s);
+      }
+    }
+  }
+  __device__ inline void unpack(float (&f)[8]) const {
+    if constexpr (L == 1) VecIO<T>::unpack(v[0], f);
+    else
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[e >> 2][e & 3]);
+  }
+  static __device__ inline void store(T* p, int64_t i, int64_t n, const float (&f)[8]) {
+    if (i + 8 <= n) {
+      if constexpr (L == 1) {
+        *reinterpret_cast<u32x4_any*>(p + i) = u32x4{pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7])};
+      } else {
+#pragma unroll
+        for (int l = 0; l < 2; ++l)
+          *reinterpret_cast<u32x4_any*>(p + i + 4 * l) =
+              u32x4{__float_as_uint(f[4 * l]), __float_as_uint(f[4 * l + 1]), __float_as_uint(f[4 * l + 2]), __float_as_uint(f[4 * l + 3])};
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (i + e < n) p[i + e] = from_f32<T>(f[e]);
+    }
+  }
+};
+
+template <typename T>
+__global__ void __launch_bounds__(ADAM8_BLOCK) adamw8_kernel(const Adam8Table t) {
+  int ti = 0;
+  while (ti + 1 < t.nt && (int)blockIdx.x >= t.blk_start[ti + 1]) ++ti;
+  const int64_t n = t.numel[ti];
+  const int64_t base = (int64_t)((int)blockIdx.x - t.blk_start[ti]) * ADAM8_CHUNK;
+  T* p = reinterpret_cast<T*>(t.p[ti]);
+  const T* g = reinterpret_cast<const T*>(t.g[ti]);
+  uint8_t* m = t.m[ti];
+  uint8_t* r = t.r[ti];
+  // all loads of the thread first, then the arithmetic
+  Adam8Vec<T> pv[ADAM8_ITERS], gv[ADAM8_ITERS];
+  u32x2 mc[ADAM8_ITERS], rc[ADAM8_ITERS];
+  int mb[ADAM8_ITERS], rb[ADAM8_ITERS];
+#pragma unroll
+  for (int it = 0; it < ADAM8_ITERS; ++it) {
+    const int64_t i = base + ((int64_t)it * ADAM8_BLOCK + threadIdx.x) * 8;
+    if (i >= n) continue;
+    pv[it].load(p, i, n);
+    gv[it].load(g, i, n);
+    mc[it] = adam8_load(m, i, n);
+    rc[it] = adam8_load(r, i, n);
+    mb[it] = t.ms[ti][i / MX_BLOCK];
+    rb[it] = t.rs[ti][i / MX_BLOCK];
+  }
+#pragma unroll
+  for (int it = 0; it < ADAM8_ITERS; ++it) {
+    const int64_t i = base + ((int64_t)it * ADAM8_BLOCK + threadIdx.x) * 8;
+    const bool in = i < n;
+    float pf[8], mf[8], rf[8];
+    uint32_t rnd[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) pf[e] = mf[e] = rf[e] = 0.f;
+    if (in) {
+      float gf[8];
+      pv[it].unpack(pf);
+      gv[it].unpack(gf);
+      mx_values(mc[it], mx_factor(mb[it]), mf);
+      mx_values(rc[it], mx_factor(rb[it]), rf);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        mf[e] = t.beta1 * mf[e] + t.one_beta1 * gf[e];
+        rf[e] = __builtin_sqrtf(t.beta2 * (rf[e] * rf[e]) + t.one_beta2 * (gf[e] * gf[e]));
+        pf[e] = t.wd_mul * pf[e] - t.lr * ((mf[e] * t.bc1) / (rf[e] * t.bc2 + t.eps));
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      rnd[e] = adam8_bits(t.key[ti], i + e);
+      if (i + e >= n) mf[e] = rf[e] = 0.f;   // behind the end nothing counts for the block
+    }
+    // the quads' lanes meet here, those behind the end with zeros
+    int bm, br;
+    const u32x2 cm = adam8_codes<false>(mf, rnd, &bm), cr = adam8_codes<true>(rf, rnd, &br);
+    if (!in) continue;
+    Adam8Vec<T>::store(p, i, n, pf);
+    adam8_store(m, i, n, cm);
+    adam8_store(r, i, n, cr);
+    if (i % MX_BLOCK == 0) {
+      t.ms[ti][i / MX_BLOCK] = (uint8_t)bm;
+      t.rs[ti][i / MX_BLOCK] = (uint8_t)br;
+    }
+  }
+}
+
+}  // namespace mns

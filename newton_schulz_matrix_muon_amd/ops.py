@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional, Sequence
+from typing import NamedTuple, Optional, Sequence
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libmuon_ns.so")
@@ -107,6 +107,14 @@ def declare(lib):
         "expert_matmul": [t, t, vp, t, vp],
         "expert_matmul_grad_input": [t, t, vp, t, vp],
         "expert_matmul_grad_weight": [t, t, vp, t, vp],
+        "rms_norm": [t, t, vp, i32, ctypes.c_float, t, t, vp, vp],
+        "rms_norm_mx8": [t, t, vp, i32, ctypes.c_float, vp, vp, t, vp, vp],
+        "mns_rms_norm_workspace_bytes": [t, P(sz)],
+        "rms_norm_backward": [t, t, vp, vp, i32, t, t, vp, vp, sz, vp],
+        "embed": [vp, i32, t, ctypes.c_float, t, vp],
+        "mns_embed_workspace_bytes": [i64, i64, i64, P(sz)],
+        "embed_backward": [t, vp, i32, ctypes.c_float, t, vp, sz, vp],
+        "adamw8_step": [ctypes.c_int, pp, pp, pp, pp, pp, pp, P(i64), i32, P(MnsAdamwParams), ctypes.c_uint64, vp],
     }
     for name, argtypes in layer.items():
         fn = getattr(lib, name)
@@ -510,16 +518,95 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, *, lr: float, beta1: float 
     return params
 
 
-def hybrid_step(matrix_groups, vector_params, *, muon: dict, adamw: dict):
+MX_BLOCK = 32   # elements that share a power of two in 8-bit values
+
+
+class Adamw8State(NamedTuple):
+    """Moments of one parameter in 8 bits: m and r = sqrt(v) as float8_e4m3fn codes (flat, one per element)
+    with float8_e8m0fnu powers of two (one per 32 elements); a value is code * power."""
+    exp_avg: object
+    exp_avg_scale: object
+    root: object
+    root_scale: object
+
+
+def adamw8_state(param) -> Adamw8State:
+    """The state of a parameter before its first step (all zero)."""
+    torch = _torch()
+    n = param.numel()
+    zeros = lambda count, dtype: torch.zeros(count, dtype=torch.uint8, device=param.device).view(dtype)
+    blocks = (n + MX_BLOCK - 1) // MX_BLOCK
+    return Adamw8State(zeros(n, torch.float8_e4m3fn), zeros(blocks, torch.float8_e8m0fnu),
+                       zeros(n, torch.float8_e4m3fn), zeros(blocks, torch.float8_e8m0fnu))
+
+
+def adamw8_step(params, grads, states, *, lr: float, step: int, beta1: float = 0.9, beta2: float = 0.95, eps: float = 1e-8,
+                weight_decay: float = 0.1, bias_correction: bool = False, seed: int = 0):
+    """One AdamW step over lists of contiguous tensors with their moments in 8 bits (C ABI ``adamw8_step``);
+    params and states (adamw8_state's, or tuples like it) are updated in place. The states are rounded at
+    random: the numbers depend on seed, step (count it up), a tensor's place in the list and the element's."""
+    torch = _torch()
+    what = "adamw8_step"
+    n = len(params)
+    if not (len(grads) == len(states) == n) or n == 0:
+        raise ValueError(f"{what}: params, grads and states must be non-empty lists of equal length")
+    if not 1 <= step < 2 ** 31:
+        raise ValueError(f"{what}: step must count from 1, got {step}")
+    if not 0 <= seed < 2 ** 64:
+        raise ValueError(f"{what}: seed must fit 64 bits, got {seed}")
+    pdt = params[0].dtype
+    code = dtype_code(params[0])
+    codes, scales = (torch.float8_e4m3fn, torch.uint8), (torch.float8_e8m0fnu, torch.uint8)
+    device = params[0].device
+    for i, (p_, g_, s_) in enumerate(zip(params, grads, states)):
+        if p_.dtype != pdt:
+            raise TypeError(f"{what}: params[{i}] is {p_.dtype}; every parameter must be {pdt}")
+        if g_.dtype != pdt:
+            raise TypeError(f"{what}: grads[{i}] is {g_.dtype}, its parameter is {pdt}")
+        numel = p_.numel()
+        if g_.numel() != numel:
+            raise ValueError(f"{what}: grads[{i}] has {g_.numel()} elements, its parameter {numel}")
+        if len(s_) != 4:
+            raise ValueError(f"{what}: states[{i}] must hold four tensors, got {len(s_)}")
+        blocks = (numel + MX_BLOCK - 1) // MX_BLOCK
+        for t_, allowed, want in zip(s_, (codes, scales, codes, scales), (numel, blocks, numel, blocks)):
+            if t_.dtype not in allowed:
+                raise TypeError(f"{what}: a tensor of states[{i}] is {t_.dtype}, expected {allowed[0]}")
+            if t_.numel() != want:
+                raise ValueError(f"{what}: a tensor of states[{i}] has {t_.numel()} elements, expected {want}")
+        for t_ in (p_, g_, *s_):
+            if not t_.is_contiguous():
+                raise ValueError(f"{what}: the tensors must be contiguous")
+    if not params[0].is_cuda:
+        raise ValueError(f"{what}: tensors must be device tensors (got {device})")
+    for i, (p_, g_, s_) in enumerate(zip(params, grads, states)):
+        for t_ in (p_, g_, *s_):
+            if t_.device != device:
+                raise ValueError(f"{what}: a tensor of params, grads or states[{i}] is on {t_.device}, expected {device}")
+    arr = lambda ts: (ctypes.c_void_p * n)(*[t.data_ptr() for t in ts])
+    numels = (ctypes.c_int64 * n)(*[t.numel() for t in params])
+    ap = MnsAdamwParams(lr, beta1, beta2, eps, weight_decay, step, 1 if bias_correction else 0)
+    _launch(what, params[0], n, arr(params), arr(grads), *(arr(ts) for ts in zip(*states)), numels, code, ctypes.byref(ap), seed)
+    return params
+
+
+def hybrid_step(matrix_groups, vector_params, *, muon: dict, adamw: dict, seed: int = 0):
     """The hybrid optimizer step: Muon for the 2-D matrices (``matrix_groups``: list of
     (W, G, M) batches, one grouped call) and AdamW for everything else (``vector_params``:
-    list of (param, grad, exp_avg, exp_avg_sq)), enqueued on the current stream."""
+    list of (param, grad, exp_avg, exp_avg_sq), or (param, grad, adamw8_state(param)) where the
+    moments are held in 8 bits; those need ``step`` in ``adamw`` and take ``seed``), enqueued on the
+    current stream."""
     if matrix_groups:
         Ws, Gs, Ms = (list(x) for x in zip(*matrix_groups))
         muon_step_grouped(Ws, Gs, Ms, **muon)
-    if vector_params:
-        ps, gs, ms, vs = (list(x) for x in zip(*vector_params))
+    in32 = [v for v in vector_params or () if len(v) == 4]
+    in8 = [v for v in vector_params or () if len(v) != 4]
+    if in32:
+        ps, gs, ms, vs = (list(x) for x in zip(*in32))
         adamw_step(ps, gs, ms, vs, **adamw)
+    if in8:
+        ps, gs, ss = (list(x) for x in zip(*in8))
+        adamw8_step(ps, gs, ss, seed=seed, **adamw)
 
 
 # ------------------------------------------------------------------ the layer around the experts
@@ -854,6 +941,152 @@ def expert_matmul_backward(dy, x, w, offsets):
     _launch("expert_matmul_grad_input", dy, dyd, describe(w), at, describe(dx))
     _launch("expert_matmul_grad_weight", dy, dyd, xd, at, describe(dw))
     return dx, dw
+
+
+# ------------------------------------------------------------------ around the layer
+# The norm and the embeddings of the model that the layer belongs to; the conventions are the layer's.
+
+def _check_scale_vector(what, x, weight):
+    torch = _torch()
+    _check_flat(what, x, (x.dtype, torch.float32), weight=weight)
+    if weight is not None:
+        _check_shape(what, "weight", weight, x.shape[-1:])
+    return F32 if weight is None else dtype_code(weight)
+
+
+def _check_like(what, x, **named):
+    """Buffers of x's shape and dtype."""
+    _check_same_shape(what, x, **named)
+    for name, t in named.items():
+        if t is not None and t.dtype != x.dtype:
+            raise TypeError(f"{what}: {name} is {t.dtype}, expected {x.dtype}")
+
+
+def _rms_forward(what, x, weight, residual, residual_out, **more):
+    _check_recorded(what, x, weight, residual, residual_out, *more.values())
+    xd = describe(x)
+    code = _check_scale_vector(what, x, weight)
+    if residual is None and residual_out is not None:
+        raise ValueError(f"{what}: residual_out without residual")
+    _check_like(what, x, residual=residual, residual_out=residual_out, out=more.get("out"))
+    _check_device(what, x, weight=weight, residual=residual, residual_out=residual_out, **more)
+    h = x if residual is None else x.new_empty(x.shape) if residual_out is None else residual_out
+    rstd = x.new_empty(x.shape[:-1], dtype=_torch().float32)
+    return xd, code, h, rstd
+
+
+def rms_norm(x, weight=None, *, residual=None, eps: float = 1e-6, out=None, residual_out=None):
+    """(y, h, rstd): h = x + residual in x's dtype (h is x without a residual) and its root-mean-square
+    norm over the columns, y = h * rstd * weight (C ABI ``rms_norm``). x: [rows, cols] or [batch, rows,
+    cols]; weight: [cols] of x's dtype or float32; rstd: float32, one per row. residual_out may be
+    residual itself: the stream is then updated in place."""
+    what = "rms_norm"
+    xd, code, h, rstd = _rms_forward(what, x, weight, residual, residual_out, out=out)
+    y = x.new_empty(x.shape) if out is None else out
+    kept = residual is not None
+    _launch(what, x, xd, describe(residual) if kept else None, _ptr(weight), code, eps, describe(y), describe(h) if kept else None, _ptr(rstd))
+    return y, h, rstd
+
+
+def rms_norm_mx8(x, weight=None, *, residual=None, eps: float = 1e-6, residual_out=None):
+    """(q, scales, h, rstd): rms_norm with its output in 8 bits (C ABI ``rms_norm_mx8``): q float8_e4m3fn of
+    x's shape, scales float8_e8m0fnu, one power of two per 32 columns; y = q * scales."""
+    torch = _torch()
+    what = "rms_norm_mx8"
+    xd, code, h, rstd = _rms_forward(what, x, weight, residual, residual_out)
+    q = x.new_empty(x.shape, dtype=torch.float8_e4m3fn)
+    scales = x.new_empty((*x.shape[:-1], (x.shape[-1] + MX_BLOCK - 1) // MX_BLOCK), dtype=torch.float8_e8m0fnu)
+    kept = residual is not None
+    _launch(what, x, xd, describe(residual) if kept else None, _ptr(weight), code, eps, _ptr(q), _ptr(scales),
+            describe(h) if kept else None, _ptr(rstd))
+    return q, scales, h, rstd
+
+
+def rms_norm_workspace_bytes(x) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib().mns_rms_norm_workspace_bytes(ctypes.byref(describe(x)), ctypes.byref(n)), "mns_rms_norm_workspace_bytes")
+    return n.value
+
+
+def rms_norm_backward(dy, h, rstd, weight=None, *, dh=None, param_grads: bool = True, out=None, workspace=None):
+    """(dx, dweight) of rms_norm (C ABI ``rms_norm_backward``): dx is the gradient of x and of residual, dh
+    (the gradient that reaches h along the stream) included. out may be dh itself. dweight has weight's
+    dtype; it is None without weight or with param_grads=False."""
+    torch = _torch()
+    what = "rms_norm_backward"
+    _check_recorded(what, dy, h, rstd, weight, dh, out)
+    hd = describe(h)
+    _check_like(what, h, dy=dy, dh=dh, out=out)
+    _check_flat(what, h, (torch.float32,), rstd=rstd)
+    _check_shape(what, "rstd", rstd, h.shape[:-1])
+    code = _check_scale_vector(what, h, weight)
+    _check_workspace(what, workspace)
+    _check_device(what, h, dy=dy, rstd=rstd, weight=weight, dh=dh, out=out, workspace=workspace)
+    dx = h.new_empty(h.shape) if out is None else out
+    dw = None
+    if weight is not None and param_grads:
+        dw = torch.empty_like(weight)
+        if workspace is None:
+            workspace = torch.empty(rms_norm_workspace_bytes(h), dtype=torch.uint8, device=h.device)
+    _launch(what, h, describe(dy), hd, _ptr(rstd), _ptr(weight), code, None if dh is None else describe(dh), describe(dx), _ptr(dw),
+            _ptr(workspace), 0 if workspace is None else _ws_bytes(workspace))
+    return dx, dw
+
+
+def _check_tokens(what, tokens):
+    torch = _torch()
+    _check_flat(what, tokens, (torch.int32, torch.int64), tokens=tokens)
+
+
+def embed(tokens, table, *, scale: float = 1.0, out=None):
+    """scale * table[tokens], a row of zeros for a token outside 0 .. rows - 1 (C ABI ``embed``). tokens: int32
+    or int64, any shape; table: [rows, cols]; the result: [*tokens.shape, cols] (out: [tokens, cols])."""
+    what = "embed"
+    _check_recorded(what, table, out)
+    _check_tokens(what, tokens)
+    _check_rows(what, table, table=table, out=out)
+    if table.shape[0] < 1:
+        raise ValueError(f"{what}: table has no rows")
+    if out is not None:
+        _check_shape(what, "out", out, (tokens.numel(), table.shape[1]))
+    _check_device(what, table, tokens=tokens, out=out)
+    y = table.new_empty((tokens.numel(), table.shape[1])) if out is None else out
+    _launch(what, table, _ptr(tokens), tokens.element_size(), describe(table), scale, describe(y))
+    return y.view(*tokens.shape, table.shape[1]) if out is None else y
+
+
+def embed_workspace_bytes(tokens: int, rows: int, cols: int) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib().mns_embed_workspace_bytes(tokens, rows, cols, ctypes.byref(n)), "mns_embed_workspace_bytes")
+    return n.value
+
+
+def embed_backward(dy, tokens, rows: int, *, scale: float = 1.0, out=None, workspace=None):
+    """The dense gradient of embed's table, [rows, cols] of dy's dtype: scale times the sum of dy's rows of each
+    token, zero for a token that does not occur (C ABI ``embed_backward``). dy: [tokens, cols], or
+    contiguous [*tokens.shape, cols]."""
+    torch = _torch()
+    what = "embed_backward"
+    _check_recorded(what, dy, out)
+    _check_tokens(what, tokens)
+    if dy.dim() != 2 and dy.shape[:-1] == tokens.shape:
+        if not dy.is_contiguous():
+            raise ValueError(f"{what}: dy of more than two dimensions must be contiguous")
+        dy = dy.view(tokens.numel(), dy.shape[-1])
+    _check_rows(what, dy, dy=dy, out=out)
+    _check_shape(what, "dy", dy, (tokens.numel(), dy.shape[1]))
+    if rows < 1:
+        raise ValueError(f"{what}: rows must be at least 1, got {rows}")
+    if out is not None:
+        _check_shape(what, "out", out, (rows, dy.shape[1]))
+    _check_workspace(what, workspace)
+    _check_device(what, dy, tokens=tokens, out=out, workspace=workspace)
+    need = embed_workspace_bytes(tokens.numel(), rows, dy.shape[1])
+    dt = dy.new_empty((rows, dy.shape[1])) if out is None else out
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dy.device)
+    _launch(what, dy, describe(dy), _ptr(tokens), tokens.element_size(), scale, describe(dt), _ptr(workspace), _ws_bytes(workspace))
+    return dt
 
 
 def gram_trace(G, *, steps: int = DEFAULT_STEPS, coeffs=None, eps: float = DEFAULT_EPS,
