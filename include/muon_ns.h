@@ -408,13 +408,49 @@ MNS_API int embed_backward(const mns_tensor* dY, const void* tokens, int32_t id_
  *   p <- (1 - lr weight_decay) p - lr m^ / (r^ + eps),
  * m^ = m and r^ = r, or m / (1 - beta1^step) and r / sqrt(1 - beta2^step) with bias_correction. The
  * update takes the fp32 m and r; the states are then rounded up or down at random, in proportion, a
- * root that is not zero to the smallest code (2^-9) at least. The random numbers depend on seed,
- * ap->step (>= 1: count it up), the tensor's place in the list and the element's in the tensor.
- * params and grads as for adamw_step, at most 2^34 elements a tensor; no two buffers may overlap.
+ * root that is not zero to the smallest code (2^-9) at least. The random numbers depend on ap->seed,
+ * ap->step (count it up), the tensor's place in the list and the element's in the tensor.
+ * params and grads as for adamw_step, at most 2^34 elements a tensor; no two buffers may overlap. The
+ * hyper-parameters are doubles: 1 - beta is rounded to fp32 once.
  */
+typedef struct mns_adamw8_params {
+  double lr, beta1, beta2, eps, weight_decay;
+  int32_t step;             /* >= 1 */
+  int32_t bias_correction;  /* 0 or 1 */
+  uint64_t seed;
+} mns_adamw8_params;
 MNS_API int adamw8_step(int ntensors, void* const* params, const void* const* grads, uint8_t* const* exp_avg,
                         uint8_t* const* exp_avg_scale, uint8_t* const* root, uint8_t* const* root_scale, const int64_t* numels,
-                        int32_t dtype, const mns_adamw_params* ap, uint64_t seed, void* stream);
+                        int32_t dtype, const mns_adamw8_params* ap, void* stream);
+
+/*
+ * The gated block of the experts (or of a dense layer, see offsets): both projections, the activation and the
+ * product in one kernel.
+ *   gate = X Wg[e]^T,  up = X Wu[e]^T,  H = act(gate) * up    X: S x K, H, G, U: S x N, row s of expert e
+ * Wg, Wu: batches of E matrices N x K (the Muon step's layout). G, U: receive gate and up for the backward
+ * pass, or both NULL. All of one dtype; the activation takes fp32 sums. offsets as in expert_matmul; NULL with
+ * E = 1: every row is the one expert's. Rows of no expert get zeros.
+ *   MNS_ACT_SILU  g / (1 + exp(-g));  MNS_ACT_GELU  g (1 + erf(g / sqrt(2))) / 2;  MNS_ACT_RELU  max(g, 0)
+ */
+#define MNS_ACT_SILU 0
+#define MNS_ACT_GELU 1
+#define MNS_ACT_RELU 2
+MNS_API int expert_gated(const mns_tensor* X, const mns_tensor* Wg, const mns_tensor* Wu, const int32_t* offsets, int32_t act,
+                         const mns_tensor* H, const mns_tensor* G, const mns_tensor* U, void* stream);
+
+/* Workspace bytes of expert_gated_backward (host-only). */
+MNS_API int mns_expert_gated_workspace_bytes(int64_t rows, int64_t inner, int32_t dtype, size_t* bytes);
+
+/*
+ * Its gradients, from gate and up as kept: dgate = dH * up * act'(gate), dup = dH * act(gate), rounded to the
+ * rows' dtype in the workspace (relu's slope at 0 is 0);
+ *   dX = dgate Wg[e] + dup Wu[e],  dWg[e] = sum_s dgate[s] X[s]^T,  dWu[e] = sum_s dup[s] X[s]^T.
+ * dX, or both dWg and dWu, may be NULL where not wanted. Rows of no expert are not read and get zeros in
+ * dX; an expert without rows gets zeros.
+ */
+MNS_API int expert_gated_backward(const mns_tensor* dH, const mns_tensor* X, const mns_tensor* Wg, const mns_tensor* Wu,
+                                  const mns_tensor* G, const mns_tensor* U, const int32_t* offsets, int32_t act, const mns_tensor* dX,
+                                  const mns_tensor* dWg, const mns_tensor* dWu, void* ws, size_t ws_bytes, void* stream);
 
 /* Static English text for a status code (never NULL). */
 MNS_API const char* mns_status_string(int code);

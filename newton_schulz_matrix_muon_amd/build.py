@@ -13,7 +13,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libmuon_ns.so")
-SOURCES = ["muon_ns.hip", os.path.join("layer", "layer.hip"), os.path.join("layer", "block.hip")]
+SOURCES = ["muon_ns.hip", os.path.join("layer", "layer.hip"), os.path.join("layer", "block.hip"),
+           os.path.join("layer", "gated.hip")]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",

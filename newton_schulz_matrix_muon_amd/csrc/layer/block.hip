@@ -150,18 +150,18 @@ EmbedPlan embed_plan(int64_t n, int64_t vocab, int64_t cols) {
 // ------------------------------------------------------------------------------------ AdamW
 
 int run_adamw8(int nt, void* const* params, const void* const* grads, uint8_t* const* m, uint8_t* const* ms, uint8_t* const* r,
-               uint8_t* const* rs, const int64_t* numels, int dt, const mns_adamw_params* ap, uint64_t seed, hipStream_t s) {
+               uint8_t* const* rs, const int64_t* numels, int dt, const mns_adamw8_params* ap, hipStream_t s) {
   Adam8Table t;
-  t.lr = ap->lr;
-  t.beta1 = ap->beta1;
-  t.beta2 = ap->beta2;
-  t.one_beta1 = (float)(1.0 - (double)ap->beta1);
-  t.one_beta2 = (float)(1.0 - (double)ap->beta2);
-  t.eps = ap->eps;
-  t.wd_mul = (float)(1.0 - (double)ap->lr * (double)ap->weight_decay);
-  t.bc1 = ap->bias_correction ? (float)(1.0 / (1.0 - std::pow((double)ap->beta1, ap->step))) : 1.f;
-  t.bc2 = ap->bias_correction ? (float)std::sqrt(1.0 / (1.0 - std::pow((double)ap->beta2, ap->step))) : 1.f;
-  const uint32_t key = adam8_mix(adam8_mix(adam8_mix((uint32_t)seed) ^ (uint32_t)(seed >> 32)) ^ (uint32_t)ap->step);
+  t.lr = (float)ap->lr;
+  t.beta1 = (float)ap->beta1;
+  t.beta2 = (float)ap->beta2;
+  t.one_beta1 = (float)(1.0 - ap->beta1);
+  t.one_beta2 = (float)(1.0 - ap->beta2);
+  t.eps = (float)ap->eps;
+  t.wd_mul = (float)(1.0 - ap->lr * ap->weight_decay);
+  t.bc1 = ap->bias_correction ? (float)(1.0 / (1.0 - std::pow(ap->beta1, ap->step))) : 1.f;
+  t.bc2 = ap->bias_correction ? (float)std::sqrt(1.0 / (1.0 - std::pow(ap->beta2, ap->step))) : 1.f;
+  const uint32_t key = adam8_mix(adam8_mix(adam8_mix((uint32_t)ap->seed) ^ (uint32_t)(ap->seed >> 32)) ^ (uint32_t)ap->step);
   int i = 0;
   while (i < nt) {
     int k = 0;
@@ -405,13 +405,13 @@ int embed_backward(const mns_tensor* dY, const void* tokens, int32_t id_bytes, f
 }
 
 int adamw8_step(int ntensors, void* const* params, const void* const* grads, uint8_t* const* exp_avg, uint8_t* const* exp_avg_scale,
-                uint8_t* const* root, uint8_t* const* root_scale, const int64_t* numels, int32_t dtype, const mns_adamw_params* ap,
-                uint64_t seed, void* stream) {
+                uint8_t* const* root, uint8_t* const* root_scale, const int64_t* numels, int32_t dtype, const mns_adamw8_params* ap,
+                void* stream) {
   if (ntensors < 1 || !params || !grads || !exp_avg || !exp_avg_scale || !root || !root_scale || !numels || !ap) return MNS_ERR_ARG;
   if (!valid_dtype(dtype)) return MNS_ERR_DTYPE;
-  for (float x : {ap->lr, ap->beta1, ap->beta2, ap->eps, ap->weight_decay})
-    if (!std::isfinite(x)) return MNS_ERR_ARG;
-  if (ap->beta1 < 0.f || ap->beta1 >= 1.f || ap->beta2 < 0.f || ap->beta2 >= 1.f || ap->eps < 0.f) return MNS_ERR_ARG;
+  for (double x : {ap->lr, ap->beta1, ap->beta2, ap->eps, ap->weight_decay})
+    if (!std::isfinite((float)x)) return MNS_ERR_ARG;
+  if (ap->beta1 < 0. || ap->beta1 >= 1. || ap->beta2 < 0. || ap->beta2 >= 1. || ap->eps < 0.) return MNS_ERR_ARG;
   if ((ap->bias_correction != 0 && ap->bias_correction != 1) || ap->step < 1) return MNS_ERR_ARG;
   // every buffer there (unless empty) and aligned to its elements, no two of them overlapping
   std::vector<std::pair<uintptr_t, uintptr_t>> iv;
@@ -432,7 +432,7 @@ int adamw8_step(int ntensors, void* const* params, const void* const* grads, uin
   std::sort(iv.begin(), iv.end());
   for (size_t k = 1; k < iv.size(); ++k)
     if (iv[k].first < iv[k - 1].second) return MNS_ERR_ARG;
-  return run_adamw8(ntensors, params, grads, exp_avg, exp_avg_scale, root, root_scale, numels, dtype, ap, seed, as_stream(stream));
+  return run_adamw8(ntensors, params, grads, exp_avg, exp_avg_scale, root, root_scale, numels, dtype, ap, as_stream(stream));
 }
 
 }  // extern "C"

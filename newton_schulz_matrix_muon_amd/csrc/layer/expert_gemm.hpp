@@ -28,8 +28,11 @@ namespace mns {
 
 constexpr int EXPERT_MAX = 1024;
 
-// Which product: forward, input gradient, weight gradient.
-enum { EX_FWD = 0, EX_DX = 1, EX_DW = 2 };
+// Which product: forward, input gradient, weight gradient; the same of two matrices side by side (gated.hpp).
+enum { EX_FWD = 0, EX_DX = 1, EX_DW = 2, EX_GATE = 3, EX_DX2 = 4, EX_DW2 = 5 };
+__host__ __device__ constexpr bool ex_fwd(int mode) { return mode == EX_FWD || mode == EX_GATE; }
+__host__ __device__ constexpr bool ex_dx(int mode) { return mode == EX_DX || mode == EX_DX2; }
+__host__ __device__ constexpr bool ex_dw(int mode) { return mode == EX_DW || mode == EX_DW2; }
 
 struct ExpertArgs {
   const char* A; int64_t lda;       // elements
@@ -44,9 +47,40 @@ struct ExpertArgs {
   int c_vec;                        // 16-byte stores fit C
 };
 
-// Beginning and end of expert e's rows; e = E: the rows of nobody.
+// Two matrices W and W2 per expert over the same rows.
+//   EX_GATE  C = act(A B^T) * (A B2^T), and the two products to C2 and C3 where they are kept
+//   EX_DX2   C = A B + A2 B2
+//   EX_DW2   C = A^T B, C2 = A2^T B
+// A tile of EX_GATE holds blocks of 32 columns of W and W2 in turn, so that a wave has both products
+// of its columns; EX_DX2's contraction runs over A and B, then over A2 and B2; EX_DW2 takes C and
+// C2 as the results of two experts.
+struct GatedArgs : ExpertArgs {
+  const char* A2;                   // rows like A's
+  const char* B2; int64_t ldb2, sB2;
+  char* C2; int64_t ldc2, sC2;
+  char* C3; int64_t ldc3;
+  int act;
+};
+enum { ACT_SILU = 0, ACT_GELU = 1, ACT_RELU = 2 };
+template <int MODE> struct ArgsOf { typedef ExpertArgs type; };
+template <> struct ArgsOf<EX_GATE> { typedef GatedArgs type; };
+template <> struct ArgsOf<EX_DX2> { typedef GatedArgs type; };
+template <> struct ArgsOf<EX_DW2> { typedef GatedArgs type; };
+
+// Columns of C that a tile of BN columns of B makes.
+template <int MODE, class CFG> constexpr int tile_cols() { return MODE == EX_GATE ? CFG::BN / 2 : CFG::BN; }
+// Matrices that the weight gradient's tiles belong to.
+template <int MODE> __host__ __device__ inline int dw_matrices(const ExpertArgs& p) { return MODE == EX_DW2 ? 2 * p.experts : p.experts; }
+
+// Beginning and end of expert e's rows; e = E: the rows of nobody. No offsets: one expert has all rows.
 __host__ __device__ inline void expert_rows(const ExpertArgs& p, int e, int* lo, int* hi) {
-  const int rows = (int)p.rows, a = p.offsets[e], b = e < p.experts ? p.offsets[e + 1] : rows;
+  const int rows = (int)p.rows;
+  if (!p.offsets) {
+    *lo = e < p.experts ? 0 : rows;
+    *hi = rows;
+    return;
+  }
+  const int a = p.offsets[e], b = e < p.experts ? p.offsets[e + 1] : rows;
   *lo = min(max(a, 0), rows);
   *hi = min(max(b, *lo), rows);
 }
@@ -118,6 +152,9 @@ struct ExpertTile {
   int m, k;               // rows of the expert's result, contraction length
   const char* a; const char* b;
   char* c;
+  const char* a2; const char* b2;   // EX_GATE, EX_DX2
+  char* c2; char* c3;               // EX_GATE
+  int64_t ldc;                      // EX_DW2
 };
 
 // 16 bytes at any element's address
@@ -163,7 +200,7 @@ struct ExpertList {
 template <int MODE, class CFG>
 __device__ inline ExpertList expert_list(const ExpertArgs& p, const int* first) {
   // below 2^31: a weight gradient's by the host's check, the others' also by list_rows
-  const int64_t total = (int64_t)p.tiles_n * (MODE == EX_DW ? p.experts * ((p.m + CFG::BM - 1) / CFG::BM) : wave_uniform(first[p.experts + 1]));
+  const int64_t total = (int64_t)p.tiles_n * (ex_dw(MODE) ? dw_matrices<MODE>(p) * ((p.m + CFG::BM - 1) / CFG::BM) : wave_uniform(first[p.experts + 1]));
   const int xcd = blockIdx.x & 7;
   const int lo = (int)(total * xcd / 8);
   return {wave_uniform(lo), wave_uniform((int)(total * (xcd + 1) / 8) - lo)};
@@ -173,16 +210,21 @@ __device__ inline ExpertList expert_list(const ExpertArgs& p, const int* first) 
 // tiles that run together share panels of both operands in L2. *from: the expert of the tile
 // before, or 0. rows (ROWS): as expert_tiles left them.
 template <int MODE, typename T, class CFG, bool ROWS = false>
-__device__ inline ExpertTile expert_tile(const ExpertArgs& p, const int* first, const ExpertList& l, int t, int* from,
+__device__ inline ExpertTile expert_tile(const typename ArgsOf<MODE>::type& p, const int* first, const ExpertList& l, int t, int* from,
                                          const int2* rows = nullptr) {
   t += l.lo;
   constexpr int ES = sizeof(T);
   ExpertTile x;
   int e, r, tm;
-  if constexpr (MODE == EX_DW) {
+  bool second = false;
+  if constexpr (ex_dw(MODE)) {
     tm = (p.m + CFG::BM - 1) / CFG::BM;
     e = t / (tm * p.tiles_n);
     r = t - e * tm * p.tiles_n;
+    if constexpr (MODE == EX_DW2) {
+      second = e & 1;
+      e >>= 1;
+    }
   } else {
     // the expert whose tiles hold t: the last tile's, or as many as end at or before t
     e = *from;
@@ -208,20 +250,40 @@ __device__ inline ExpertTile expert_tile(const ExpertArgs& p, const int* first, 
   hi = wave_uniform(hi);
   const TileAt at = tile_at(r, tm, p.tiles_n);
   x.row0 = at.row * CFG::BM;
-  x.col0 = at.col * CFG::BN;
+  x.col0 = at.col * tile_cols<MODE, CFG>();
   x.a = p.A + (int64_t)lo * p.lda * ES;
-  if constexpr (MODE == EX_DW) {
+  if constexpr (ex_dw(MODE)) {
     x.m = p.m;
     x.k = hi - lo;
     x.b = p.B + (int64_t)lo * p.ldb * ES;
     x.c = p.C + (int64_t)e * p.sC * ES;
+    if constexpr (MODE == EX_DW2) {
+      x.ldc = second ? p.ldc2 : p.ldc;
+      if (second) {
+        x.a = p.A2 + (int64_t)lo * p.lda * ES;
+        x.c = p.C2 + (int64_t)e * p.sC2 * ES;
+      }
+    }
   } else {
     x.m = hi - lo;
     x.k = e < p.experts ? p.k : 0;
     x.b = p.B + (int64_t)(e < p.experts ? e : 0) * p.sB * ES;
     x.c = p.C + (int64_t)lo * p.ldc * ES;
+    if constexpr (MODE == EX_GATE || MODE == EX_DX2) x.b2 = p.B2 + (int64_t)(e < p.experts ? e : 0) * p.sB2 * ES;
+    if constexpr (MODE == EX_DX2) x.a2 = p.A2 + (int64_t)lo * p.lda * ES;
+    if constexpr (MODE == EX_GATE) {
+      x.c2 = p.C2 ? p.C2 + (int64_t)lo * p.ldc2 * ES : nullptr;
+      x.c3 = p.C2 ? p.C3 + (int64_t)lo * p.ldc3 * ES : nullptr;
+    }
   }
   return x;
+}
+
+// From one row of a tile's result to the next.
+template <int MODE, class P>
+__device__ inline int64_t row_step(const P& p, const ExpertTile& x) {
+  if constexpr (MODE == EX_DW2) return x.ldc;
+  else return p.ldc;
 }
 
 // Elements c .. c + 7 of a row of n, at any address.
@@ -244,11 +306,41 @@ __device__ inline void store_eight(T* out, int c, int n, const f32x4& a, const f
   }
 }
 
+// The activation of a gate's value.
+__device__ inline float activate(float g, int act) {
+  if (act == ACT_SILU) return g / (1.f + __expf(-g));
+  if (act == ACT_GELU) return 0.5f * g * (1.f + erff(g * 0.70710678118654752f));
+  return fmaxf(g, 0.f);
+}
+
+// Columns lc .. lc + 7 of row lr of a slab's tile to C (EX_GATE: from blocks of 32 columns of both products, to C and
+// where they are kept to C2 and C3). read(column): four sums of the row.
+template <int MODE, typename T, class P, class R>
+__device__ inline void store_from(const P& p, const ExpertTile& x, int r, int c, int lc, R&& read) {
+  if constexpr (MODE == EX_GATE) {
+    const int at = (lc >> 5) * 64 + (lc & 31);
+    const f32x4 g0 = read(at), g1 = read(at + 4), u0 = read(at + 32), u1 = read(at + 36);
+    f32x4 h0, h1;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      h0[e] = activate(g0[e], p.act) * u0[e];
+      h1[e] = activate(g1[e], p.act) * u1[e];
+    }
+    store_eight(reinterpret_cast<T*>(x.c) + (int64_t)r * p.ldc, c, p.n, h0, h1);
+    if (x.c2) {
+      store_eight(reinterpret_cast<T*>(x.c2) + (int64_t)r * p.ldc2, c, p.n, g0, g1);
+      store_eight(reinterpret_cast<T*>(x.c3) + (int64_t)r * p.ldc3, c, p.n, u0, u1);
+    }
+  } else {
+    store_eight(reinterpret_cast<T*>(x.c) + (int64_t)r * row_step<MODE>(p, x), c, p.n, read(lc), read(lc + 4));
+  }
+}
+
 // Accumulators to C: through an fp32 slab in LDS, whole rows of 16-byte vectors out.
-template <typename T, class CFG>
-__device__ inline void expert_store(const ExpertArgs& p, const ExpertTile& x, char* lds, const f32x16 (&acc)[CFG::TM][CFG::TN], int lane) {
-  constexpr int BN = CFG::BN, NT = CFG::NT, WTM = CFG::WTM, CP = CFG::CP;
-  constexpr int SR = CFG::SR, SROWS = SR * WTM, VPR = BN / 8;
+template <int MODE, typename T, class CFG>
+__device__ inline void expert_store(const typename ArgsOf<MODE>::type& p, const ExpertTile& x, char* lds, const f32x16 (&acc)[CFG::TM][CFG::TN], int lane) {
+  constexpr int NT = CFG::NT, WTM = CFG::WTM, CP = CFG::CP;
+  constexpr int SR = CFG::SR, SROWS = SR * WTM, VPR = tile_cols<MODE, CFG>() / 8;
   const int wave = wave_uniform(threadIdx.x >> 6), tid = wave * 64 + lane;
   const int wm = wave / CFG::WVN, wn = wave % CFG::WVN;
   float* Cs = reinterpret_cast<float*>(lds);
@@ -259,11 +351,8 @@ __device__ inline void expert_store(const ExpertArgs& p, const ExpertTile& x, ch
     for (int idx = tid; idx < SROWS * VPR; idx += NT) {
       const int lr = idx / VPR, lc = (idx - lr * VPR) * 8;
       const int r = x.row0 + sl * SROWS + lr, c = x.col0 + lc;
-      if (r < x.m && c < p.n) {
-        const f32x4 a = *reinterpret_cast<const f32x4*>(Cs + lr * CP + lc);
-        const f32x4 b = *reinterpret_cast<const f32x4*>(Cs + lr * CP + lc + 4);
-        store_eight(reinterpret_cast<T*>(x.c) + (int64_t)r * p.ldc, c, p.n, a, b);
-      }
+      if (r < x.m && c < p.n)
+        store_from<MODE, T>(p, x, r, c, lc, [&](int at) { return *reinterpret_cast<const f32x4*>(Cs + lr * CP + at); });
     }
     lds_barrier();
   }
@@ -280,9 +369,9 @@ __device__ inline int stage_frag_off(int lane, int n0) {
 }
 
 // G waves' sums of one tile to C, added up in the waves' order.
-template <typename T, class CFG, int G>
-__device__ inline void expert_store_split(const ExpertArgs& p, const ExpertTile& x, char* lds, const f32x16 (&acc)[CFG::TM][CFG::TN], int lane) {
-  constexpr int BM = CFG::BM, BN = CFG::BN, CP = CFG::CP, VPR = BN / 8;
+template <int MODE, typename T, class CFG, int G>
+__device__ inline void expert_store_split(const typename ArgsOf<MODE>::type& p, const ExpertTile& x, char* lds, const f32x16 (&acc)[CFG::TM][CFG::TN], int lane) {
+  constexpr int BM = CFG::BM, CP = CFG::CP, VPR = tile_cols<MODE, CFG>() / 8;
   const int wave = wave_uniform(threadIdx.x >> 6);
   acc_to_slab<CFG>(reinterpret_cast<float*>(lds + wave * CFG::STAGE), acc, lane, 0, 0);
   lds_barrier();
@@ -290,16 +379,13 @@ __device__ inline void expert_store_split(const ExpertArgs& p, const ExpertTile&
   for (int idx = wave * 64 + lane; idx < BM * VPR; idx += 64 * G) {
     const int lr = idx / VPR, lc = (idx - lr * VPR) * 8;
     const int r = x.row0 + lr, c = x.col0 + lc;
-    if (r < x.m && c < p.n) {
-      f32x4 a = {0.f, 0.f, 0.f, 0.f}, b = a;
+    if (r < x.m && c < p.n)
+      store_from<MODE, T>(p, x, r, c, lc, [&](int at) {
+        f32x4 a = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        const float* Cs = reinterpret_cast<const float*>(lds + g * CFG::STAGE) + lr * CP + lc;
-        a += *reinterpret_cast<const f32x4*>(Cs);
-        b += *reinterpret_cast<const f32x4*>(Cs + 4);
-      }
-      store_eight(reinterpret_cast<T*>(x.c) + (int64_t)r * p.ldc, c, p.n, a, b);
-    }
+        for (int g = 0; g < G; ++g) a += *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(lds + g * CFG::STAGE) + lr * CP + at);
+        return a;
+      });
   }
   lds_barrier();
 }
@@ -319,10 +405,10 @@ __device__ inline void expert_store_split(const ExpertArgs& p, const ExpertTile&
 // LDS, barrier, MFMAs one after the other; fp32 1.8), so eight waves side by side cut the time of a
 // long contraction to a third: 3 experts of 504 x 4000 bf16, 256 rows each, 61 us to 20.
 template <int MODE, typename T, int FIT, class CFG, int G = 1>
-__global__ void __launch_bounds__(CFG::NT * G, CFG::OCC) expert_gemm_staged(const ExpertArgs p) {
+__global__ void __launch_bounds__(CFG::NT * G, CFG::OCC) expert_gemm_staged(const typename ArgsOf<MODE>::type p) {
   constexpr int ES = sizeof(T), BM = CFG::BM, BN = CFG::BN, NT = CFG::NT, KB = CFG::KB, ROWB = CFG::ROWB;
   constexpr int EPC = 16 / ES, BK = KB / ES, CPR = CFG::CPR, TM = CFG::TM, TN = CFG::TN;
-  constexpr bool AKM = MODE == EX_DW, BKM = MODE != EX_FWD;
+  constexpr bool AKM = ex_dw(MODE), BKM = !ex_fwd(MODE);
   constexpr int CPM = BM * ES / 16, CPN = BN * ES / 16;   // chunks per contraction-major row
   static_assert(G == 1 || (CFG::NT == 64 && CFG::STAGE >= CFG::SLAB), "the parts of a split tile are waves");
   __shared__ __align__(16) char lds_all[G > 1 ? G * CFG::STAGE : CFG::LDS];
@@ -332,7 +418,7 @@ __global__ void __launch_bounds__(CFG::NT * G, CFG::OCC) expert_gemm_staged(cons
   char* lds = lds_all + part * CFG::STAGE;
   const int tid = G > 1 ? threadIdx.x & 63 : threadIdx.x, lane = tid & 63, wave = G > 1 ? 0 : wave_uniform(tid >> 6);
   const int wm = wave / CFG::WVN, wn = wave % CFG::WVN;
-  if constexpr (MODE != EX_DW) expert_tiles<NT * G, BM>(p, first, wsum);
+  if constexpr (!ex_dw(MODE)) expert_tiles<NT * G, BM>(p, first, wsum);
   const ExpertList l = expert_list<MODE, CFG>(p, first);
   int from = 0;
   for (int t = blockIdx.x >> 3; t < l.n; t += gridDim.x >> 3) {
@@ -344,8 +430,8 @@ __global__ void __launch_bounds__(CFG::NT * G, CFG::OCC) expert_gemm_staged(cons
       for (int j = 0; j < TN; ++j)
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-    const T* A = reinterpret_cast<const T*>(x.a);
-    const T* B = reinterpret_cast<const T*>(x.b);
+    const int nh = (x.k + BK - 1) / BK;            // stages of a contraction, EX_DX2: of either
+    const int nk = MODE == EX_DX2 ? 2 * nh : nh;
     // A thread's chunks of a stage: loaded without a branch from places clamped into the operand,
     // so that the loads of a stage are all in flight together; what the clamps moved is put right
     // when the registers go to LDS, in the stages and tiles that have an edge. Only the contraction
@@ -353,6 +439,9 @@ __global__ void __launch_bounds__(CFG::NT * G, CFG::OCC) expert_gemm_staged(cons
     u32x4 ra[CFG::CA], rb[CFG::CB];
     constexpr int RPQ = NT / CPR;       // rows that one chunk of every thread covers
     constexpr bool CLAMP = FIT != CHUNK_TINY;
+    // A of EX_DX2 and EX_DW2 has rows of whole chunks, zeros behind the end
+    const int klen = MODE == EX_DX2 && CLAMP ? (x.k + EPC - 1) / EPC * EPC : x.k;
+    const int mlen = MODE == EX_DW2 && CLAMP ? (x.m + EPC - 1) / EPC * EPC : x.m;
     auto load_rows = [&](const T* src, int64_t ld, int row0, int rows, int k0, auto& r) {
       const int e0 = k0 + (tid % CPR) * EPC, row = tid / CPR;
 #pragma unroll
@@ -360,7 +449,7 @@ __global__ void __launch_bounds__(CFG::NT * G, CFG::OCC) expert_gemm_staged(cons
         const int first = row0 + RPQ * q;
         if (first >= rows) break;       // equal in every lane
         const T* at = src + (int64_t)min(first + row, rows - 1) * ld;
-        r[q] = load_chunk<T, FIT>(at, CLAMP ? min(e0, x.k - EPC) : e0, x.k);
+        r[q] = load_chunk<T, FIT>(at, CLAMP ? min(e0, klen - EPC) : e0, klen);
       }
     };
     auto load_deep = [&](const T* src, int64_t ld, int col0, int cols, int k0, auto& r, auto cpr_c) {
@@ -376,8 +465,8 @@ __global__ void __launch_bounds__(CFG::NT * G, CFG::OCC) expert_gemm_staged(cons
       const int e0 = k0 + (tid % CPR) * EPC;
 #pragma unroll
       for (int q = 0; q < (int)(sizeof(r) / 16); ++q) {
-        if constexpr (FIT == CHUNK_ALIGNED) r[q] = e0 < x.k ? r[q] : u32x4{0, 0, 0, 0};
-        else if constexpr (CLAMP) r[q] = drop_first<T>(r[q], e0 - min(e0, x.k - EPC));
+        if constexpr (FIT == CHUNK_ALIGNED) r[q] = e0 < klen ? r[q] : u32x4{0, 0, 0, 0};
+        else if constexpr (CLAMP) r[q] = drop_first<T>(r[q], e0 - min(e0, klen - EPC));
       }
     };
     auto mend_deep = [&](int col0, int cols, int k0, auto& r, auto cpr_c) {
@@ -389,20 +478,51 @@ __global__ void __launch_bounds__(CFG::NT * G, CFG::OCC) expert_gemm_staged(cons
         r[q] = k0 + tid / C + NT / C * q < x.k ? r[q] : u32x4{0, 0, 0, 0};
       }
     };
+    // the columns' rows of both matrices, a block of 32 of either in turn
+    auto load_gated = [&](int k0, auto& r) {
+      const int e0 = k0 + (tid % CPR) * EPC, row = tid / CPR;
+#pragma unroll
+      for (int q = 0; q < (int)(sizeof(r) / 16); ++q) {
+        constexpr int BLOCK = 32;
+        const int block = RPQ * q / BLOCK, first = x.col0 + (block >> 1) * BLOCK + RPQ * q % BLOCK;
+        if (first >= p.n) continue;     // equal in every lane
+        const T* src = reinterpret_cast<const T*>(block & 1 ? x.b2 : x.b);
+        int64_t ld = p.ldb;
+        if constexpr (MODE == EX_GATE)
+          if (block & 1) ld = p.ldb2;
+        const T* at = src + (int64_t)min(first + row, p.n - 1) * ld;
+        r[q] = load_chunk<T, FIT>(at, CLAMP ? min(e0, x.k - EPC) : e0, x.k);
+      }
+    };
     using CM = std::integral_constant<int, CPM>;
     using CN = std::integral_constant<int, CPN>;
-    auto load_stage = [&](int k0) {
-      if constexpr (AKM) load_deep(A, p.lda, x.row0, x.m, k0, ra, CM{});
+    // where stage kt begins in its contraction, and the operands of that one
+    auto begin_of = [&](int kt) { return (MODE == EX_DX2 && kt >= nh ? kt - nh : kt) * BK; };
+    auto load_stage = [&](int kt) {
+      const int k0 = begin_of(kt);
+      const T* A = reinterpret_cast<const T*>(x.a);
+      const T* B = reinterpret_cast<const T*>(x.b);
+      int64_t ldb = p.ldb;
+      if constexpr (MODE == EX_DX2) {
+        if (kt >= nh) {
+          A = reinterpret_cast<const T*>(x.a2);
+          B = reinterpret_cast<const T*>(x.b2);
+          ldb = p.ldb2;
+        }
+      }
+      if constexpr (AKM) load_deep(A, p.lda, x.row0, mlen, k0, ra, CM{});
       else load_rows(A, p.lda, x.row0, x.m, k0, ra);
-      if constexpr (BKM) load_deep(B, p.ldb, x.col0, p.n, k0, rb, CN{});
-      else load_rows(B, p.ldb, x.col0, p.n, k0, rb);
+      if constexpr (BKM) load_deep(B, ldb, x.col0, p.n, k0, rb, CN{});
+      else if constexpr (MODE == EX_GATE) load_gated(k0, rb);
+      else load_rows(B, ldb, x.col0, p.n, k0, rb);
     };
-    auto store_stage = [&](int buf, int k0) {
+    auto store_stage = [&](int buf, int kt) {
+      const int k0 = begin_of(kt);
       char* As = lds + buf * CFG::STAGE;
       char* Bs = As + BM * ROWB;
       const bool cut = k0 + BK > x.k;
       if constexpr (AKM) {
-        if (cut || (FIT == CHUNK_ANY && x.row0 + BM > x.m)) mend_deep(x.row0, x.m, k0, ra, CM{});
+        if (cut || (FIT == CHUNK_ANY && x.row0 + BM > mlen)) mend_deep(x.row0, mlen, k0, ra, CM{});
       } else {
         if (cut) mend_rows(k0, ra);
       }
@@ -434,7 +554,6 @@ __global__ void __launch_bounds__(CFG::NT * G, CFG::OCC) expert_gemm_staged(cons
     for (int i = 0; i < TM; ++i) aoff[i] = AKM ? stage_frag_off<BM * ES>(lane, wm * CFG::WTM + i * 32) : 0;
 #pragma unroll
     for (int j = 0; j < TN; ++j) boff[j] = BKM ? stage_frag_off<BN * ES>(lane, wn * CFG::WTN + j * 32) : 0;
-    const int nk = (x.k + BK - 1) / BK;
     // A stage's products of the wave's first R row blocks.
     auto compute = [&](int buf, auto r_c) {
       constexpr int R = decltype(r_c)::value;
@@ -467,15 +586,15 @@ __global__ void __launch_bounds__(CFG::NT * G, CFG::OCC) expert_gemm_staged(cons
       }
     };
     if constexpr (G > 1) {
-      if (part < nk) load_stage(part * BK);
+      if (part < nk) load_stage(part);
       for (int kt = part; kt < nk; kt += G) {
-        store_stage(0, kt * BK);
+        store_stage(0, kt);
         __builtin_amdgcn_wave_barrier();
-        if (kt + G < nk) load_stage((kt + G) * BK);
+        if (kt + G < nk) load_stage(kt + G);
         products(0);
         __builtin_amdgcn_wave_barrier();
       }
-      expert_store_split<T, CFG, G>(p, x, lds_all, acc, lane);
+      expert_store_split<MODE, T, CFG, G>(p, x, lds_all, acc, lane);
       continue;
     }
     if (nk) {
@@ -484,12 +603,12 @@ __global__ void __launch_bounds__(CFG::NT * G, CFG::OCC) expert_gemm_staged(cons
       __syncthreads();
     }
     for (int kt = 0; kt < nk; ++kt) {
-      if (kt + 1 < nk) load_stage((kt + 1) * BK);
+      if (kt + 1 < nk) load_stage(kt + 1);
       products(kt & 1);
-      if (kt + 1 < nk) store_stage((kt & 1) ^ 1, (kt + 1) * BK);
+      if (kt + 1 < nk) store_stage((kt & 1) ^ 1, kt + 1);
       __syncthreads();
     }
-    expert_store<T, CFG>(p, x, lds, acc, lane);
+    expert_store<MODE, T, CFG>(p, x, lds, acc, lane);
   }
 }
 

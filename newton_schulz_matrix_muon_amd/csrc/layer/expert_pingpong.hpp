@@ -86,10 +86,9 @@ __device__ inline FragOf<T> read_major(const char* at) {
 }
 
 template <int MODE, typename T>
-__global__ void __launch_bounds__(TilePP::NT, TilePP::OCC) expert_gemm_pp(const ExpertArgs p) {
+__global__ void __launch_bounds__(TilePP::NT, TilePP::OCC) expert_gemm_pp(const typename ArgsOf<MODE>::type p) {
   constexpr int BK = 64, OPB = TilePP::OPB, NT = TilePP::NT;
-  constexpr bool AKM = MODE == EX_DW, BKM = MODE != EX_FWD;
-  constexpr int STORES = 16;
+  constexpr bool AKM = ex_dw(MODE), BKM = !ex_fwd(MODE);
   // A's two stages, then B's
   __shared__ __align__(1024) char lds[4 * OPB];
   __shared__ int first[EXPERT_MAX + 2];
@@ -121,7 +120,12 @@ __global__ void __launch_bounds__(TilePP::NT, TilePP::OCC) expert_gemm_pp(const 
   const char* srca = p.A; const char* srcb = p.B;   // where the stage begins
   uint32_t lena = 0, lenb = 0;       // bytes from there to the operand's end
   int exta = 0, extb = 0;            // rows or columns of the tile that exist
-  const int rba = (int)p.lda * 2, rbb = (int)p.ldb * 2;     // bytes per row of memory
+  const int rba = (int)p.lda * 2;    // bytes per row of memory
+  int rbb = (int)p.ldb * 2;
+  if constexpr (MODE == EX_GATE)     // a wave brings rows of one of the two matrices
+    if (wave & 1) rbb = (int)p.ldb2 * 2;
+  const char* later_a = nullptr; const char* later_b = nullptr;   // EX_DX2: the contraction that follows
+  bool follows = false;
   int ti = t - step;                 // tile being issued
   int klen = 0, k0 = 0;              // its contraction length, the stage being issued
   int efrom = 0, islot = 1;
@@ -135,13 +139,31 @@ __global__ void __launch_bounds__(TilePP::NT, TilePP::OCC) expert_gemm_pp(const 
     const int r = i * 8 + (l0 >> 3);
     return (uint32_t)(r * rb + ((l0 & 7) ^ chunk_swizzle<8>(r)) * 16);
   };
+  // EX_GATE: rows 64 b .. 64 b + 31 of the stage are rows 32 b .. of W, the next 32 those of W2
+  auto offset_b = [&](int l0, int ext, int j) {
+    if constexpr (MODE == EX_GATE) {
+      const int r = b_piece(j) * 8 + (l0 >> 3), row = (wave >> 1) * 32 + j * 8 + (l0 >> 3);
+      return (uint32_t)(row * rbb + ((l0 & 7) ^ chunk_swizzle<8>(r)) * 16);
+    } else {
+      return offset(l0, BKM, rbb, ext, b_piece(j));
+    }
+  };
   // the next stage of the stream: of this tile, of the next tile that has any, or none
   auto advance = [&]() {
     islot ^= 1;
     k0 += BK;
     srca += AKM ? (int64_t)BK * rba : BK * 2;
     srcb += BKM ? (int64_t)BK * rbb : BK * 2;
-    if (k0 >= klen) {
+    if (MODE == EX_DX2 && k0 >= klen && follows) {
+      follows = false;
+      k0 = 0;
+      srca = later_a;
+      srcb = later_b;
+      if constexpr (MODE == EX_DX2) rbb = (int)p.ldb2 * 2;
+      const int l0 = opaque(lane);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) offb[j] = offset_b(l0, extb, j);
+    } else if (k0 >= klen) {
       k0 = klen = 0;
       while (live && klen == 0) {
         ti += step;
@@ -151,14 +173,25 @@ __global__ void __launch_bounds__(TilePP::NT, TilePP::OCC) expert_gemm_pp(const 
         klen = x.k;
         if (klen > 0) {
           srca = x.a + (AKM ? (int64_t)x.row0 * 2 : (int64_t)x.row0 * rba);
-          srcb = x.b + (BKM ? (int64_t)x.col0 * 2 : (int64_t)x.col0 * rbb);
+          if constexpr (MODE == EX_GATE) {
+            srcb = (wave & 1 ? x.b2 : x.b) + (int64_t)x.col0 * rbb;
+          } else {
+            if constexpr (MODE == EX_DX2) {
+              rbb = (int)p.ldb * 2;
+              later_a = x.a2 + (int64_t)x.row0 * rba;
+              later_b = x.b2 + (int64_t)x.col0 * 2;
+              follows = true;
+            }
+            srcb = x.b + (BKM ? (int64_t)x.col0 * 2 : (int64_t)x.col0 * rbb);
+          }
           exta = min(x.m - x.row0, 256);
-          extb = min(p.n - x.col0, 256);
+          if constexpr (MODE == EX_DW2) exta = (exta + 7) & ~7;   // whole chunks, zeros behind the end
+          extb = min(p.n - x.col0, tile_cols<MODE, TilePP>());
           const int l0 = opaque(lane);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             offa[j] = offset(l0, AKM, rba, exta, a_piece(j));
-            offb[j] = offset(l0, BKM, rbb, extb, b_piece(j));
+            offb[j] = offset_b(l0, extb, j);
           }
         }
       }
@@ -166,7 +199,8 @@ __global__ void __launch_bounds__(TilePP::NT, TilePP::OCC) expert_gemm_pp(const 
     const int rest = klen - k0;
     srca = uniform(srca);
     srcb = uniform(srcb);
-    lena = !live ? 0 : AKM ? (min(rest, BK) - 1) * rba + exta * 2 : (exta - 1) * rba + rest * 2;
+    const int resta = MODE == EX_DX2 ? (rest + 7) & ~7 : rest;   // whole chunks as well
+    lena = !live ? 0 : AKM ? (min(rest, BK) - 1) * rba + exta * 2 : (exta - 1) * rba + resta * 2;
     lenb = !live ? 0 : BKM ? (min(rest, BK) - 1) * rbb + extb * 2 : (extb - 1) * rbb + rest * 2;
     lena = wave_uniform(lena);
     lenb = wave_uniform(lenb);
@@ -265,7 +299,12 @@ __global__ void __launch_bounds__(TilePP::NT, TilePP::OCC) expert_gemm_pp(const 
   };
   // at most eight pieces still on their way, and the stores of the tile before if `stored`
   auto landed = [&](bool stored) {
-    wait_vmcnt<8 + STORES>();
+    if constexpr (MODE == EX_GATE) {
+      if (p.C2) wait_vmcnt<8 + 24>();
+      else wait_vmcnt<8 + 8>();
+    } else {
+      wait_vmcnt<8 + 16>();
+    }
     if (!stored) wait_vmcnt<8>();
   };
   auto phase_end = [&]() {
@@ -273,10 +312,49 @@ __global__ void __launch_bounds__(TilePP::NT, TilePP::OCC) expert_gemm_pp(const 
     barrier_nofence();
     __builtin_amdgcn_sched_barrier(0);
   };
-  // Stores: 16 a wave whatever the tile (rows and columns outside fall to the range check).
+  // Stores: 16 a wave whatever the tile (rows and columns outside fall to the range check); EX_GATE: 8, or 24
+  // with both products.
+  auto store_gated = [&](const ExpertTile& x) {
+    const int ln = opaque(lane), h = ln >> 5;
+    // eight columns of one row: runs of four from either half of the lanes
+    auto put = [&](const float (&v)[8], const __amdgpu_buffer_rsrc_t& rs, uint32_t off) {
+      uint32_t w[2][2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) w[u][e] = pack2<T>(v[u * 4 + 2 * e], v[u * 4 + 2 * e + 1]);
+      const auto s0 = __builtin_amdgcn_permlane32_swap(w[0][0], w[1][0], false, false);
+      const auto s1 = __builtin_amdgcn_permlane32_swap(w[0][1], w[1][1], false, false);
+      __builtin_amdgcn_raw_buffer_store_b128(u32x4{s0[0], s1[0], s0[1], s1[1]}, rs, off, 0, 0);
+    };
+    auto each = [&](const char* to, int64_t ld, auto&& value) {
+      const __amdgpu_buffer_rsrc_t rs = make_rsrc(uniform(to + ((int64_t)x.row0 * ld + x.col0) * 2), 0x7ffffff0u);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = wm * 128 + i * 32 + (ln & 31);
+        const bool in = x.row0 + r < x.m;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int c = wn * 32 + q * 16 + h * 8;
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = value(i, q * 8 + e);
+          put(v, rs, in && x.col0 + c < p.n ? (uint32_t)(r * (int)ld + c) * 2 : OOB);
+        }
+      }
+    };
+    if constexpr (MODE == EX_GATE) {
+      if (x.c2) {
+        each(x.c2, p.ldc2, [&](int i, int e) { return acc[i][0][e]; });
+        each(x.c3, p.ldc3, [&](int i, int e) { return acc[i][1][e]; });
+      }
+      each(x.c, p.ldc, [&](int i, int e) { return activate(acc[i][0][e], p.act) * acc[i][1][e]; });
+    }
+  };
   auto store = [&](const ExpertTile& x) {
     const int ln = opaque(lane), h = ln >> 5;
-    const __amdgpu_buffer_rsrc_t rs = make_rsrc(uniform(x.c + ((int64_t)x.row0 * p.ldc + x.col0) * 2), 0x7ffffff0u);
+    const int64_t ldc = row_step<MODE>(p, x);
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(uniform(x.c + ((int64_t)x.row0 * ldc + x.col0) * 2), 0x7ffffff0u);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = wm * 128 + i * 32 + (ln & 31);
@@ -294,7 +372,7 @@ __global__ void __launch_bounds__(TilePP::NT, TilePP::OCC) expert_gemm_pp(const 
           const auto s0 = __builtin_amdgcn_permlane32_swap(w[0][0], w[1][0], false, false);
           const auto s1 = __builtin_amdgcn_permlane32_swap(w[0][1], w[1][1], false, false);
           const u32x4 v = {s0[0], s1[0], s0[1], s1[1]};
-          const uint32_t off = in && x.col0 + c < p.n ? (uint32_t)(r * (int)p.ldc + c) * 2 : OOB;
+          const uint32_t off = in && x.col0 + c < p.n ? (uint32_t)(r * (int)ldc + c) * 2 : OOB;
           __builtin_amdgcn_raw_buffer_store_b128(v, rs, off, 0, 0);
         }
     }
@@ -318,7 +396,7 @@ __global__ void __launch_bounds__(TilePP::NT, TilePP::OCC) expert_gemm_pp(const 
   clear();
   for (; t < l.n; t += step) {
     const ExpertTile x = expert_tile<MODE, T, TilePP, true>(p, first, l, t, &cfrom, rows);
-    const int nk = (x.k + BK - 1) / BK;
+    const int nk = (x.k + BK - 1) / BK * (MODE == EX_DX2 ? 2 : 1);
     // blocks whose rows all lie outside are not computed (the barriers stay)
     const bool busy0 = x.row0 + wm * 128 < x.m, busy1 = x.row0 + wm * 128 + (AKM ? 0 : 64) < x.m;
     for (int kt = 0; kt < nk; ++kt) {
@@ -347,7 +425,8 @@ __global__ void __launch_bounds__(TilePP::NT, TilePP::OCC) expert_gemm_pp(const 
       }
       toggle = -toggle;
     }
-    store(x);
+    if constexpr (MODE == EX_GATE) store_gated(x);
+    else store(x);
     __builtin_amdgcn_sched_barrier(0);
     clear();
     begin = false;

@@ -1,0 +1,255 @@
+// Host side of the gated block (gated.hpp). As in layer.hip, validation happens before any HIP call and a
+// call only enqueues kernels on the caller's stream.
+
+#include "muon_ns.h"
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "checks.hpp"
+#include "expert_pingpong.hpp"
+#include "gated.hpp"
+
+using namespace mns;
+
+namespace {
+
+using Tile64 = TileCfg<64, 64, 1, 1, 128, 1, 2>;
+
+// Tile rows and columns of a product over all experts, as the kernels cut them.
+template <int MODE, class CFG>
+int64_t tile_rows(const GatedArgs& a) {
+  if (ex_dw(MODE)) return (int64_t)dw_matrices<MODE>(a) * ((a.m + CFG::BM - 1) / CFG::BM);
+  return (a.rows + CFG::BM - 1) / CFG::BM + std::min<int64_t>(a.experts, a.rows) + 1;
+}
+template <int MODE, class CFG>
+int tile_columns(const GatedArgs& a) { return (a.n + tile_cols<MODE, CFG>() - 1) / tile_cols<MODE, CFG>(); }
+
+// Persistent grid: enough workgroups for every tile, at most those the chip holds at once, the same
+// number on each of the eight XCDs.
+template <int MODE, class CFG>
+unsigned grid_for(const GatedArgs& a, int per_cu) {
+  const int64_t tiles = tile_rows<MODE, CFG>(a) * a.tiles_n;
+  return (unsigned)(8 * std::max<int64_t>(1, (std::min(tiles, (int64_t)device_cus() * per_cu) + 7) / 8));
+}
+
+template <int MODE, class CFG, int G>
+int run_staged(GatedArgs a, int dt, int fit, hipStream_t s) {
+  a.tiles_n = tile_columns<MODE, CFG>(a);
+  const int per_cu = G > 1 ? 1 : std::max(1, std::min((160 * 1024) / (CFG::LDS + 8192), 4 * CFG::OCC / (CFG::NT / 64)));
+  const dim3 g(grid_for<MODE, CFG>(a, per_cu)), b(CFG::NT * G);
+  return by_type(dt, [&](auto x) {
+    using T = decltype(x);
+    return launch(K_EXPERT_GEMM, s, [&] {
+      if (fit == CHUNK_ALIGNED) hipLaunchKernelGGL((expert_gemm_staged<MODE, T, CHUNK_ALIGNED, CFG, G>), g, b, 0, s, a);
+      else if (fit == CHUNK_ANY) hipLaunchKernelGGL((expert_gemm_staged<MODE, T, CHUNK_ANY, CFG, G>), g, b, 0, s, a);
+      else if constexpr (G == 1 || !ex_fwd(MODE))   // a split forward product's contraction would be one short row
+        hipLaunchKernelGGL((expert_gemm_staged<MODE, T, CHUNK_TINY, CFG, G>), g, b, 0, s, a);
+    });
+  });
+}
+
+template <int MODE>
+int run_pingpong(GatedArgs a, int dt, hipStream_t s) {
+  a.tiles_n = tile_columns<MODE, TilePP>(a);
+  const unsigned g = grid_for<MODE, TilePP>(a, 1);
+  return launch(K_EXPERT_GEMM, s, [&] {
+    if (dt == BF16) hipLaunchKernelGGL((expert_gemm_pp<MODE, __bf16>), dim3(g), dim3(TilePP::NT), 0, s, a);
+    else hipLaunchKernelGGL((expert_gemm_pp<MODE, _Float16>), dim3(g), dim3(TilePP::NT), 0, s, a);
+  });
+}
+
+int run_few(const GatedArgs& a, int dt, int fit, hipStream_t s) {
+  const dim3 g((a.n + 15) / 16, (unsigned)std::min<int64_t>(a.experts, a.rows) + 1);
+  return by_type(dt, [&](auto x) {
+    using T = decltype(x);
+    return launch(K_EXPERT_GEMM, s, [&] {
+      if (fit == CHUNK_ALIGNED) hipLaunchKernelGGL((expert_few_gated<T, CHUNK_ALIGNED>), g, dim3(256), 0, s, a);
+      else if (fit == CHUNK_ANY) hipLaunchKernelGGL((expert_few_gated<T, CHUNK_ANY>), g, dim3(256), 0, s, a);
+      else hipLaunchKernelGGL((expert_few_gated<T, CHUNK_TINY>), g, dim3(256), 0, s, a);
+    });
+  });
+}
+
+// The rules of the single products (layer.hip), with their tiles counted for two matrices.
+bool few_rows(const GatedArgs& a, int dt, int fit) {
+  const int64_t tiles = std::min<int64_t>(a.experts, a.rows) * ((a.n + 63) / 64);
+  const int64_t most = (fit == CHUNK_ALIGNED ? 4 : 2) * (dt == F32 ? 2 : 1) * (int64_t)a.experts;
+  const bool whole = fit == CHUNK_ALIGNED || dt == F32;
+  if (2 * tiles <= device_cus()) return a.rows <= (whole ? 4 * most : most);
+  return a.rows <= most && a.k * dtype_size(dt) >= 512 && whole;
+}
+
+template <int MODE>
+bool split_tiles(const GatedArgs& a, int dt) {
+  const int64_t stage = 128 / dtype_size(dt);
+  const int64_t some = std::min<int64_t>(a.experts, a.rows);   // experts that can have rows
+  const int64_t high = ex_dw(MODE) ? tile_rows<MODE, Tile64>(a) : std::max(some, a.rows / 64 + some / 2);
+  const int64_t tiles = high * tile_columns<MODE, Tile64>(a), deep = ex_dw(MODE) ? a.rows / a.experts : MODE == EX_DX2 ? 2 * (int64_t)a.k : a.k;
+  return deep >= 4 * stage && tiles <= (dt == F32 && !ex_dw(MODE) ? 9 : 1) * (int64_t)device_cus();
+}
+
+// vec: operands' rows of whole aligned chunks.
+template <int MODE>
+int run_product(const GatedArgs& a, int dt, bool vec, hipStream_t s) {
+  // the largest list of the smallest tiles of the persistent kernels
+  if (tile_rows<MODE, Tile64>(a) * (int64_t)tile_columns<MODE, Tile64>(a) > INT32_MAX) return MNS_ERR_SHAPE;
+  const int chunk = 16 / dtype_size(dt);
+  const bool tiny = (ex_dw(MODE) ? a.m : a.k) < chunk || (!ex_fwd(MODE) && a.n < chunk);
+  const int fit = vec ? CHUNK_ALIGNED : tiny ? CHUNK_TINY : CHUNK_ANY;
+  if constexpr (MODE == EX_GATE)
+    if (few_rows(a, dt, fit)) return run_few(a, dt, fit, s);
+  const bool whole = vec && a.c_vec && a.n % 8 == 0 && dt != F32 && a.n > (MODE == EX_GATE ? 64 : 128) && (!ex_dw(MODE) || a.m > 128);
+  const int64_t high = ex_dw(MODE) ? tile_rows<MODE, TilePP>(a) : a.rows / 256 + std::min<int64_t>(a.experts, a.rows);
+  if (whole && 2 * high * tile_columns<MODE, TilePP>(a) >= device_cus()) return run_pingpong<MODE>(a, dt, s);
+  if (split_tiles<MODE>(a, dt)) return run_staged<MODE, Tile64, 8>(a, dt, fit, s);
+  return run_staged<MODE, Tile128, 1>(a, dt, fit, s);
+}
+
+// Results that 16-byte stores fit.
+bool vec_out(const mns_tensor* t) {
+  const int64_t es = dtype_size(t->dtype);
+  return aligned16(t->ptr) && t->ld * es % 16 == 0 && (t->batch == 1 || t->stride * es % 16 == 0);
+}
+
+// X: S x K, Wg and Wu: E matrices N x K.
+int check_pair(const mns_tensor* X, const mns_tensor* Wg, const mns_tensor* Wu, const int32_t* offsets, int32_t act) {
+  for (const mns_tensor* t : {X, Wg, Wu}) {
+    if (int st = check_rows(t)) return st;
+    if (t->dtype != X->dtype) return MNS_ERR_DTYPE;
+  }
+  if (X->batch != 1 || !same_rows(Wg, Wu) || Wg->rows < 1 || Wg->batch > EXPERT_MAX || X->cols != Wg->cols) return MNS_ERR_SHAPE;
+  if (act != MNS_ACT_SILU && act != MNS_ACT_GELU && act != MNS_ACT_RELU) return MNS_ERR_ARG;
+  static_assert(ACT_SILU == MNS_ACT_SILU && ACT_GELU == MNS_ACT_GELU && ACT_RELU == MNS_ACT_RELU, "one numbering");
+  if (!offsets) return Wg->batch == 1 ? MNS_OK : MNS_ERR_ARG;
+  return check_experts(offsets, (int32_t)Wg->batch);
+}
+
+// A buffer of S x N rows.
+int check_inner(const mns_tensor* t, const mns_tensor* X, const mns_tensor* W) {
+  if (int st = check_rows(t)) return st;
+  if (t->dtype != X->dtype) return MNS_ERR_DTYPE;
+  return t->batch == 1 && t->rows == X->rows && t->cols == W->rows ? MNS_OK : MNS_ERR_SHAPE;
+}
+
+GatedArgs gated_args(const mns_tensor* A, const mns_tensor* Wg, const mns_tensor* Wu, const mns_tensor* C, const int32_t* offsets,
+                     int experts, int64_t rows) {
+  GatedArgs a{};
+  static_cast<ExpertArgs&>(a) = product_args(A, Wg, C, offsets, experts, rows);
+  a.B2 = reinterpret_cast<const char*>(Wu->ptr);
+  a.ldb2 = Wu->ld;
+  a.sB2 = Wu->batch > 1 ? Wu->stride : 0;
+  return a;
+}
+
+Span offsets_span(const int32_t* offsets, int64_t experts) { return span(offsets, offsets ? offsets_bytes(experts) : 0); }
+
+// dgate and dup of a backward pass: rows of whole 16-byte chunks.
+int64_t inner_ld(int64_t n) { return round_up(n, 8); }
+int64_t inner_bytes(int64_t rows, int64_t n, int dt) { return round_up(rows * inner_ld(n) * dtype_size(dt), 16); }
+
+}  // namespace
+
+// ==========================================================================================
+extern "C" {
+
+int expert_gated(const mns_tensor* X, const mns_tensor* Wg, const mns_tensor* Wu, const int32_t* offsets, int32_t act, const mns_tensor* H,
+                 const mns_tensor* G, const mns_tensor* U, void* stream) {
+  if (int st = check_pair(X, Wg, Wu, offsets, act)) return st;
+  if ((G == nullptr) != (U == nullptr)) return MNS_ERR_ARG;
+  for (const mns_tensor* t : {H, G ? G : H, U ? U : H})
+    if (int st = check_inner(t, X, Wg)) return st;
+  const Span none = span(static_cast<const void*>(nullptr), 0);
+  if (clash({span(H), G ? span(G) : none, U ? span(U) : none}, {span(X), span(Wg), span(Wu), offsets_span(offsets, Wg->batch)})) return MNS_ERR_ARG;
+  if (!X->rows) return MNS_OK;
+  GatedArgs a = gated_args(X, Wg, Wu, H, offsets, (int)Wg->batch, X->rows);
+  a.k = (int)X->cols;
+  a.act = act;
+  if (G) {
+    a.C2 = reinterpret_cast<char*>(G->ptr);
+    a.ldc2 = G->ld;
+    a.C3 = reinterpret_cast<char*>(U->ptr);
+    a.ldc3 = U->ld;
+    a.c_vec = a.c_vec && vec_out(G) && vec_out(U);
+  }
+  return run_product<EX_GATE>(a, X->dtype, vec_rows(X) && vec_rows(Wg) && vec_rows(Wu), as_stream(stream));
+}
+
+int mns_expert_gated_workspace_bytes(int64_t rows, int64_t inner, int32_t dtype, size_t* bytes) {
+  if (!bytes) return MNS_ERR_ARG;
+  if (!valid_dtype(dtype)) return MNS_ERR_DTYPE;
+  if (rows < 0 || rows > kMaxRows || inner < 1 || inner > kMaxCols) return MNS_ERR_SHAPE;
+  *bytes = (size_t)(2 * inner_bytes(rows, inner, dtype));
+  return MNS_OK;
+}
+
+int expert_gated_backward(const mns_tensor* dH, const mns_tensor* X, const mns_tensor* Wg, const mns_tensor* Wu, const mns_tensor* G,
+                          const mns_tensor* U, const int32_t* offsets, int32_t act, const mns_tensor* dX, const mns_tensor* dWg,
+                          const mns_tensor* dWu, void* ws, size_t ws_bytes, void* stream) {
+  if (int st = check_pair(X, Wg, Wu, offsets, act)) return st;
+  for (const mns_tensor* t : {dH, G, U})
+    if (int st = check_inner(t, X, Wg)) return st;
+  if ((dWg == nullptr) != (dWu == nullptr) || (!dX && !dWg)) return MNS_ERR_ARG;
+  for (const mns_tensor* t : {dX ? dX : X, dWg ? dWg : Wg, dWu ? dWu : Wu}) {
+    if (int st = check_rows(t)) return st;
+    if (t->dtype != X->dtype) return MNS_ERR_DTYPE;
+  }
+  if ((dX && !same_rows(dX, X)) || (dWg && (!same_rows(dWg, Wg) || !same_rows(dWu, Wg)))) return MNS_ERR_SHAPE;
+  const int64_t half = inner_bytes(X->rows, Wg->rows, X->dtype);
+  if (X->rows && (!ws || ws_bytes < (size_t)(2 * half) || !aligned16(ws))) return MNS_ERR_WORKSPACE;
+  const Span none = span(static_cast<const void*>(nullptr), 0);
+  if (clash({dX ? span(dX) : none, dWg ? span(dWg) : none, dWu ? span(dWu) : none, X->rows ? span(ws, 2 * half) : none},
+            {span(dH), span(X), span(Wg), span(Wu), span(G), span(U), offsets_span(offsets, Wg->batch)}))
+    return MNS_ERR_ARG;
+  const hipStream_t s = as_stream(stream);
+  // the rows of dgate and dup
+  mns_tensor d = *X;
+  d.ptr = ws;
+  d.cols = Wg->rows;
+  d.ld = inner_ld(Wg->rows);
+  char* dup = reinterpret_cast<char*>(ws) + half;
+  if (X->rows) {
+    GatedGradArgs g{};
+    g.dh = reinterpret_cast<const char*>(dH->ptr);
+    g.gate = reinterpret_cast<const char*>(G->ptr);
+    g.up = reinterpret_cast<const char*>(U->ptr);
+    g.ldh = dH->ld;
+    g.ldg = G->ld;
+    g.ldu = U->ld;
+    g.dgate = reinterpret_cast<char*>(ws);
+    g.dup = dup;
+    g.ld = d.ld;
+    g.offsets = offsets;
+    g.experts = (int)Wg->batch;
+    g.rows = X->rows;
+    g.n = (int)Wg->rows;
+    g.units = (int)(d.ld / 8);
+    if (int st = by_type(X->dtype, [&](auto x) {
+          using T = decltype(x);
+          return launch(K_EXPERT_GEMM, s, [&] { hipLaunchKernelGGL(gated_grad<T>, grid_of((g.rows * g.units + 255) / 256), dim3(256), 0, s, g, act); });
+        }))
+      return st;
+  }
+  // Their rows are whole chunks whatever N is: zeros behind the end meet rows of W behind its end, which
+  // read as zeros, or are rows of dW behind its end, which are not stored.
+  if (dX && X->rows) {
+    GatedArgs a = gated_args(&d, Wg, Wu, dX, offsets, (int)Wg->batch, X->rows);
+    a.A2 = dup;
+    a.k = (int)Wg->rows;
+    if (int st = run_product<EX_DX2>(a, X->dtype, vec_rows(Wg) && vec_rows(Wu), s)) return st;
+  }
+  if (!dWg) return MNS_OK;
+  if (!X->rows) d.ptr = nullptr;
+  GatedArgs a{};
+  static_cast<ExpertArgs&>(a) = product_args(&d, X, dWg, offsets, (int)Wg->batch, X->rows);
+  a.A2 = X->rows ? dup : nullptr;
+  a.C2 = reinterpret_cast<char*>(dWu->ptr);
+  a.ldc2 = dWu->ld;
+  a.sC2 = dWu->batch > 1 ? dWu->stride : 0;
+  a.c_vec = a.c_vec && vec_out(dWu);
+  a.m = (int)Wg->rows;
+  return run_product<EX_DW2>(a, X->dtype, vec_rows(X), s);
+}
+
+}  // extern "C"

@@ -114,7 +114,10 @@ def declare(lib):
         "embed": [vp, i32, t, ctypes.c_float, t, vp],
         "mns_embed_workspace_bytes": [i64, i64, i64, P(sz)],
         "embed_backward": [t, vp, i32, ctypes.c_float, t, vp, sz, vp],
-        "adamw8_step": [ctypes.c_int, pp, pp, pp, pp, pp, pp, P(i64), i32, P(MnsAdamwParams), ctypes.c_uint64, vp],
+        "expert_gated": [t, t, t, vp, i32, t, t, t, vp],
+        "mns_expert_gated_workspace_bytes": [i64, i64, i32, P(sz)],
+        "expert_gated_backward": [t, t, t, t, t, t, vp, i32, t, t, t, vp, sz, vp],
+        "adamw8_step": [ctypes.c_int, pp, pp, pp, pp, pp, pp, P(i64), i32, P(MnsAdamw8Params), vp],
     }
     for name, argtypes in layer.items():
         fn = getattr(lib, name)
@@ -518,6 +521,12 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, *, lr: float, beta1: float 
     return params
 
 
+class MnsAdamw8Params(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("step", ctypes.c_int32),
+                ("bias_correction", ctypes.c_int32), ("seed", ctypes.c_uint64)]
+
+
 MX_BLOCK = 32   # elements that share a power of two in 8-bit values
 
 
@@ -585,8 +594,8 @@ def adamw8_step(params, grads, states, *, lr: float, step: int, beta1: float = 0
                 raise ValueError(f"{what}: a tensor of params, grads or states[{i}] is on {t_.device}, expected {device}")
     arr = lambda ts: (ctypes.c_void_p * n)(*[t.data_ptr() for t in ts])
     numels = (ctypes.c_int64 * n)(*[t.numel() for t in params])
-    ap = MnsAdamwParams(lr, beta1, beta2, eps, weight_decay, step, 1 if bias_correction else 0)
-    _launch(what, params[0], n, arr(params), arr(grads), *(arr(ts) for ts in zip(*states)), numels, code, ctypes.byref(ap), seed)
+    ap = MnsAdamw8Params(lr, beta1, beta2, eps, weight_decay, step, 1 if bias_correction else 0, seed)
+    _launch(what, params[0], n, arr(params), arr(grads), *(arr(ts) for ts in zip(*states)), numels, code, ctypes.byref(ap))
     return params
 
 
@@ -941,6 +950,76 @@ def expert_matmul_backward(dy, x, w, offsets):
     _launch("expert_matmul_grad_input", dy, dyd, describe(w), at, describe(dx))
     _launch("expert_matmul_grad_weight", dy, dyd, xd, at, describe(dw))
     return dx, dw
+
+
+ACTIVATIONS = {"silu": 0, "gelu": 1, "relu": 2}
+
+
+def _check_gated(what, x, w_gate, w_up, offsets, act, **inner):
+    """Both matrices of every expert, or of a dense layer (2-D, no offsets); inner: buffers of [rows, N]."""
+    _check_recorded(what, x, w_gate, w_up, *inner.values())
+    if act not in ACTIVATIONS:
+        raise ValueError(f"{what}: act must be one of {', '.join(ACTIVATIONS)}, got {act!r}")
+    if w_gate.dim() not in (2, 3):
+        raise ValueError(f"{what}: w_gate must be [experts, rows, cols] or [rows, cols], got {w_gate.dim()}-D")
+    _check_like(what, w_gate, w_up=w_up)
+    if offsets is not None:
+        _check_offsets(what, offsets)
+    if offsets is None and _batch(w_gate) != 1:
+        raise ValueError(f"{what}: {_batch(w_gate)} experts need offsets")
+    if offsets is not None and _batch(w_gate) != offsets.numel() - 1:
+        raise ValueError(f"{what}: w_gate holds {_batch(w_gate)} experts, offsets {offsets.numel() - 1}")
+    _check_rows(what, w_gate, x=x, **inner)
+    _check_shape(what, "x", x, (x.shape[0], w_gate.shape[-1]))
+    for name, t in inner.items():
+        if t is not None:
+            _check_shape(what, name, t, (x.shape[0], w_gate.shape[-2]))
+    return ACTIVATIONS[act]
+
+
+def expert_gated(x, w_gate, w_up, offsets=None, *, act: str = "silu", keep: bool = False, out=None):
+    """act(x w_gate[e]^T) * (x w_up[e]^T) for the rows of expert e, the rows of no expert zero, in one kernel
+    (C ABI ``expert_gated``). x: [rows, K] sorted by expert, w_gate and w_up: [experts, N, K] with offsets as
+    expert_sort gives them, or [N, K] without offsets: a dense layer. act: silu, gelu (with erf) or relu.
+    keep=True: (h, gate, up) with both projections, for expert_gated_backward."""
+    what = "expert_gated"
+    code = _check_gated(what, x, w_gate, w_up, offsets, act, out=out)
+    _check_device(what, x, w_gate=w_gate, w_up=w_up, offsets=offsets, out=out)
+    shape = (x.shape[0], w_gate.shape[-2])
+    h = x.new_empty(shape) if out is None else out
+    gate, up = (x.new_empty(shape), x.new_empty(shape)) if keep else (None, None)
+    _launch(what, x, describe(x), describe(w_gate), describe(w_up), _ptr(offsets), code, describe(h), describe(gate) if keep else None,
+            describe(up) if keep else None)
+    return (h, gate, up) if keep else h
+
+
+def expert_gated_workspace_bytes(rows: int, inner: int, like) -> int:
+    """like: a tensor of the rows' dtype."""
+    n = ctypes.c_size_t()
+    _check(_lib().mns_expert_gated_workspace_bytes(rows, inner, dtype_code(like), ctypes.byref(n)), "mns_expert_gated_workspace_bytes")
+    return n.value
+
+
+def expert_gated_backward(dh, x, w_gate, w_up, gate, up, offsets=None, *, act: str = "silu", need_input: bool = True,
+                          need_weights: bool = True, workspace=None):
+    """(dx, dw_gate, dw_up) of expert_gated from gate and up as it kept them (C ABI ``expert_gated_backward``):
+    the weights' gradients as the batches that muon_step takes. need_input, need_weights: what is not
+    wanted is None."""
+    torch = _torch()
+    what = "expert_gated_backward"
+    code = _check_gated(what, x, w_gate, w_up, offsets, act, dh=dh, gate=gate, up=up)
+    if not need_input and not need_weights:
+        raise ValueError(f"{what}: nothing wanted")
+    _check_workspace(what, workspace)
+    _check_device(what, x, dh=dh, w_gate=w_gate, w_up=w_up, gate=gate, up=up, offsets=offsets, workspace=workspace)
+    if workspace is None:
+        workspace = torch.empty(expert_gated_workspace_bytes(x.shape[0], w_gate.shape[-2], x), dtype=torch.uint8, device=x.device)
+    dx = x.new_empty(x.shape) if need_input else None
+    dwg, dwu = (w_gate.new_empty(w_gate.shape), w_gate.new_empty(w_gate.shape)) if need_weights else (None, None)
+    opt = lambda t: None if t is None else describe(t)
+    _launch(what, x, describe(dh), describe(x), describe(w_gate), describe(w_up), describe(gate), describe(up), _ptr(offsets), code, opt(dx),
+            opt(dwg), opt(dwu), _ptr(workspace), _ws_bytes(workspace))
+    return dx, dwg, dwu
 
 
 # ------------------------------------------------------------------ around the layer

@@ -109,15 +109,15 @@ def test_embed_backward_refusals(L):
 
 
 def test_adamw8_refusals(L):
-    from newton_schulz_matrix_muon_amd.ops import MnsAdamwParams
+    from newton_schulz_matrix_muon_amd.ops import MnsAdamw8Params
     arr = lambda *v: (ctypes.c_void_p * len(v))(*v)
     good = dict(n=2, p=(P, P + 4096), g=(Q, Q + 4096), m=(R, R + 101), ms=(R + 4096, R + 4100), r=(S, S + 4096), rs=(S + 8192, S + 8300),
                 numels=(100, 50), dt=BF16)
 
-    def call(hyper=(1e-3, 0.9, 0.95, 1e-8, 0.1, 1, 0), **k):
+    def call(hyper=(1e-3, 0.9, 0.95, 1e-8, 0.1, 1, 0, 0), **k):
         a = {**good, **k}
         lists = [None if a[i] is None else arr(*a[i]) for i in ("p", "g", "m", "ms", "r", "rs")]
-        return L.adamw8_step(a["n"], *lists, (ctypes.c_int64 * len(a["numels"]))(*a["numels"]), a["dt"], ctypes.byref(MnsAdamwParams(*hyper)), 0, None)
+        return L.adamw8_step(a["n"], *lists, (ctypes.c_int64 * len(a["numels"]))(*a["numels"]), a["dt"], ctypes.byref(MnsAdamw8Params(*hyper)), None)
     for name in ("p", "g", "m", "ms", "r", "rs"):
         assert call(**{name: None}) == ARG
         assert call(**{name: (None, good[name][1])}) == ARG
@@ -126,8 +126,8 @@ def test_adamw8_refusals(L):
     assert call(m=(R, R + 99)) == ARG                                        # the second tensor's codes begin in the first's
     assert call(rs=(S + 8192, S + 8195)) == ARG                              # ... and its powers
     assert call(p=(P, P)) == ARG and call(g=(P, Q)) == ARG and call(r=(R + 4096, S)) == ARG
-    for i, bad in ((0, float("nan")), (1, 1.0), (1, -0.1), (2, 1.0), (3, -1e-8), (4, float("inf")), (5, 0), (6, 2)):
-        h = [1e-3, 0.9, 0.95, 1e-8, 0.1, 1, 0]
+    for i, bad in ((0, float("nan")), (0, 1e39), (1, 1.0), (1, -0.1), (2, 1.0), (3, -1e-8), (4, float("inf")), (5, 0), (6, 2)):
+        h = [1e-3, 0.9, 0.95, 1e-8, 0.1, 1, 0, 0]
         h[i] = bad
         assert call(hyper=tuple(h)) == ARG, (i, bad)
     none = (None, None)

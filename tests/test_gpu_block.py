@@ -360,20 +360,21 @@ def state_values(torch, codes, scales):
 def check_adamw8(torch, p0, g, s0, p1, s1, hp, place, dtype):
     """One step of one tensor from its inputs' copies; hp as ops.adamw8_step takes them."""
     f32 = lambda v: float(torch.tensor(v, dtype=torch.float32))
-    lr, b1, b2, eps, wd = (f32(hp[k]) for k in ("lr", "beta1", "beta2", "eps", "weight_decay"))
+    lr, b1, b2, eps = (f32(hp[k]) for k in ("lr", "beta1", "beta2", "eps"))
+    c1, c2, keep = f32(1 - hp["beta1"]), f32(1 - hp["beta2"]), f32(1 - hp["lr"] * hp["weight_decay"])
     n = p0.numel()
     if n == 0:
         return
     p0, g = p0.double(), g.double()
     m0, r0 = state_values(torch, s0[0], s0[1]), state_values(torch, s0[2], s0[3])
-    m, v = b1 * m0 + (1 - b1) * g, b2 * r0 ** 2 + (1 - b2) * g ** 2
+    m, v = b1 * m0 + c1 * g, b2 * r0 ** 2 + c2 * g ** 2
     r = v.sqrt()
-    fix = (1 - b1 ** hp["step"], math.sqrt(1 - b2 ** hp["step"])) if hp["bias_correction"] else (1.0, 1.0)
-    dm = 4 * U * (b1 * m0.abs() + (1 - b1) * g.abs()) + 1e-38
+    fix = (1 - hp["beta1"] ** hp["step"], math.sqrt(1 - hp["beta2"] ** hp["step"])) if hp["bias_correction"] else (1.0, 1.0)
+    dm = 4 * U * (b1 * m0.abs() + c1 * g.abs()) + 1e-38
     upd = (m / fix[0]) / (r / fix[1] + eps)
     # r: three roundings under the root, halved, and the root's own; the quotient three more
-    slack = 4 * U * ((1 - lr * wd) * p0.abs() + lr * upd.abs()) + lr * (dm / fix[0] / (r / fix[1] + eps) + 8 * U * upd.abs())
-    close(p1, (1 - lr * wd) * p0 - lr * upd, slack, "parameter")
+    slack = 4 * U * (keep * p0.abs() + lr * upd.abs()) + lr * (dm / fix[0] / (r / fix[1] + eps) + 8 * U * upd.abs())
+    close(p1, keep * p0 - lr * upd, slack, "parameter")
     rm, rr = random_bits(torch, hp["seed"], hp["step"], place, n)
     for name, val, off, codes, scales, rnd, least in (("m", m, dm, s1[0], s1[1], rm, 0.0), ("r", r, 4 * U * r + 1e-38, s1[2], s1[3], rr, 2.0 ** -9)):
         top = torch.nn.functional.pad(val.abs(), (0, -n % 32)).view(-1, 32).amax(dim=1)
