@@ -49,36 +49,45 @@ __host__ __device__ inline uint32_t adam8_mix(uint32_t x) {
   x *= ADAM8_MIX2;
   return x ^ (x >> 16);
 }
-// 16 bits for m (low) and 16 for r (high) of element i.
-__device__ inline uint32_t adam8_bits(uint32_t key, int64_t i) {
+// Elements i .. i + 7 (i a multiple of 8): 16 bits for m (low) and 16 for r (high) each.
+__device__ inline void adam8_bits(uint32_t key, int64_t i, uint32_t (&rnd)[8]) {
   if (i >> 32) key = adam8_mix(key ^ (uint32_t)(i >> 32));
-  return adam8_mix((uint32_t)i * ADAM8_MIX0 + key);
+  const uint32_t x = (uint32_t)i * ADAM8_MIX0 + key;
+#pragma unroll
+  for (uint32_t e = 0; e < 8; ++e) rnd[e] = adam8_mix(x + e * ADAM8_MIX0);
 }
 
 // A magnitude of at most 448 to a multiple of e4m3's step below or above it, above by the chance
-// that rnd / 2^16 is under the rest: fp32 keeps 20 bits more than e4m3, and below 2^-6 the step is 2^-9.
+// that rnd / 2^16 is under the rest. fp32 keeps 20 bits more than e4m3, which rnd is added to and which are
+// then cut off; below 2^-6 the step is 2^-9 throughout, as it is for x + 2^-6.
 __device__ inline float adam8_round(float x, uint32_t rnd) {
-  const float high = __uint_as_float((__float_as_uint(x) + (rnd << 4)) & 0xfff00000u);
-  const float low = floorf(x * 512.f + (float)rnd * 0x1p-16f) * 0x1p-9f;
-  return x < 0x1p-6f ? low : high;
+  const float low = x < 0x1p-6f ? 0x1p-6f : 0.f;
+  return __uint_as_float((__float_as_uint(x + low) + (rnd << 4)) & 0xfff00000u) - low;
 }
 
 // Eight elements' new states as codes with their block's byte: adam8_round of the scaled magnitudes.
 template <bool ROOT>
 __device__ inline u32x2 adam8_codes(const float (&v)[8], const uint32_t (&rnd)[8], int* byte) {
-  float top = 0.f, q[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) top = fmaxf(top, finite_size(v[e]));
-  *byte = mx_byte(quad_max(top));
+  float q[8];
+  bool odd;
+  *byte = mx_byte(quad_max(mx_top(v, &odd)));
   const float d = mx_divisor(*byte);
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const float a = __builtin_fabsf(v[e]);
     float s = adam8_round(a * d, ROOT ? rnd[e] >> 16 : rnd[e] & 0xffffu);
-    if (ROOT && a > 0.f) s = fmaxf(s, 0x1p-9f);
-    q[e] = a < __builtin_inff() ? __builtin_copysignf(s, v[e]) : __builtin_nanf("");
+    if (ROOT) s = fmaxf(s, a > 0.f ? 0x1p-9f : 0.f);
+    q[e] = ROOT ? s : __builtin_copysignf(s, v[e]);
   }
-  return u32x2{mx_pack(q[0], q[1], q[2], q[3]), mx_pack(q[4], q[5], q[6], q[7])};
+  return mx_codes(v, q, odd);
+}
+
+// Square root to 1 ulp (2 half steps) in one instruction, which takes no denormals: small numbers are
+// moved up by 2^64 first.
+__device__ inline float adam8_sqrt(float v) {
+  const bool small = v < 0x1p-64f;
+  const float r = __builtin_amdgcn_sqrtf(small ? v * 0x1p64f : v);
+  return small ? r * 0x1p-32f : r;
 }
 
 __device__ inline u32x2 adam8_load(const uint8_t* p, int64_t i, int64_t n) {
@@ -185,14 +194,16 @@ __global__ void __launch_bounds__(ADAM8_BLOCK) adamw8_kernel(const Adam8Table t)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         mf[e] = t.beta1 * mf[e] + t.one_beta1 * gf[e];
-        rf[e] = __builtin_sqrtf(t.beta2 * (rf[e] * rf[e]) + t.one_beta2 * (gf[e] * gf[e]));
-        pf[e] = t.wd_mul * pf[e] - t.lr * ((mf[e] * t.bc1) / (rf[e] * t.bc2 + t.eps));
+        rf[e] = adam8_sqrt(t.beta2 * (rf[e] * rf[e]) + t.one_beta2 * (gf[e] * gf[e]));
+        // the reciprocal to 1 ulp: its error in p is 2^-23 of the step
+        pf[e] = t.wd_mul * pf[e] - t.lr * ((mf[e] * t.bc1) * __builtin_amdgcn_rcpf(rf[e] * t.bc2 + t.eps));
       }
     }
+    adam8_bits(t.key[ti], i, rnd);
+    if (i + 8 > n) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      rnd[e] = adam8_bits(t.key[ti], i + e);
-      if (i + e >= n) mf[e] = rf[e] = 0.f;   // behind the end nothing counts for the block
+      for (int e = 0; e < 8; ++e)
+        if (i + e >= n) mf[e] = rf[e] = 0.f;   // behind the end nothing counts for the block
     }
     // the quads' lanes meet here, those behind the end with zeros
     int bm, br;

@@ -24,37 +24,40 @@ namespace {
 constexpr int held(int nt, int vpt) { return nt * vpt * 8; }
 constexpr int kRmsHeld = held(1024, 2);   // backward: longer rows take the kernels that read them again
 
-// Workgroups that share the rows of a backward pass, each with a part of dweight.
+// Threads that hold a row, a chunk each: whole waves, and past 256 threads as many on each of a CU's four SIMDs,
+// so that as many workgroups fit a CU as its registers allow.
+int row_threads(int64_t cols) {
+  const int64_t nt = (cols + 511) / 512 * 64;
+  return (int)std::min<int64_t>(1024, nt <= 256 ? nt : round_up(nt, 256));
+}
+
+// Workgroups that share the rows of a backward pass, each with a part of dweight: as many as the chip holds at
+// once (20 waves a CU), but at least four turns of rows each once every CU has one, because each part costs as
+// much traffic as two fp32 rows.
 int rms_parts(int64_t rows, int64_t cols) {
-  const int64_t turns = cols <= held(64, 2) ? (rows + 3) / 4 : rows;   // four rows at a time where a wave holds one
-  const int64_t most = cols <= held(256, 1) ? 1024 : 512;
+  const int64_t turns = cols <= held(64, 1) ? (rows + 3) / 4 : rows;   // four rows at a time where a wave holds one
+  const int64_t most = 256 * (20 / (std::max(cols <= held(64, 1) ? 256 : 64, row_threads(cols)) / 64));
   return (int)std::max<int64_t>(1, turns <= 256 ? turns : std::min(most, std::max<int64_t>(256, turns / 4)));
 }
 
 template <typename T, typename WT, bool MX>
 void launch_rms_fwd(const RmsArgs& a, hipStream_t s) {
-  const dim3 one = grid_of(a.rows), four = grid_of((a.rows + 3) / 4);
-  if (a.cols <= held(64, 1)) hipLaunchKernelGGL((rms_fwd_row<T, WT, 64, 1, MX>), four, dim3(256), 0, s, a);
-  else if (a.cols <= held(64, 2)) hipLaunchKernelGGL((rms_fwd_row<T, WT, 64, 2, MX>), four, dim3(256), 0, s, a);
-  else if (a.cols <= held(64, 4)) hipLaunchKernelGGL((rms_fwd_row<T, WT, 64, 4, MX>), four, dim3(256), 0, s, a);
-  else if (a.cols <= held(256, 2)) hipLaunchKernelGGL((rms_fwd_row<T, WT, 256, 2, MX>), one, dim3(256), 0, s, a);
-  else if (a.cols <= held(256, 4)) hipLaunchKernelGGL((rms_fwd_row<T, WT, 256, 4, MX>), one, dim3(256), 0, s, a);
-  else if (a.cols <= held(1024, 2)) hipLaunchKernelGGL((rms_fwd_row<T, WT, 1024, 2, MX>), one, dim3(1024), 0, s, a);
-  else hipLaunchKernelGGL((rms_fwd_long<T, WT, MX>), one, dim3(1024), 0, s, a);
+  // as many workgroups as the chip holds at once (32 waves a CU), or a row each
+  auto turns = [&](int64_t n, int nt) { return dim3((unsigned)std::min<int64_t>(n, (int64_t)device_cus() * std::max(1, 2048 / nt))); };
+  const int nt = row_threads(a.cols);
+  if (a.cols <= held(64, 1)) hipLaunchKernelGGL((rms_fwd_row<T, WT, true, 1, MX>), turns((a.rows + 3) / 4, 256), dim3(256), 0, s, a);
+  else if (a.cols <= held(1024, 1)) hipLaunchKernelGGL((rms_fwd_row<T, WT, false, 1, MX>), turns(a.rows, nt), dim3(nt), 0, s, a);
+  else if (a.cols <= held(1024, 2)) hipLaunchKernelGGL((rms_fwd_row<T, WT, false, 2, MX>), turns(a.rows, 1024), dim3(1024), 0, s, a);
+  else hipLaunchKernelGGL((rms_fwd_long<T, WT, MX>), grid_of(a.rows), dim3(1024), 0, s, a);
 }
 
 template <typename T, typename WT>
 void launch_rms_bwd(const RmsArgs& a, hipStream_t s) {
   const dim3 g((unsigned)a.nparts);
-  if (a.cols <= held(64, 1)) hipLaunchKernelGGL((rms_bwd_row<T, WT, 64, 1>), g, dim3(256), 0, s, a);
-  else if (a.cols <= held(64, 2)) hipLaunchKernelGGL((rms_bwd_row<T, WT, 64, 2>), g, dim3(256), 0, s, a);
-  else if (a.cols <= held(256, 1)) hipLaunchKernelGGL((rms_bwd_row<T, WT, 256, 1>), g, dim3(256), 0, s, a);
-  else if (a.cols <= held(256, 2)) hipLaunchKernelGGL((rms_bwd_row<T, WT, 256, 2>), g, dim3(256), 0, s, a);
-  else if (a.cols <= held(512, 2)) {
-    // wider elements need the registers of two chunks for one
-    if constexpr (sizeof(T) == 2) hipLaunchKernelGGL((rms_bwd_row<T, WT, 512, 2>), g, dim3(512), 0, s, a);
-    else hipLaunchKernelGGL((rms_bwd_row<T, WT, 1024, 1>), g, dim3(1024), 0, s, a);
-  } else hipLaunchKernelGGL((rms_bwd_row<T, WT, 1024, 2>), g, dim3(1024), 0, s, a);
+  const int nt = row_threads(a.cols);
+  if (a.cols <= held(64, 1)) hipLaunchKernelGGL((rms_bwd_row<T, WT, true, 1>), g, dim3(256), 32 * 64, s, a);
+  else if (a.cols <= held(1024, 1)) hipLaunchKernelGGL((rms_bwd_row<T, WT, false, 1>), g, dim3(nt), 32 * nt, s, a);
+  else hipLaunchKernelGGL((rms_bwd_row<T, WT, false, 2>), g, dim3(1024), 64 * 1024, s, a);
 }
 
 // Whether `out` is the very buffer `in`: a row of it is read before it is written, by the same threads.
@@ -118,7 +121,7 @@ int units_of(int64_t cols, int v) { return (int)((cols + v - 1) / v); }
 // The workspace of a gradient, in bytes from its beginning.
 struct EmbedPlan {
   int bits, passes, steps, nblocks;
-  int64_t tiles, marks, key[2], pos[2], hist, part, total;
+  int64_t tiles, marks, sorted[2], hist, part, total;
 };
 EmbedPlan embed_plan(int64_t n, int64_t vocab, int64_t cols) {
   EmbedPlan e{};
@@ -127,7 +130,7 @@ EmbedPlan embed_plan(int64_t n, int64_t vocab, int64_t cols) {
   e.passes = (width + 9) / 10;
   e.bits = (width + e.passes - 1) / e.passes;
   const int64_t waves = (n + EMBED_NT - 1) / EMBED_NT;   // 64-position steps per wave of one workgroup
-  e.steps = (int)(n <= EMBED_ONE ? std::max<int64_t>(1, waves) : (waves + 255) / 256);
+  e.steps = (int)(n <= EMBED_ONE ? std::max<int64_t>(1, waves) : round_up((waves + 255) / 256, EMBED_MANY));
   e.nblocks = (int)std::max<int64_t>(1, (waves + e.steps - 1) / e.steps);
   e.tiles = (n + EMBED_TILE - 1) / EMBED_TILE;
   int64_t at = 0;
@@ -137,10 +140,7 @@ EmbedPlan embed_plan(int64_t n, int64_t vocab, int64_t cols) {
     return here;
   };
   e.marks = take(vocab);
-  for (int i = 0; i < 2; ++i) {
-    e.key[i] = take(4 * n);
-    e.pos[i] = take(4 * n);
-  }
+  for (int64_t& s : e.sorted) s = take(8 * n);
   e.hist = take(n > EMBED_ONE ? 4 * (int64_t)e.nblocks * EMBED_DIGITS : 0);
   e.part = take(e.tiles > 1 ? 8 * e.tiles * cols : 0);
   e.total = at;
@@ -356,16 +356,20 @@ int embed_backward(const mns_tensor* dY, const void* tokens, int32_t id_bytes, f
   p.passes = e.passes;
   p.steps = e.steps;
   p.nblocks = e.nblocks;
-  for (int i = 0; i < 2; ++i) {
-    p.key[i] = reinterpret_cast<int32_t*>(base + e.key[i]);
-    p.pos[i] = reinterpret_cast<int32_t*>(base + e.pos[i]);
-  }
+  for (int i = 0; i < 2; ++i) p.sorted[i] = reinterpret_cast<int2*>(base + e.sorted[i]);
   p.hist = reinterpret_cast<int32_t*>(base + e.hist);
   p.marks = reinterpret_cast<uint8_t*>(base + e.marks);
   const hipStream_t s = as_stream(stream);
   auto sort = [&](auto id) {
     using ID = decltype(id);
-    if (p.n <= EMBED_ONE) return launch(K_ROUTE, s, [&] { hipLaunchKernelGGL(embed_sort_one<ID>, dim3(1), dim3(EMBED_NT), 0, s, p); });
+    if (!p.n) return launch(K_ROUTE, s, [&] { hipLaunchKernelGGL(embed_no_marks<256>, dim3((p.vocab + 4095) / 4096), dim3(256), 0, s, p); });
+    if (p.n <= EMBED_ONE)
+      return launch(K_ROUTE, s, [&] {
+        if (p.steps <= 1) hipLaunchKernelGGL((embed_sort_one<ID, 1>), dim3(1), dim3(EMBED_NT), 0, s, p);
+        else if (p.steps <= 4) hipLaunchKernelGGL((embed_sort_one<ID, 4>), dim3(1), dim3(EMBED_NT), 0, s, p);
+        else if (p.steps <= 8) hipLaunchKernelGGL((embed_sort_one<ID, 8>), dim3(1), dim3(EMBED_NT), 0, s, p);
+        else hipLaunchKernelGGL((embed_sort_one<ID, 16>), dim3(1), dim3(EMBED_NT), 0, s, p);
+      });
     for (int pass = 0; pass < p.passes; ++pass) {
       if (int st = launch(K_ROUTE, s, [&] { hipLaunchKernelGGL(embed_sort_count<ID>, dim3(p.nblocks), dim3(EMBED_NT), 0, s, p, pass); })) return st;
       if (int st = launch(K_ROUTE, s, [&] { hipLaunchKernelGGL(embed_sort_place<ID>, dim3(p.nblocks), dim3(EMBED_NT), 0, s, p, pass); })) return st;
@@ -378,8 +382,7 @@ int embed_backward(const mns_tensor* dY, const void* tokens, int32_t id_bytes, f
   a.dy_ld = row_bytes(dY);
   a.dt = reinterpret_cast<char*>(dT->ptr);
   a.dt_ld = row_bytes(dT);
-  a.key = p.key[(p.passes - 1) & 1];
-  a.pos = p.pos[(p.passes - 1) & 1];
+  a.sorted = p.sorted[(p.passes - 1) & 1];
   a.marks = p.marks;
   a.part = reinterpret_cast<float*>(base + e.part);
   a.n = p.n;

@@ -100,43 +100,47 @@ struct EmbedSortArgs {
   int bits, passes;                // per pass
   int steps;                       // 64-position steps per wave: a workgroup takes EMBED_NT * steps positions
   int nblocks;
-  int32_t* key[2];                 // token (vocab: none) of the sorted positions, after even and odd passes
-  int32_t* pos[2];                 // and the positions
+  int2* sorted[2];                 // token (vocab: none) and position, after even and odd passes
   int32_t* hist;                   // [nblocks][EMBED_DIGITS]
   uint8_t* marks;                  // [vocab]: whether the token occurs
 };
 
-struct EmbedDigit {
-  int key, pos, digit;             // digit -1: past the end
+// A wave's positions of one pass, 64 at a time: digit -1 past the end. Held in registers from the counts to
+// the places, and loaded together, so that a pass waits for memory once.
+template <int STEPS>
+struct EmbedRun {
+  int key[STEPS], pos[STEPS], digit[STEPS];
 };
-template <typename ID>
-__device__ inline EmbedDigit embed_digit(const EmbedSortArgs& p, int pass, int64_t s) {
-  if (s >= p.n) return {0, 0, -1};
-  EmbedDigit d;
-  if (pass == 0) {
-    const int v = token_of<ID>(p.tokens, s, p.vocab);
-    d.key = v < 0 ? p.vocab : v;
-    d.pos = (int)s;
-  } else {
-    d.key = p.key[(pass - 1) & 1][s];
-    d.pos = p.pos[(pass - 1) & 1][s];
+template <typename ID, int STEPS>
+__device__ inline void embed_load(const EmbedSortArgs& p, int pass, int64_t s0, EmbedRun<STEPS>& d) {
+  const int from = (pass - 1) & 1;
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) {
+    const int64_t s = min(s0 + 64 * i, p.n - 1);
+    if (pass == 0) {
+      const int v = token_of<ID>(p.tokens, s, p.vocab);
+      d.key[i] = v < 0 ? p.vocab : v;
+      d.pos[i] = (int)s;
+    } else {
+      const int2 kp = p.sorted[from][s];
+      d.key[i] = kp.x;
+      d.pos[i] = kp.y;
+    }
   }
-  d.digit = (d.key >> (pass * p.bits)) & ((1 << p.bits) - 1);
-  return d;
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) d.digit[i] = s0 + 64 * i < p.n ? (d.key[i] >> (pass * p.bits)) & ((1 << p.bits) - 1) : -1;
 }
 
-// Each wave's positions by digit into at[wave], for this workgroup's run of positions.
-template <typename ID>
-__device__ inline void embed_count(const EmbedSortArgs& p, int pass, int64_t s0, int (*at)[EMBED_DIGITS]) {
+// Each wave's positions by digit into at[wave].
+template <int STEPS>
+__device__ inline void embed_count(const EmbedRun<STEPS>& d, int (*at)[EMBED_DIGITS]) {
   const int wv = threadIdx.x >> 6;
-  for (int e = threadIdx.x; e < EMBED_DIGITS; e += EMBED_NT)
 #pragma unroll
-    for (int w = 0; w < EMBED_WAVES; ++w) at[w][e] = 0;
+  for (int w = 0; w < EMBED_WAVES; ++w) at[w][threadIdx.x] = 0;
   __syncthreads();
-  for (int i = 0; i < p.steps; ++i) {
-    const int d = embed_digit<ID>(p, pass, s0 + 64 * i).digit;
-    if (d >= 0) atomicAdd(&at[wv][d], 1);
-  }
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i)
+    if (d.digit[i] >= 0) atomicAdd(&at[wv][d.digit[i]], 1);
   __syncthreads();
 }
 
@@ -164,67 +168,85 @@ __device__ inline void embed_places(int total, int before, int (*at)[EMBED_DIGIT
 }
 
 // The positions to their places: a wave ranks 64 at a time, equal digits by lane number.
-template <typename ID>
-__device__ inline void embed_place(const EmbedSortArgs& p, int pass, int64_t s0, int (*at)[EMBED_DIGITS]) {
+template <int STEPS>
+__device__ inline void embed_place(const EmbedSortArgs& p, int pass, const EmbedRun<STEPS>& d, int (*at)[EMBED_DIGITS]) {
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  for (int i = 0; i < p.steps; ++i) {
-    const EmbedDigit d = embed_digit<ID>(p, pass, s0 + 64 * i);
-    uint64_t same = __ballot(d.digit >= 0);
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) {
+    const int digit = d.digit[i];
+    uint64_t same = __ballot(digit >= 0);
     for (int b = 0; b < p.bits; ++b) {
-      const uint64_t m = __ballot((d.digit >> b) & 1);
-      same &= (d.digit >> b) & 1 ? m : ~m;
+      const uint64_t m = __ballot((digit >> b) & 1);
+      same &= (digit >> b) & 1 ? m : ~m;
     }
     const int lead = __builtin_ctzll(same | (1ull << 63));
     int next = 0;
-    if (d.digit >= 0 && lane == lead) next = atomicAdd(&at[wv][d.digit], __builtin_popcountll(same));
+    if (digit >= 0 && lane == lead) next = atomicAdd(&at[wv][digit], __builtin_popcountll(same));
     next = __shfl(next, lead);
-    if (d.digit < 0) continue;
-    const int to = next + __builtin_popcountll(same & ((1ull << lane) - 1));
-    p.key[pass & 1][to] = d.key;
-    p.pos[pass & 1][to] = d.pos;
-    if (pass == 0 && d.key < p.vocab) p.marks[d.key] = 1;
+    if (digit >= 0) {
+      const int to = next + __builtin_popcountll(same & ((1ull << lane) - 1));
+      p.sorted[pass & 1][to] = int2{d.key[i], d.pos[i]};
+      if (pass == 0 && d.key[i] < p.vocab) p.marks[d.key[i]] = 1;
+    }
   }
 }
 
-// Every pass in one workgroup, and the marks.
-template <typename ID>
+// Every pass in one workgroup, and the marks. At least one position.
+template <typename ID, int STEPS>
 __global__ void __launch_bounds__(EMBED_NT) embed_sort_one(const EmbedSortArgs p) {
   __shared__ int at[EMBED_WAVES][EMBED_DIGITS];
   __shared__ int scan[EMBED_WAVES];
   // the workspace begins at a multiple of 16 bytes, and so do the marks, with room behind them
   for (int64_t i = (int64_t)threadIdx.x * 16; i < p.vocab; i += EMBED_NT * 16) *reinterpret_cast<u32x4*>(p.marks + i) = u32x4{0, 0, 0, 0};
-  const int64_t s0 = (int64_t)(threadIdx.x >> 6) * 64 * p.steps + (threadIdx.x & 63);
+  const int64_t s0 = (int64_t)(threadIdx.x >> 6) * 64 * STEPS + (threadIdx.x & 63);
   for (int pass = 0; pass < p.passes; ++pass) {
-    embed_count<ID>(p, pass, s0, at);
+    EmbedRun<STEPS> d;
+    embed_load<ID>(p, pass, s0, d);
+    embed_count(d, at);
     int total = 0;
+#pragma unroll
     for (int w = 0; w < EMBED_WAVES; ++w) total += at[w][threadIdx.x];
     embed_places(total, 0, at, scan);
-    embed_place<ID>(p, pass, s0, at);
+    embed_place(p, pass, d, at);
     __syncthreads();
   }
 }
 
+// No position: every row of the table is zeros.
+template <int NT>
+__global__ void __launch_bounds__(NT) embed_no_marks(const EmbedSortArgs p) {
+  const int64_t i = ((int64_t)blockIdx.x * NT + threadIdx.x) * 16;
+  if (i < p.vocab) *reinterpret_cast<u32x4*>(p.marks + i) = u32x4{0, 0, 0, 0};
+}
+
 template <typename ID>
 __global__ void __launch_bounds__(EMBED_NT) embed_sort_count(const EmbedSortArgs p, int pass) {
-  __shared__ int at[EMBED_WAVES][EMBED_DIGITS];
+  __shared__ int at[EMBED_DIGITS];
   if (pass == 0)
     for (int64_t i = ((int64_t)blockIdx.x * EMBED_NT + threadIdx.x) * 16; i < p.vocab; i += (int64_t)gridDim.x * EMBED_NT * 16)
       *reinterpret_cast<u32x4*>(p.marks + i) = u32x4{0, 0, 0, 0};
-  const int64_t s0 = ((int64_t)blockIdx.x * EMBED_WAVES + (threadIdx.x >> 6)) * 64 * p.steps + (threadIdx.x & 63);
-  embed_count<ID>(p, pass, s0, at);
-  int total = 0;
-  for (int w = 0; w < EMBED_WAVES; ++w) total += at[w][threadIdx.x];
-  p.hist[(int64_t)blockIdx.x * EMBED_DIGITS + threadIdx.x] = total;
+  at[threadIdx.x] = 0;
+  __syncthreads();
+  const int64_t lo = (int64_t)blockIdx.x * EMBED_NT * p.steps;
+  for (int i = 0; i < p.steps; ++i) {
+    EmbedRun<1> d;
+    embed_load<ID>(p, pass, lo + (int64_t)i * EMBED_NT + threadIdx.x, d);
+    if (d.digit[0] >= 0) atomicAdd(&at[d.digit[0]], 1);
+  }
+  __syncthreads();
+  p.hist[(int64_t)blockIdx.x * EMBED_DIGITS + threadIdx.x] = at[threadIdx.x];
 }
 
 // Every workgroup adds up the counts itself: all of them for the digits before, the earlier
-// workgroups' for its own positions.
+// workgroups' for its own positions, which it takes EMBED_MANY steps of each wave at a time.
+constexpr int EMBED_MANY = 1;
 template <typename ID>
 __global__ void __launch_bounds__(EMBED_NT) embed_sort_place(const EmbedSortArgs p, int pass) {
   __shared__ int at[EMBED_WAVES][EMBED_DIGITS];
   __shared__ int scan[EMBED_WAVES];
-  const int64_t s0 = ((int64_t)blockIdx.x * EMBED_WAVES + (threadIdx.x >> 6)) * 64 * p.steps + (threadIdx.x & 63);
-  embed_count<ID>(p, pass, s0, at);
+  const int64_t lo = (int64_t)blockIdx.x * EMBED_NT * p.steps, own = (int64_t)(threadIdx.x >> 6) * 64 * EMBED_MANY + (threadIdx.x & 63);
+  EmbedRun<EMBED_MANY> d;
+  embed_load<ID>(p, pass, lo + own, d);
   int total = 0, before = 0;
   for (int b0 = 0; b0 < p.nblocks; b0 += 16) {
     int n[16];
@@ -236,8 +258,17 @@ __global__ void __launch_bounds__(EMBED_NT) embed_sort_place(const EmbedSortArgs
       before += b0 + b < (int)blockIdx.x ? n[b] : 0;
     }
   }
-  embed_places(total, before, at, scan);
-  embed_place<ID>(p, pass, s0, at);
+  for (int i = 0; i < p.steps; i += EMBED_MANY) {
+    if (i) embed_load<ID>(p, pass, lo + (int64_t)i * EMBED_NT + own, d);
+    embed_count(d, at);
+    int mine = 0;
+#pragma unroll
+    for (int w = 0; w < EMBED_WAVES; ++w) mine += at[w][threadIdx.x];
+    embed_places(total, before, at, scan);
+    embed_place(p, pass, d, at);
+    before += mine;
+    __syncthreads();
+  }
 }
 
 // --------------------------------------------------------------------------------- gradient
@@ -246,7 +277,7 @@ constexpr int EMBED_TILE = 32;
 struct EmbedGradArgs {
   const char* dy; int64_t dy_ld;   // bytes per row
   char* dt; int64_t dt_ld;
-  const int32_t* key; const int32_t* pos;   // sorted
+  const int2* sorted;              // tokens (x) and positions (y)
   const uint8_t* marks;
   float* part;                     // [2 * tiles][cols]: a tile's part of the token that came in from the tile before, of the one that goes on
   int64_t n, tiles;
@@ -291,9 +322,9 @@ __global__ void __launch_bounds__(256) embed_grad(const EmbedGradArgs p) {
   if (tile >= p.tiles) return;
   const int c = EmbedUnit<T, V>::at((int)(x - q * (unsigned)p.units), p.cols);
   const int64_t lo = tile * EMBED_TILE, hi = min(lo + EMBED_TILE, p.n);
-  const int after = hi < p.n ? p.key[hi] : -1;
-  int now = p.key[lo];
-  bool came = lo > 0 && p.key[lo - 1] == now;
+  const int after = hi < p.n ? p.sorted[hi].x : -1;
+  int now = p.sorted[lo].x;
+  bool came = lo > 0 && p.sorted[lo - 1].x == now;
   float acc[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) acc[e] = 0.f;
@@ -313,19 +344,19 @@ __global__ void __launch_bounds__(256) embed_grad(const EmbedGradArgs p) {
     came = false;
   };
   for (int64_t s = lo; s < hi; s += U) {
-    int key[U];
+    int2 at[U];
     EmbedUnit<T, V> row[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) key[u] = s + u < hi ? p.key[s + u] : p.vocab;
     // the rows behind the tile's end read the tile's last and are left out: no branch between the loads
 #pragma unroll
-    for (int u = 0; u < U; ++u) row[u].load(reinterpret_cast<const T*>(p.dy + (int64_t)p.pos[min(s + u, hi - 1)] * p.dy_ld), c);
+    for (int u = 0; u < U; ++u) at[u] = p.sorted[min(s + u, hi - 1)];
+#pragma unroll
+    for (int u = 0; u < U; ++u) row[u].load(reinterpret_cast<const T*>(p.dy + (int64_t)at[u].y * p.dy_ld), c);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (s + u >= hi) continue;
-      if (key[u] != now) {
+      if (at[u].x != now) {
         leave(false);
-        now = key[u];
+        now = at[u].x;
       }
       if (now >= p.vocab) return;  // sorted behind all tokens
       float f[V];
@@ -346,26 +377,36 @@ __global__ void __launch_bounds__(256) embed_join(const EmbedGradArgs p) {
   const int64_t a = block_id();    // the tile that it begins in
   if (a + 1 >= p.tiles) return;
   const int64_t hi = (a + 1) * EMBED_TILE;
-  const int token = p.key[hi];
-  if (token >= p.vocab || p.key[hi - 1] != token) return;
-  if (a > 0 && p.key[a * EMBED_TILE] == token && p.key[a * EMBED_TILE - 1] == token) return;   // it came from further ahead
-  // the first tile behind that does not begin within the token
+  const int token = p.sorted[hi].x, last = p.sorted[hi - 1].x, begin = p.sorted[a * EMBED_TILE].x, ahead = a > 0 ? p.sorted[a * EMBED_TILE - 1].x : -1;
+  if (token >= p.vocab || last != token) return;
+  if (begin == token && ahead == token) return;   // it came from further ahead
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  // the first tile behind that does not begin within the token: 64 places looked at together
   int64_t lo = a + 1, end = p.tiles;
   while (end - lo > 1) {
-    const int64_t mid = (lo + end) / 2;
-    if (p.key[mid * EMBED_TILE] == token) lo = mid;
-    else end = mid;
+    const int64_t step = (end - lo + 63) / 64, t = lo + lane * step;
+    const int in = __builtin_popcountll(__ballot(t < end && p.sorted[min(t, end - 1) * EMBED_TILE].x == token));
+    lo += (in - 1) * step;                        // the first of them is lo itself
+    end = min(lo + step, end);
   }
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   for (int64_t c0 = (int64_t)blockIdx.z * 512; c0 < p.cols; c0 += (int64_t)gridDim.z * 512) {
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    auto add = [&](const float* part) {
+    if (wv == 0) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (c0 + e * 64 + lane < p.cols) acc[e] += part[c0 + e * 64 + lane];
-    };
-    if (wv == 0) add(p.part + (2 * a + 1) * p.cols);
-    for (int64_t t = a + 1 + wv; t < end; t += 4) add(p.part + 2 * t * p.cols);
+      for (int e = 0; e < 8; ++e) acc[e] = p.part[(2 * a + 1) * p.cols + min(c0 + e * 64 + lane, (int64_t)p.cols - 1)];
+    }
+    // four tiles' parts in flight; the tiles behind the last read the last and are left out
+    for (int64_t t = a + 1 + wv; t < end; t += 16) {
+      float v[4][8];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[u][e] = p.part[2 * min(t + 4 * u, end - 1) * p.cols + min(c0 + e * 64 + lane, (int64_t)p.cols - 1)];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] += t + 4 * u < end ? v[u][e] : 0.f;
+    }
     if (wv)
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum[wv - 1][e][lane] = acc[e];

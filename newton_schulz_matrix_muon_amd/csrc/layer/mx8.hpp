@@ -24,9 +24,23 @@ __device__ inline int mx_byte(float top) {
 __device__ inline float mx_divisor(int byte) { return __uint_as_float((uint32_t)(254 - byte) << 23); }
 __device__ inline float mx_factor(int byte) { return byte ? __uint_as_float((uint32_t)byte << 23) : 0x1p-127f; }
 
-__device__ inline float finite_size(float v) {
-  const float a = __builtin_fabsf(v);
-  return a < __builtin_inff() ? a : 0.f;
+// The largest finite magnitude of eight values, and whether any value of the wave is not finite (rare,
+// equal in every lane). Magnitudes compare as their bits do.
+__device__ inline float mx_top(const float (&v)[8], bool* odd) {
+  constexpr uint32_t INF = 0x7f800000u;
+  uint32_t top = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
+  *odd = __any(top >= INF);
+  if (*odd) {
+    top = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t u = __float_as_uint(v[e]) & 0x7fffffffu;
+      top = max(top, u < INF ? u : 0u);
+    }
+  }
+  return __uint_as_float(top);
 }
 
 // The maximum over the four lanes that hold a block, eight values each.
@@ -41,21 +55,23 @@ __device__ inline uint32_t mx_pack(float a, float b, float c, float d) {
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
 }
 
-// Eight values of which the largest scaled magnitude is 448 at most.
-__device__ inline u32x2 mx_codes(const float (&v)[8], float divisor) {
-  float q[8];
+// Eight values as codes, q as scaled and rounded; odd: as mx_top found.
+__device__ inline u32x2 mx_codes(const float (&v)[8], float (&q)[8], bool odd) {
+  if (odd) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) q[e] = __builtin_fabsf(v[e]) < __builtin_inff() ? v[e] * divisor : __builtin_nanf("");
+    for (int e = 0; e < 8; ++e) q[e] = __builtin_fabsf(v[e]) < __builtin_inff() ? q[e] : __builtin_nanf("");
+  }
   return u32x2{mx_pack(q[0], q[1], q[2], q[3]), mx_pack(q[4], q[5], q[6], q[7])};
 }
 
 __device__ inline void mx_values(const u32x2& codes, float factor, float (&v)[8]) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    v[4 * h] = __builtin_amdgcn_cvt_f32_fp8((int)codes[h], 0) * factor;
-    v[4 * h + 1] = __builtin_amdgcn_cvt_f32_fp8((int)codes[h], 1) * factor;
-    v[4 * h + 2] = __builtin_amdgcn_cvt_f32_fp8((int)codes[h], 2) * factor;
-    v[4 * h + 3] = __builtin_amdgcn_cvt_f32_fp8((int)codes[h], 3) * factor;
+    const auto a = __builtin_amdgcn_cvt_pk_f32_fp8((int)codes[h], false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)codes[h], true);
+    v[4 * h] = a[0] * factor;
+    v[4 * h + 1] = a[1] * factor;
+    v[4 * h + 2] = b[0] * factor;
+    v[4 * h + 3] = b[1] * factor;
   }
 }
 

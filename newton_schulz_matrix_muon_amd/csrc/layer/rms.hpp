@@ -95,29 +95,53 @@ struct Chunk {
   }
 };
 
-template <int NT>
-__device__ inline float block_sum(float v, float* red) {
-  v = wave_sum(v);
-  if constexpr (NT > 64) {
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+// Sum over a wave's lanes, in every lane: moves within rows of 16 lanes, then swaps of rows and halves
+// (in one instruction each; through LDS, as __shfl goes, the sum takes several times as long).
+__device__ inline float lanes_sum(float v) {
+  auto moved = [](float x, auto ctrl_c) {
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), decltype(ctrl_c)::value, 0xf, 0xf, true));
+  };
+  v += moved(v, std::integral_constant<int, 0xb1>{});    // quads: 1 0 3 2
+  v += moved(v, std::integral_constant<int, 0x4e>{});    // quads: 2 3 0 1
+  v += moved(v, std::integral_constant<int, 0x141>{});   // half rows backwards
+  v += moved(v, std::integral_constant<int, 0x140>{});   // rows backwards
+  const auto rows = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(rows[0]) + __uint_as_float(rows[1]);
+  const auto halves = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(halves[0]) + __uint_as_float(halves[1]);
+}
+
+// Sum over the workgroup's waves (up to 16), in every thread; within the wave alone where a wave has a row
+// (WAVE). red: 16 floats that no other sum between two barriers uses, zero where there is no wave.
+template <bool WAVE>
+__device__ inline float block_sum(float v, f32x4* red) {
+  v = lanes_sum(v);
+  if constexpr (!WAVE) {
+    if ((threadIdx.x & 63) == 0) reinterpret_cast<float*>(red)[threadIdx.x >> 6] = v;
     lds_barrier();   // loads and stores on their way stay in flight
-    v = 0.f;
-#pragma unroll
-    for (int i = 0; i < NT / 64; ++i) v += red[i];
+    const f32x4 s = (red[0] + red[1]) + (red[2] + red[3]);
+    v = (s[0] + s[1]) + (s[2] + s[3]);
   }
   return v;
+}
+// Zeros where block_sum has no wave; a barrier follows before the first sum's reads.
+__device__ inline void clear_sums(f32x4* red, int n) {
+  for (int i = threadIdx.x; i < n; i += blockDim.x) red[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  __syncthreads();
 }
 
 // y of eight columns, as the rows' type or in 8 bits (MX).
 template <typename T, bool MX>
 __device__ inline void rms_store(const RmsArgs& p, int64_t r, T* y, int c, const float (&f)[8]) {
   if constexpr (MX) {
-    float top = 0.f;
+    bool odd;
+    const int byte = mx_byte(quad_max(mx_top(f, &odd)));
+    const float d = mx_divisor(byte);
+    float v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) top = fmaxf(top, finite_size(f[e]));
-    const int byte = mx_byte(quad_max(top));
+    for (int e = 0; e < 8; ++e) v[e] = f[e] * d;
+    const u32x2 codes = mx_codes(f, v, odd);
     if (c >= p.cols) return;
-    const u32x2 codes = mx_codes(f, mx_divisor(byte));
     uint8_t* q = p.q + r * p.cols + c;
     if (c + 8 <= p.cols) {
       *reinterpret_cast<u32x2_any*>(q) = codes;
@@ -134,76 +158,89 @@ __device__ inline void rms_store(const RmsArgs& p, int64_t r, T* y, int c, const
   }
 }
 
-// NT threads hold a row, VPT chunks each (NT = 64: four rows a workgroup, no barrier).
-template <typename T, typename WT, int NT, int VPT, bool MX>
-__global__ void __launch_bounds__(NT < 256 ? 256 : NT) rms_fwd_row(const RmsArgs p) {
-  __shared__ float red[16];
-  const int tid = threadIdx.x % NT;
-  const int64_t r = block_id() * (NT < 256 ? 256 / NT : 1) + threadIdx.x / NT;
-  if (r >= p.rows) return;   // whole waves (NT = 64), else the whole workgroup
-  const T* x = row_ptr<T>(p.x, r);
-  Chunk<T> px[VPT];
+// A row is held by a wave (WAVE: four rows a workgroup, no barrier) or by the workgroup, as many waves as it
+// takes, VPT chunks a thread. A workgroup walks every gridDim.x-th row (or four of them) with the weight
+// in registers and the next row's x and r already on their way.
+template <typename T, typename WT, bool WAVE, int VPT, bool MX>
+__global__ void __launch_bounds__(WAVE ? 256 : 1024, !WAVE && VPT == 1 && sizeof(T) == 2 ? 8 : 1) rms_fwd_row(const RmsArgs p) {
+  constexpr int RPW = WAVE ? 4 : 1;
+  constexpr bool AHEAD = VPT == 1;
+  __shared__ f32x4 red[2][4];
+  const int NT = WAVE ? 64 : blockDim.x, tid = WAVE ? threadIdx.x & 63 : threadIdx.x;
+  if constexpr (!WAVE) clear_sums(red[0], 8);
+  const int64_t step = (int64_t)gridDim.x * RPW;
+  // whole waves leave together (NT = 64), else the whole workgroup
+  int64_t r = (int64_t)blockIdx.x * RPW + (WAVE ? threadIdx.x >> 6 : 0);
+  if (r >= p.rows) return;
+  Chunk<T> nx[VPT], nr[VPT];
+  auto fetch = [&](int64_t row) {
+    const T* x = row_ptr<T>(p.x, row);
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) px[i].load(x, (i * NT + tid) * 8, p.cols);
-  if (p.r.p) {
-    Chunk<T> pr[VPT];
-    const T* res = row_ptr<T>(p.r, r);
+    for (int i = 0; i < VPT; ++i) nx[i].load(x, (i * NT + tid) * 8, p.cols);
+    if (!p.r.p) return;
+    const T* res = row_ptr<T>(p.r, row);
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) pr[i].load(res, (i * NT + tid) * 8, p.cols);
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      float a[8], b[8];
-      px[i].unpack(a);
-      pr[i].unpack(b);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) a[e] += b[e];
-      px[i].pack(a);
-    }
-  }
+    for (int i = 0; i < VPT; ++i) nr[i].load(res, (i * NT + tid) * 8, p.cols);
+  };
+  fetch(r);
   Chunk<WT> pw[VPT];
   if (p.w) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) pw[i].load(reinterpret_cast<const WT*>(p.w), (i * NT + tid) * 8, p.cols);
   }
-  float s = 0.f;
+  for (int flip = 0; r < p.rows; r += step, flip ^= 1) {
+    Chunk<T> px[VPT];
+    float s = 0.f;
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    float v[8];
-    px[i].unpack(v);
+    for (int i = 0; i < VPT; ++i) {
+      float a[8];
+      px[i] = nx[i];
+      if (p.r.p) {
+        float b[8];
+        px[i].unpack(a);
+        nr[i].unpack(b);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s += v[e] * v[e];
-  }
-  // every load of the row has landed behind this sum: h may lie in the residual's own buffer
-  s = block_sum<NT>(s, red);
-  const float rstd = 1.f / __builtin_sqrtf(s / p.n + p.eps);
-  if (p.h.p) {
-    T* h = row_ptr<T>(p.h, r);
+        for (int e = 0; e < 8; ++e) a[e] += b[e];
+        px[i].pack(a);
+      }
+      px[i].unpack(a);
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) px[i].store(h, (i * NT + tid) * 8, p.cols);
-  }
-  T* y = MX ? nullptr : row_ptr<T>(p.y, r);
-#pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    float f[8];
-    px[i].unpack(f);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] *= rstd;
-    if (p.w) {
-      float w[8];
-      pw[i].unpack(w);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] *= w[e];
+      for (int e = 0; e < 8; ++e) s += a[e] * a[e];
     }
-    rms_store<T, MX>(p, r, y, (i * NT + tid) * 8, f);
+    if (AHEAD && r + step < p.rows) fetch(r + step);
+    // every load of this row has landed behind the sum: h may lie in the residual's own buffer
+    s = block_sum<WAVE>(s, red[flip]);
+    const float rstd = 1.f / __builtin_sqrtf(s / p.n + p.eps);
+    if (p.h.p) {
+      T* h = row_ptr<T>(p.h, r);
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) px[i].store(h, (i * NT + tid) * 8, p.cols);
+    }
+    T* y = MX ? nullptr : row_ptr<T>(p.y, r);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      float f[8];
+      px[i].unpack(f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] *= rstd;
+      if (p.w) {
+        float w[8];
+        pw[i].unpack(w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] *= w[e];
+      }
+      rms_store<T, MX>(p, r, y, (i * NT + tid) * 8, f);
+    }
+    if (tid == 0) p.rstd[r] = rstd;
+    if (!AHEAD && r + step < p.rows) fetch(r + step);
   }
-  if (tid == 0) p.rstd[r] = rstd;
 }
 
 // Rows longer than the kernels above hold: a workgroup of 1024 threads reads x and r twice, the
 // second time from cache. A thread writes only elements of h that it alone reads.
 template <typename T, typename WT, bool MX>
 __global__ void __launch_bounds__(1024) rms_fwd_long(const RmsArgs p) {
-  __shared__ float red[16];
+  __shared__ f32x4 red[4];
   const int64_t r = block_id();
   if (r >= p.rows) return;
   const T* x = row_ptr<T>(p.x, r);
@@ -229,7 +266,7 @@ __global__ void __launch_bounds__(1024) rms_fwd_long(const RmsArgs p) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) s += f[e] * f[e];
   }
-  s = block_sum<1024>(s, red);
+  s = block_sum<false>(s, red);
   const float rstd = 1.f / __builtin_sqrtf(s / p.n + p.eps);
   T* h = p.h.p ? row_ptr<T>(p.h, r) : nullptr;
   T* y = MX ? nullptr : row_ptr<T>(p.y, r);
@@ -256,15 +293,17 @@ __global__ void __launch_bounds__(1024) rms_fwd_long(const RmsArgs p) {
 }
 
 // Backward: a workgroup walks every gridDim.x-th row (or four of them, NT = 64) with the next
-// row's h and dy already on their way (dh, which is needed last, with its own row), and keeps its columns' dw in registers; they leave once,
+// row's (16-bit types: the next two rows') h, dy and dh already on their way, and keeps its columns' dw in registers; they leave once,
 // as one part, for rms_dw_sum to add up.
-template <typename T, typename WT, int NT, int VPT>
-__global__ void __launch_bounds__(NT < 256 ? 256 : NT, NT >= 512 ? 4 : 1) rms_bwd_row(const RmsArgs p) {
-  constexpr int RPW = NT < 256 ? 256 / NT : 1;
-  constexpr bool AHEAD = NT * VPT < 2048;   // the longest rows leave no registers for the next one
-  __shared__ float red[2][16];
-  __shared__ f32x4 w[VPT][2][NT];           // the weight: kept out of the registers
-  const int tid = threadIdx.x % NT, sub = threadIdx.x / NT;
+template <typename T, typename WT, bool WAVE, int VPT>
+__global__ void __launch_bounds__(WAVE ? 256 : 1024, 4) rms_bwd_row(const RmsArgs p) {
+  constexpr int RPW = WAVE ? 4 : 1;
+  constexpr bool AHEAD = VPT == 1;          // the longest rows leave no registers for the next one
+  constexpr int DEEP = VPT == 1 && sizeof(T) == 2 ? 2 : 1;   // rows on their way
+  __shared__ f32x4 red[2][4];
+  extern __shared__ f32x4 w[];              // the weight, [VPT][2][threads of a row]: kept out of the registers
+  const int NT = WAVE ? 64 : blockDim.x, tid = WAVE ? threadIdx.x & 63 : threadIdx.x, sub = WAVE ? threadIdx.x >> 6 : 0;
+  if constexpr (!WAVE) clear_sums(red[0], 8);
   float aw[VPT][8];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
@@ -277,74 +316,105 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT, NT >= 512 ? 4 : 1) rms_bw
         pw.load(reinterpret_cast<const WT*>(p.w), (i * NT + tid) * 8, p.cols);
         pw.unpack(f);
       }
-      w[i][0][tid] = f32x4{f[0], f[1], f[2], f[3]};
-      w[i][1][tid] = f32x4{f[4], f[5], f[6], f[7]};
+      w[2 * i * NT + tid] = f32x4{f[0], f[1], f[2], f[3]};
+      w[(2 * i + 1) * NT + tid] = f32x4{f[4], f[5], f[6], f[7]};
     }
   }
   __syncthreads();
   const int64_t step = (int64_t)gridDim.x * RPW;
   int64_t r = (int64_t)blockIdx.x * RPW + sub;
-  Chunk<T> ph[VPT], pg[VPT], pd[VPT];
-  float rstd = 0.f;
-  auto fetch = [&](int64_t row) {
+  int flip = 0;
+  Chunk<T> ph[DEEP][VPT], pg[DEEP][VPT], pd[DEEP][VPT];
+  float rstd[DEEP];
+  auto fetch = [&](auto slot_c, int64_t row) {
+    constexpr int S = decltype(slot_c)::value;
+    if (row >= p.rows) return;
     const T* h = row_ptr<T>(p.h, row);
     const T* g = row_ptr<T>(p.dy, row);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      ph[i].load(h, (i * NT + tid) * 8, p.cols);
-      pg[i].load(g, (i * NT + tid) * 8, p.cols);
+      ph[S][i].load(h, (i * NT + tid) * 8, p.cols);
+      pg[S][i].load(g, (i * NT + tid) * 8, p.cols);
     }
-    rstd = p.rstd[row];
-  };
-  if (AHEAD && r < p.rows) fetch(r);
-  for (int flip = 0; r < p.rows; r += step, flip ^= 1) {
-    if (!AHEAD) fetch(r);
-    float xh[VPT][8], g[VPT][8], a = 0.f;
-    const float rs = rstd;
     if (p.dh.p) {
-      const T* d = row_ptr<T>(p.dh, r);
+      const T* d = row_ptr<T>(p.dh, row);
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) pd[i].load(d, (i * NT + tid) * 8, p.cols);
+      for (int i = 0; i < VPT; ++i) pd[S][i].load(d, (i * NT + tid) * 8, p.cols);
     }
+    rstd[S] = p.rstd[row];
+  };
+  // row r from slot S, whose next row is ordered while this one is added up
+  auto row = [&](auto slot_c) {
+    constexpr int S = decltype(slot_c)::value;
+    // this row, as loaded: unpacked twice, which takes fewer registers than to keep it unpacked
+    Chunk<T> h[VPT], dy[VPT], dh[VPT];
+    const float rs = rstd[S];
+    float a = 0.f;
+    auto terms = [&](int i, float (&xh)[8], float (&g)[8]) {
+      h[i].unpack(xh);
+      dy[i].unpack(g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) xh[e] *= rs;
+    };
+    auto weigh = [&](int i, float (&g)[8]) {
+      const f32x4 w0 = w[2 * i * NT + tid], w1 = w[(2 * i + 1) * NT + tid];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) g[e] *= e < 4 ? w0[e & 3] : w1[e & 3];
+    };
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      ph[i].unpack(xh[i]);
-      pg[i].unpack(g[i]);
-      const f32x4 w0 = w[i][0][tid], w1 = w[i][1][tid];
+      h[i] = ph[S][i];
+      dy[i] = pg[S][i];
+      dh[i] = pd[S][i];
+      float xh[8], g[8];
+      terms(i, xh, g);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        xh[i][e] *= rs;
-        aw[i][e] += g[i][e] * xh[i][e];
-        g[i][e] *= e < 4 ? w0[e & 3] : w1[e & 3];
-        a += g[i][e] * xh[i][e];
-      }
+      for (int e = 0; e < 8; ++e) aw[i][e] += g[e] * xh[e];
+      weigh(i, g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) a += g[e] * xh[e];
     }
-    if (AHEAD && r + step < p.rows) fetch(r + step);
-    a = block_sum<NT>(a, red[flip]) / p.n;
+    if (AHEAD) fetch(slot_c, r + DEEP * step);
+    a = block_sum<WAVE>(a, red[flip]) / p.n;
+    flip ^= 1;
     T* dx = row_ptr<T>(p.dx, r);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      float f[8], s[8];
+      float xh[8], g[8];
+      terms(i, xh, g);
+      weigh(i, g);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = rs * (g[i][e] - xh[i][e] * a);
+      for (int e = 0; e < 8; ++e) g[e] = rs * (g[e] - xh[e] * a);
       if (p.dh.p) {
-        pd[i].unpack(s);
+        dh[i].unpack(xh);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] += s[e];
+        for (int e = 0; e < 8; ++e) g[e] += xh[e];
       }
       Chunk<T> o;
-      o.pack(f);
+      o.pack(g);
       o.store(dx, (i * NT + tid) * 8, p.cols);
     }
+    r += step;
+  };
+  using S0 = std::integral_constant<int, 0>;
+  using S1 = std::integral_constant<int, DEEP - 1>;
+  if (AHEAD) {
+    fetch(S0{}, r);
+    if (DEEP > 1) fetch(S1{}, r + step);
+  }
+  while (r < p.rows) {
+    if (!AHEAD) fetch(S0{}, r);
+    row(S0{});
+    if (DEEP > 1 && r < p.rows) row(S1{});
   }
   if (!p.part) return;
   if constexpr (RPW > 1) {   // the four waves' sums meet in the first, in order
-    __shared__ float sum[RPW - 1][NT * VPT * 8];
+    __shared__ float sum[RPW - 1][64 * VPT * 8];
     if (sub) {
 #pragma unroll
       for (int i = 0; i < VPT; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum[sub - 1][(i * 8 + e) * NT + tid] = aw[i][e];
+        for (int e = 0; e < 8; ++e) sum[sub - 1][(i * 8 + e) * 64 + tid] = aw[i][e];
     }
     __syncthreads();
     if (sub) return;
@@ -352,7 +422,7 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT, NT >= 512 ? 4 : 1) rms_bw
 #pragma unroll
       for (int i = 0; i < VPT; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) aw[i][e] += sum[k][(i * 8 + e) * NT + tid];
+        for (int e = 0; e < 8; ++e) aw[i][e] += sum[k][(i * 8 + e) * 64 + tid];
   }
   float* part = p.part + (int64_t)blockIdx.x * p.cols;
 #pragma unroll
@@ -366,7 +436,7 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT, NT >= 512 ? 4 : 1) rms_bw
 // Longer rows: dx by rows, a workgroup of 1024 threads that reads them twice, and dw by columns.
 template <typename T, typename WT>
 __global__ void __launch_bounds__(1024) rms_dx_long(const RmsArgs p) {
-  __shared__ float red[16];
+  __shared__ f32x4 red[4];
   const int64_t r = block_id();
   if (r >= p.rows) return;
   const T* h = row_ptr<T>(p.h, r);
@@ -397,7 +467,7 @@ __global__ void __launch_bounds__(1024) rms_dx_long(const RmsArgs p) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) a += g[e] * xh[e];
   }
-  a = block_sum<1024>(a, red) / p.n;
+  a = block_sum<false>(a, red) / p.n;
   for (int c = threadIdx.x * 8; c < p.cols; c += 8192) {
     float xh[8], g[8];
     terms(c, xh, g);

@@ -7,6 +7,7 @@ library is missing this module raises; there is no fallback path.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 from typing import NamedTuple, Optional, Sequence
@@ -539,6 +540,10 @@ class Adamw8State(NamedTuple):
     root_scale: object
 
 
+def _dtype_of(t):
+    return t.dtype
+
+
 def adamw8_state(param) -> Adamw8State:
     """The state of a parameter before its first step (all zero)."""
     torch = _torch()
@@ -563,39 +568,41 @@ def adamw8_step(params, grads, states, *, lr: float, step: int, beta1: float = 0
         raise ValueError(f"{what}: step must count from 1, got {step}")
     if not 0 <= seed < 2 ** 64:
         raise ValueError(f"{what}: seed must fit 64 bits, got {seed}")
-    pdt = params[0].dtype
     code = dtype_code(params[0])
+    if set(map(len, states)) != {4}:
+        i = next(i for i, s in enumerate(states) if len(s) != 4)
+        raise ValueError(f"{what}: states[{i}] must hold four tensors, got {len(states[i])}")
+    # column by column: a list of some hundred tensors costs more in these checks than in its kernels
+    Tensor = torch.Tensor
+    numels = list(map(Tensor.numel, params))
+    blocks = [(count + MX_BLOCK - 1) // MX_BLOCK for count in numels]
     codes, scales = (torch.float8_e4m3fn, torch.uint8), (torch.float8_e8m0fnu, torch.uint8)
+    columns = (list(params), list(grads), *map(list, zip(*states)))
+    names = ("params", "grads", *Adamw8State._fields)
+    own = (params[0].dtype,)
+    for name, column, allowed, sizes in zip(names, columns, (own, own, codes, scales, codes, scales), (numels, numels, numels, blocks, numels, blocks)):
+        if not set(map(_dtype_of, column)).issubset(allowed):
+            i = next(i for i, t in enumerate(column) if t.dtype not in allowed)
+            raise TypeError(f"{what}: {name}[{i}] is {column[i].dtype}, expected {allowed[0]}")
+        if list(map(Tensor.numel, column)) != sizes:
+            i = next(i for i, t in enumerate(column) if t.numel() != sizes[i])
+            raise ValueError(f"{what}: {name}[{i}] has {column[i].numel()} elements, expected {sizes[i]}")
+        if not all(map(Tensor.is_contiguous, column)):
+            i = next(i for i, t in enumerate(column) if not t.is_contiguous())
+            raise ValueError(f"{what}: {name}[{i}] must be contiguous")
     device = params[0].device
-    for i, (p_, g_, s_) in enumerate(zip(params, grads, states)):
-        if p_.dtype != pdt:
-            raise TypeError(f"{what}: params[{i}] is {p_.dtype}; every parameter must be {pdt}")
-        if g_.dtype != pdt:
-            raise TypeError(f"{what}: grads[{i}] is {g_.dtype}, its parameter is {pdt}")
-        numel = p_.numel()
-        if g_.numel() != numel:
-            raise ValueError(f"{what}: grads[{i}] has {g_.numel()} elements, its parameter {numel}")
-        if len(s_) != 4:
-            raise ValueError(f"{what}: states[{i}] must hold four tensors, got {len(s_)}")
-        blocks = (numel + MX_BLOCK - 1) // MX_BLOCK
-        for t_, allowed, want in zip(s_, (codes, scales, codes, scales), (numel, blocks, numel, blocks)):
-            if t_.dtype not in allowed:
-                raise TypeError(f"{what}: a tensor of states[{i}] is {t_.dtype}, expected {allowed[0]}")
-            if t_.numel() != want:
-                raise ValueError(f"{what}: a tensor of states[{i}] has {t_.numel()} elements, expected {want}")
-        for t_ in (p_, g_, *s_):
-            if not t_.is_contiguous():
-                raise ValueError(f"{what}: the tensors must be contiguous")
     if not params[0].is_cuda:
         raise ValueError(f"{what}: tensors must be device tensors (got {device})")
-    for i, (p_, g_, s_) in enumerate(zip(params, grads, states)):
-        for t_ in (p_, g_, *s_):
-            if t_.device != device:
-                raise ValueError(f"{what}: a tensor of params, grads or states[{i}] is on {t_.device}, expected {device}")
-    arr = lambda ts: (ctypes.c_void_p * n)(*[t.data_ptr() for t in ts])
-    numels = (ctypes.c_int64 * n)(*[t.numel() for t in params])
+    index = params[0].get_device()
+    for name, column in zip(names, columns):
+        if set(map(Tensor.get_device, column)) != {index}:
+            i = next(i for i, t in enumerate(column) if t.get_device() != index)
+            raise ValueError(f"{what}: {name}[{i}] is on {column[i].device}, expected {device}")
+    pointers = ctypes.c_void_p * n
+    lists = [pointers.from_buffer(array.array("Q", map(Tensor.data_ptr, column))) for column in columns]
+    sizes = (ctypes.c_int64 * n).from_buffer(array.array("q", numels))
     ap = MnsAdamw8Params(lr, beta1, beta2, eps, weight_decay, step, 1 if bias_correction else 0, seed)
-    _launch(what, params[0], n, arr(params), arr(grads), *(arr(ts) for ts in zip(*states)), numels, code, ctypes.byref(ap))
+    _launch(what, params[0], n, *lists, sizes, code, ctypes.byref(ap))
     return params
 
 
