@@ -313,68 +313,58 @@ __global__ void __launch_bounds__(TilePP::NT, TilePP::OCC) expert_gemm_pp(const 
     __builtin_amdgcn_sched_barrier(0);
   };
   // Stores: 16 a wave whatever the tile (rows and columns outside fall to the range check); EX_GATE: 8, or 24
-  // with both products.
-  auto store_gated = [&](const ExpertTile& x) {
-    const int ln = opaque(lane), h = ln >> 5;
-    // eight columns of one row: runs of four from either half of the lanes
-    auto put = [&](const float (&v)[8], const __amdgpu_buffer_rsrc_t& rs, uint32_t off) {
-      uint32_t w[2][2];
+  // with both products. A block's lane holds runs of four columns of one of 32 rows; a swap of lane halves makes them
+  // eight, and a swap of rows of 16 lanes then puts the 32 columns of one row into four lanes, so that a
+  // store writes 64 bytes of each of 16 rows. value(e): column run e / 4 (8 apart, and 4 for the upper half), e % 4 of it.
+  auto put_block = [&](int ln, const __amdgpu_buffer_rsrc_t& rs, int r0, int c0, int ld, const ExpertTile& x, auto&& value) {
+    uint32_t w[2][4];                // [half of the columns][16 bytes]
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+    for (int q = 0; q < 2; ++q)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) w[u][e] = pack2<T>(v[u * 4 + 2 * e], v[u * 4 + 2 * e + 1]);
-      const auto s0 = __builtin_amdgcn_permlane32_swap(w[0][0], w[1][0], false, false);
-      const auto s1 = __builtin_amdgcn_permlane32_swap(w[0][1], w[1][1], false, false);
-      __builtin_amdgcn_raw_buffer_store_b128(u32x4{s0[0], s1[0], s0[1], s1[1]}, rs, off, 0, 0);
-    };
-    auto each = [&](const char* to, int64_t ld, auto&& value) {
-      const __amdgpu_buffer_rsrc_t rs = make_rsrc(uniform(to + ((int64_t)x.row0 * ld + x.col0) * 2), 0x7ffffff0u);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = wm * 128 + i * 32 + (ln & 31);
-        const bool in = x.row0 + r < x.m;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int c = wn * 32 + q * 16 + h * 8;
-          float v[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = value(i, q * 8 + e);
-          put(v, rs, in && x.col0 + c < p.n ? (uint32_t)(r * (int)ld + c) * 2 : OOB);
-        }
+      for (int e = 0; e < 2; ++e) {
+        const auto s = __builtin_amdgcn_permlane32_swap(pack2<T>(value(q * 8 + 2 * e), value(q * 8 + 2 * e + 1)),
+                                                        pack2<T>(value(q * 8 + 4 + 2 * e), value(q * 8 + 4 + 2 * e + 1)), false, false);
+        w[q][e] = s[0];
+        w[q][2 + e] = s[1];
       }
-    };
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const auto s = __builtin_amdgcn_permlane16_swap(w[0][e], w[1][e], false, false);
+      w[0][e] = s[0];
+      w[1][e] = s[1];
+    }
+    const int c = c0 + ((ln >> 4) & 1) * 16 + (ln >> 5) * 8;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int r = r0 + k * 16 + (ln & 15);
+      const uint32_t off = x.row0 + r < x.m && x.col0 + c < p.n ? (uint32_t)(r * ld + c) * 2 : OOB;
+      __builtin_amdgcn_raw_buffer_store_b128(u32x4{w[k][0], w[k][1], w[k][2], w[k][3]}, rs, off, 0, 0);
+    }
+  };
+  auto result = [&](const char* to, int64_t ld, const ExpertTile& x) {
+    return make_rsrc(uniform(to + ((int64_t)x.row0 * ld + x.col0) * 2), 0x7ffffff0u);
+  };
+  auto store = [&](const ExpertTile& x) {
+    const int ln = opaque(lane);
     if constexpr (MODE == EX_GATE) {
+      auto each = [&](const char* to, int64_t ld, auto&& value) {
+        const __amdgpu_buffer_rsrc_t rs = result(to, ld, x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) put_block(ln, rs, wm * 128 + i * 32, wn * 32, (int)ld, x, [&](int e) { return value(i, e); });
+      };
       if (x.c2) {
         each(x.c2, p.ldc2, [&](int i, int e) { return acc[i][0][e]; });
         each(x.c3, p.ldc3, [&](int i, int e) { return acc[i][1][e]; });
       }
       each(x.c, p.ldc, [&](int i, int e) { return activate(acc[i][0][e], p.act) * acc[i][1][e]; });
-    }
-  };
-  auto store = [&](const ExpertTile& x) {
-    const int ln = opaque(lane), h = ln >> 5;
-    const int64_t ldc = row_step<MODE>(p, x);
-    const __amdgpu_buffer_rsrc_t rs = make_rsrc(uniform(x.c + ((int64_t)x.row0 * ldc + x.col0) * 2), 0x7ffffff0u);
+    } else {
+      const int64_t ldc = row_step<MODE>(p, x);
+      const __amdgpu_buffer_rsrc_t rs = result(x.c, ldc, x);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = wm * 128 + i * 32 + (ln & 31);
-      const bool in = x.row0 + r < x.m;
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int c = wn * 64 + j * 32 + q * 16 + h * 8;
-          uint32_t w[2][2];
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) w[u][e] = pack2<T>(acc[i][j][q * 8 + u * 4 + 2 * e], acc[i][j][q * 8 + u * 4 + 2 * e + 1]);
-          const auto s0 = __builtin_amdgcn_permlane32_swap(w[0][0], w[1][0], false, false);
-          const auto s1 = __builtin_amdgcn_permlane32_swap(w[0][1], w[1][1], false, false);
-          const u32x4 v = {s0[0], s1[0], s0[1], s1[1]};
-          const uint32_t off = in && x.col0 + c < p.n ? (uint32_t)(r * (int)ldc + c) * 2 : OOB;
-          __builtin_amdgcn_raw_buffer_store_b128(v, rs, off, 0, 0);
-        }
+        for (int j = 0; j < 2; ++j)
+          put_block(ln, rs, wm * 128 + i * 32, wn * 64 + j * 32, (int)ldc, x, [&](int e) { return acc[i][j][e]; });
     }
   };
   using S0 = std::integral_constant<int, 0>;
@@ -425,8 +415,7 @@ __global__ void __launch_bounds__(TilePP::NT, TilePP::OCC) expert_gemm_pp(const 
       }
       toggle = -toggle;
     }
-    if constexpr (MODE == EX_GATE) store_gated(x);
-    else store(x);
+    store(x);
     __builtin_amdgcn_sched_barrier(0);
     clear();
     begin = false;
