@@ -109,10 +109,14 @@ __host__ __device__ inline TileAt tile_at(int r, int tm, int tiles_n) {
   return {band * EXPERT_BAND + r % high, r / high};
 }
 
+// What a tile of a weight gradient costs, in stages of 64 rows: three more than it has, for its stores and
+// the tile's begin (one MI355X, 256 x 256 tiles: 1.66 us a stage, 5.3 us a tile without any).
+__host__ __device__ inline int dw_cost(int rows) { return (rows + 63) / 64 + 3; }
+
 // first[e] = tile rows (of BM) of the experts before e, as list_rows cuts them, e = 0 .. E + 1: entry
 // E begins the tile rows over the rows of nobody, entry E + 1 is the total. rows (ROWS): beginning and number of each
-// expert's rows. Ends with a barrier.
-template <int NT, int BM, bool ROWS = false>
+// expert's rows. COST: first[e] = what a tile of each of the experts before e costs. Ends with a barrier.
+template <int NT, int BM, bool ROWS = false, bool COST = false>
 __device__ inline void expert_tiles(const ExpertArgs& p, int* first, int* wsum, int2* rows = nullptr) {
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   int base = 0;
@@ -122,7 +126,7 @@ __device__ inline void expert_tiles(const ExpertArgs& p, int* first, int* wsum, 
     if (e <= p.experts) {
       int lo, hi;
       expert_rows(p, e, &lo, &hi);
-      n = (hi - lo + BM - 1) / BM;
+      n = COST ? (e < p.experts ? dw_cost(hi - lo) : 0) : (hi - lo + BM - 1) / BM;
       if constexpr (ROWS) rows[e] = int2{lo, hi - lo};
     }
     int run = n;
@@ -139,8 +143,8 @@ __device__ inline void expert_tiles(const ExpertArgs& p, int* first, int* wsum, 
       all += wsum[w];
     }
     base += all;
-    if (e <= p.experts) first[e] = list_rows(before + run - n, p.tiles_n);
-    if (e == p.experts) first[e + 1] = list_rows(before + run, p.tiles_n);
+    if (e <= p.experts) first[e] = COST ? before + run - n : list_rows(before + run - n, p.tiles_n);
+    if (e == p.experts) first[e + 1] = COST ? before + run : list_rows(before + run, p.tiles_n);
     __syncthreads();
   }
 }
@@ -204,6 +208,27 @@ __device__ inline ExpertList expert_list(const ExpertArgs& p, const int* first) 
   const int xcd = blockIdx.x & 7;
   const int lo = (int)(total * xcd / 8);
   return {wave_uniform(lo), wave_uniform((int)(total * (xcd + 1) / 8) - lo)};
+}
+
+// The same for a weight gradient whose experts' tiles cost as COST says: eight parts of equal cost, so that
+// experts with many rows do not fall to one XCD. cost_begin: where part x begins, in tiles; first, T (tiles
+// per expert) as above; which: the expert that the part begins in.
+__host__ __device__ inline int64_t cost_target(const int* first, int experts, int64_t T, int x) { return first[experts] * T * x / 8; }
+__host__ __device__ inline int cost_begin(const int* first, int experts, int64_t T, int x, int which) {
+  if (which >= experts) return (int)(experts * T);
+  return (int)(which * T + (cost_target(first, experts, T, x) - first[which] * T) / (first[which + 1] - first[which]));
+}
+__device__ inline ExpertList cost_list(const ExpertArgs& p, const int* first, int64_t T) {
+  const int xcd = blockIdx.x & 7, lane = threadIdx.x & 63;
+  int begin[2];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    const int64_t target = cost_target(first, p.experts, T, xcd + s);
+    int e = 0;
+    for (int i = lane; i - lane < p.experts; i += 64) e += __builtin_popcountll(__ballot(i < p.experts && first[i + 1] * T <= target));
+    begin[s] = wave_uniform(cost_begin(first, p.experts, T, xcd + s, e));
+  }
+  return {begin[0], begin[1] - begin[0]};
 }
 
 // Tile t of an XCD's list. Tiles go expert by expert, within one in bands (tile_at), so that the

@@ -97,8 +97,10 @@ __global__ void __launch_bounds__(TilePP::NT, TilePP::OCC) expert_gemm_pp(const 
   typedef FragOf<T> F;
   const int wave = wave_uniform(threadIdx.x >> 6), wm = wave >> 2, wn = wave & 3;
   const int lane = threadIdx.x & 63;
-  expert_tiles<NT, TilePP::BM, true>(p, first, wsum, rows);
-  const ExpertList l = expert_list<MODE, TilePP>(p, first);
+  expert_tiles<NT, TilePP::BM, true, ex_dw(MODE)>(p, first, wsum, rows);
+  ExpertList l;
+  if constexpr (ex_dw(MODE)) l = cost_list(p, first, (int64_t)((p.m + 255) / 256) * p.tiles_n * (MODE == EX_DW2 ? 2 : 1));
+  else l = expert_list<MODE, TilePP>(p, first);
   const int step = gridDim.x >> 3;
   int t = blockIdx.x >> 3;
   if (t >= l.n) return;
