@@ -430,16 +430,21 @@ MNS_API int adamw8_step(int ntensors, void* const* params, const void* const* gr
  * Wg, Wu: batches of E matrices N x K (the Muon step's layout). G, U: receive gate and up for the backward
  * pass, or both NULL. All of one dtype; the activation takes fp32 sums. offsets as in expert_matmul; NULL with
  * E = 1: every row is the one expert's. Rows of no expert get zeros.
+ * ws: a dense call (offsets NULL) in 16 bits may take a workspace, in which the tiles of a last round that would leave
+ * most CUs idle are cut along the contraction; without it, or with a smaller one, the call runs uncut.
  *   MNS_ACT_SILU  g / (1 + exp(-g));  MNS_ACT_GELU  g (1 + erf(g / sqrt(2))) / 2;  MNS_ACT_RELU  max(g, 0)
  */
 #define MNS_ACT_SILU 0
 #define MNS_ACT_GELU 1
 #define MNS_ACT_RELU 2
 MNS_API int expert_gated(const mns_tensor* X, const mns_tensor* Wg, const mns_tensor* Wu, const int32_t* offsets, int32_t act,
-                         const mns_tensor* H, const mns_tensor* G, const mns_tensor* U, void* stream);
+                         const mns_tensor* H, const mns_tensor* G, const mns_tensor* U, void* ws, size_t ws_bytes, void* stream);
 
-/* Workspace bytes of expert_gated_backward (host-only). */
-MNS_API int mns_expert_gated_workspace_bytes(int64_t rows, int64_t inner, int32_t dtype, size_t* bytes);
+/*
+ * Workspace bytes of expert_gated (none but for dense calls) and of expert_gated_backward. experts: 0 for a dense call
+ * (offsets NULL). The backward pass needs 2 * rows * inner elements of it; the rest is for a dense call's split.
+ */
+MNS_API int mns_expert_gated_workspace_bytes(int64_t rows, int64_t inner, int32_t experts, int32_t dtype, size_t* forward, size_t* backward);
 
 /*
  * Its gradients, from gate and up as kept: dgate = dH * up * act'(gate), dup = dH * act(gate), rounded to the

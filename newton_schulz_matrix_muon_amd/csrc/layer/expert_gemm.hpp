@@ -60,6 +60,8 @@ struct GatedArgs : ExpertArgs {
   char* C2; int64_t ldc2, sC2;
   char* C3; int64_t ldc3;
   int act;
+  // expert_gemm_pp, SPLIT: sums of the parts, 256 x 256 floats a workgroup, and workgroups per XCD
+  float* parts; int wgs;
 };
 enum { ACT_SILU = 0, ACT_GELU = 1, ACT_RELU = 2 };
 template <int MODE> struct ArgsOf { typedef ExpertArgs type; };

@@ -85,7 +85,49 @@ __device__ inline FragOf<T> read_major(const char* at) {
   return __builtin_bit_cast(FragOf<T>, (s16x8)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-template <int MODE, typename T>
+// A block's 32 columns of 32 rows to the result at (r0, c0) of the tile. A lane holds runs of four columns of one row;
+// a swap of lane halves makes them eight, and a swap of rows of 16 lanes then puts the 32 columns of one row
+// into four lanes, so that a store writes 64 bytes of each of 16 rows. value(e): column run e / 4 (8 apart, and 4
+// for the upper half), e % 4 of it.
+template <typename T, class V>
+__device__ inline void store_block(int ln, const __amdgpu_buffer_rsrc_t& rs, int r0, int c0, int ld, const ExpertTile& x, int n, V&& value) {
+  uint32_t w[2][4];                  // [half of the columns][16 bytes]
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const auto s = __builtin_amdgcn_permlane32_swap(pack2<T>(value(q * 8 + 2 * e), value(q * 8 + 2 * e + 1)),
+                                                      pack2<T>(value(q * 8 + 4 + 2 * e), value(q * 8 + 4 + 2 * e + 1)), false, false);
+      w[q][e] = s[0];
+      w[q][2 + e] = s[1];
+    }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const auto s = __builtin_amdgcn_permlane16_swap(w[0][e], w[1][e], false, false);
+    w[0][e] = s[0];
+    w[1][e] = s[1];
+  }
+  const int c = c0 + ((ln >> 4) & 1) * 16 + (ln >> 5) * 8;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int r = r0 + k * 16 + (ln & 15);
+    const uint32_t off = x.row0 + r < x.m && x.col0 + c < n ? (uint32_t)(r * ld + c) * 2 : OOB;
+    __builtin_amdgcn_raw_buffer_store_b128(u32x4{w[k][0], w[k][1], w[k][2], w[k][3]}, rs, off, 0, 0);
+  }
+}
+
+// The last round of an XCD's list where it leaves at least half of the workgroups idle (SPLIT): each of its
+// `over` tiles is cut along the contraction into `parts` that as many workgroups take, and expert_split_sum adds
+// them up. full: tiles of the rounds before.
+struct LastRound {
+  int full, over, parts;
+};
+__host__ __device__ inline LastRound last_round(int tiles, int wgs) {
+  const int over = tiles % wgs, parts = over ? wgs / over : 1;
+  return parts < 2 ? LastRound{tiles, 0, 1} : LastRound{tiles - over, over, parts};
+}
+
+template <int MODE, typename T, bool SPLIT = false>
 __global__ void __launch_bounds__(TilePP::NT, TilePP::OCC) expert_gemm_pp(const typename ArgsOf<MODE>::type p) {
   constexpr int BK = 64, OPB = TilePP::OPB, NT = TilePP::NT;
   constexpr bool AKM = ex_dw(MODE), BKM = !ex_fwd(MODE);
@@ -103,7 +145,25 @@ __global__ void __launch_bounds__(TilePP::NT, TilePP::OCC) expert_gemm_pp(const 
   else l = expert_list<MODE, TilePP>(p, first);
   const int step = gridDim.x >> 3;
   int t = blockIdx.x >> 3;
-  if (t >= l.n) return;
+  const int own = t;
+  LastRound last{l.n, 0, 1};
+  if constexpr (SPLIT) {
+    last = last_round(l.n, step);
+    if (own >= last.over * last.parts && own >= last.full) return;
+  } else if (t >= l.n) {
+    return;
+  }
+  // the workgroup's tile in the round that begins with tile at - own: its place in the list, or -1
+  auto tile_of = [&](int at) {
+    if (!SPLIT || at < last.full) return at < l.n ? at : -1;
+    return at == last.full + own && own < last.over * last.parts ? last.full + own / last.parts : -1;
+  };
+  // the stages of it that the workgroup takes
+  auto stages_of = [&](int at, int nk, int* begin, int* end) {
+    const bool cut = SPLIT && at >= last.full;
+    *begin = cut ? nk * (own % last.parts) / last.parts : 0;
+    *end = cut ? nk * (own % last.parts + 1) / last.parts : nk;
+  };
 
   // ------------------------------------------------------------------ the stages on their way
   // A piece is 1 KB of an operand's stage: rows 8 i .. 8 i + 7 of a contiguous operand, contraction
@@ -132,6 +192,7 @@ __global__ void __launch_bounds__(TilePP::NT, TilePP::OCC) expert_gemm_pp(const 
   int klen = 0, k0 = 0;              // its contraction length, the stage being issued
   int efrom = 0, islot = 1;
   bool live = true;
+  int left = 0;                      // SPLIT: stages of the tile that are not issued yet
   const uint32_t lds0 = (uint32_t)(size_t)(__attribute__((address_space(3))) char*)lds;
   auto offset = [&](int l0, bool km, int rb, int ext, int i) {
     if (km) {
@@ -156,7 +217,7 @@ __global__ void __launch_bounds__(TilePP::NT, TilePP::OCC) expert_gemm_pp(const 
     k0 += BK;
     srca += AKM ? (int64_t)BK * rba : BK * 2;
     srcb += BKM ? (int64_t)BK * rbb : BK * 2;
-    if (MODE == EX_DX2 && k0 >= klen && follows) {
+    auto follow = [&]() {              // EX_DX2: to the second contraction
       follows = false;
       k0 = 0;
       srca = later_a;
@@ -165,13 +226,19 @@ __global__ void __launch_bounds__(TilePP::NT, TilePP::OCC) expert_gemm_pp(const 
       const int l0 = opaque(lane);
 #pragma unroll
       for (int j = 0; j < 4; ++j) offb[j] = offset_b(l0, extb, j);
-    } else if (k0 >= klen) {
+    };
+    bool done = k0 >= klen;
+    if constexpr (SPLIT) done = --left <= 0;
+    if (MODE == EX_DX2 && k0 >= klen && follows && !(SPLIT && done)) {
+      follow();
+    } else if (done) {
       k0 = klen = 0;
       while (live && klen == 0) {
         ti += step;
-        live = ti < l.n;
+        const int place = tile_of(ti);
+        live = place >= 0;
         if (!live) break;
-        const ExpertTile x = expert_tile<MODE, T, TilePP, true>(p, first, l, ti, &efrom, rows);
+        const ExpertTile x = expert_tile<MODE, T, TilePP, true>(p, first, l, place, &efrom, rows);
         klen = x.k;
         if (klen > 0) {
           srca = x.a + (AKM ? (int64_t)x.row0 * 2 : (int64_t)x.row0 * rba);
@@ -194,6 +261,19 @@ __global__ void __launch_bounds__(TilePP::NT, TilePP::OCC) expert_gemm_pp(const 
           for (int j = 0; j < 4; ++j) {
             offa[j] = offset(l0, AKM, rba, exta, a_piece(j));
             offb[j] = offset_b(l0, extb, j);
+          }
+          if constexpr (SPLIT) {
+            const int nh = (klen + BK - 1) / BK;
+            int begin, end;
+            stages_of(ti, MODE == EX_DX2 ? 2 * nh : nh, &begin, &end);
+            left = end - begin;
+            if (MODE == EX_DX2 && begin >= nh) {
+              follow();
+              begin -= nh;
+            }
+            k0 = begin * BK;
+            srca += AKM ? (int64_t)k0 * rba : (int64_t)k0 * 2;
+            srcb += BKM ? (int64_t)k0 * rbb : (int64_t)k0 * 2;
           }
         }
       }
@@ -315,33 +395,9 @@ __global__ void __launch_bounds__(TilePP::NT, TilePP::OCC) expert_gemm_pp(const 
     __builtin_amdgcn_sched_barrier(0);
   };
   // Stores: 16 a wave whatever the tile (rows and columns outside fall to the range check); EX_GATE: 8, or 24
-  // with both products. A block's lane holds runs of four columns of one of 32 rows; a swap of lane halves makes them
-  // eight, and a swap of rows of 16 lanes then puts the 32 columns of one row into four lanes, so that a
-  // store writes 64 bytes of each of 16 rows. value(e): column run e / 4 (8 apart, and 4 for the upper half), e % 4 of it.
+  // with both products.
   auto put_block = [&](int ln, const __amdgpu_buffer_rsrc_t& rs, int r0, int c0, int ld, const ExpertTile& x, auto&& value) {
-    uint32_t w[2][4];                // [half of the columns][16 bytes]
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const auto s = __builtin_amdgcn_permlane32_swap(pack2<T>(value(q * 8 + 2 * e), value(q * 8 + 2 * e + 1)),
-                                                        pack2<T>(value(q * 8 + 4 + 2 * e), value(q * 8 + 4 + 2 * e + 1)), false, false);
-        w[q][e] = s[0];
-        w[q][2 + e] = s[1];
-      }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const auto s = __builtin_amdgcn_permlane16_swap(w[0][e], w[1][e], false, false);
-      w[0][e] = s[0];
-      w[1][e] = s[1];
-    }
-    const int c = c0 + ((ln >> 4) & 1) * 16 + (ln >> 5) * 8;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int r = r0 + k * 16 + (ln & 15);
-      const uint32_t off = x.row0 + r < x.m && x.col0 + c < p.n ? (uint32_t)(r * ld + c) * 2 : OOB;
-      __builtin_amdgcn_raw_buffer_store_b128(u32x4{w[k][0], w[k][1], w[k][2], w[k][3]}, rs, off, 0, 0);
-    }
+    store_block<T>(ln, rs, r0, c0, ld, x, p.n, value);
   };
   auto result = [&](const char* to, int64_t ld, const ExpertTile& x) {
     return make_rsrc(uniform(to + ((int64_t)x.row0 * ld + x.col0) * 2), 0x7ffffff0u);
@@ -386,9 +442,16 @@ __global__ void __launch_bounds__(TilePP::NT, TilePP::OCC) expert_gemm_pp(const 
   int toggle = OPB;
   bool begin = true;                 // no stores yet
   clear();
-  for (; t < l.n; t += step) {
-    const ExpertTile x = expert_tile<MODE, T, TilePP, true>(p, first, l, t, &cfrom, rows);
-    const int nk = (x.k + BK - 1) / BK * (MODE == EX_DX2 ? 2 : 1);
+  for (;; t += step) {
+    const int place = tile_of(t);
+    if (place < 0) break;
+    const ExpertTile x = expert_tile<MODE, T, TilePP, true>(p, first, l, place, &cfrom, rows);
+    int nk = (x.k + BK - 1) / BK * (MODE == EX_DX2 ? 2 : 1);
+    if constexpr (SPLIT) {
+      int begin, end;
+      stages_of(t, nk, &begin, &end);
+      nk = end - begin;
+    }
     // blocks whose rows all lie outside are not computed (the barriers stay)
     const bool busy0 = x.row0 + wm * 128 < x.m, busy1 = x.row0 + wm * 128 + (AKM ? 0 : 64) < x.m;
     for (int kt = 0; kt < nk; ++kt) {
@@ -417,6 +480,22 @@ __global__ void __launch_bounds__(TilePP::NT, TilePP::OCC) expert_gemm_pp(const 
       }
       toggle = -toggle;
     }
+    if constexpr (SPLIT) {
+      if (t >= last.full) {            // the last: its sums as they lie in the registers
+        const __amdgpu_buffer_rsrc_t rs = make_rsrc(uniform(reinterpret_cast<const char*>(p.parts) + (int64_t)blockIdx.x * (256 * 256 * 4)), 256 * 256 * 4);
+        const uint32_t at = opaque((wave * 64 + lane) * 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const f32x4 v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+              __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rs, at, ((i * 2 + j) * 4 + q) * NT * 16, 0);
+            }
+        break;
+      }
+    }
     store(x);
     __builtin_amdgcn_sched_barrier(0);
     clear();
@@ -424,6 +503,49 @@ __global__ void __launch_bounds__(TilePP::NT, TilePP::OCC) expert_gemm_pp(const 
   }
   if (!wm) barrier_nofence();
   wait_vmcnt<0>();                   // the last pieces land before the LDS is given back
+}
+
+// The parts of a cut tile added up in order, and the tile's epilogue: a wave takes 32 rows of one wave's share of
+// a tile.
+template <int MODE, typename T>
+__global__ void __launch_bounds__(64) expert_split_sum(const typename ArgsOf<MODE>::type p) {
+  __shared__ int first[EXPERT_MAX + 2];
+  __shared__ int2 rows[EXPERT_MAX + 1];
+  __shared__ int wsum[1];
+  expert_tiles<64, TilePP::BM, true>(p, first, wsum, rows);
+  const ExpertList l = expert_list<MODE, TilePP>(p, first);
+  const LastRound last = last_round(l.n, p.wgs);
+  const int i = (blockIdx.x >> 3) & 3, wave = (blockIdx.x >> 5) & 7, q = blockIdx.x >> 8, lane = threadIdx.x;
+  if (q >= last.over) return;
+  int from = 0;
+  const ExpertTile x = expert_tile<MODE, T, TilePP, true>(p, first, l, last.full + q, &from, rows);
+  f32x4 acc[2][4];
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) acc[j][r] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const f32x4* parts = reinterpret_cast<const f32x4*>(p.parts) + wave * 64 + lane;
+  for (int s = 0; s < last.parts; ++s) {
+    const f32x4* part = parts + (int64_t)((q * last.parts + s) * 8 + (blockIdx.x & 7)) * (256 * 64);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[j][r] += part[((i * 2 + j) * 4 + r) * TilePP::NT];
+  }
+  const int r0 = (wave >> 2) * 128 + i * 32, wn = wave & 3;
+  auto result = [&](const char* to, int64_t ld) { return make_rsrc(uniform(to + ((int64_t)x.row0 * ld + x.col0) * 2), 0x7ffffff0u); };
+  if constexpr (MODE == EX_GATE) {
+    if (x.c2) {
+      store_block<T>(lane, result(x.c2, p.ldc2), r0, wn * 32, (int)p.ldc2, x, p.n, [&](int e) { return acc[0][e >> 2][e & 3]; });
+      store_block<T>(lane, result(x.c3, p.ldc3), r0, wn * 32, (int)p.ldc3, x, p.n, [&](int e) { return acc[1][e >> 2][e & 3]; });
+    }
+    store_block<T>(lane, result(x.c, p.ldc), r0, wn * 32, (int)p.ldc, x, p.n,
+                   [&](int e) { return activate(acc[0][e >> 2][e & 3], p.act) * acc[1][e >> 2][e & 3]; });
+  } else {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      store_block<T>(lane, result(x.c, p.ldc), r0, wn * 64 + j * 32, (int)p.ldc, x, p.n, [&](int e) { return acc[j][e >> 2][e & 3]; });
+  }
 }
 
 }  // namespace mns

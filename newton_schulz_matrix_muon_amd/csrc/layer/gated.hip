@@ -60,6 +60,34 @@ int run_pingpong(GatedArgs a, int dt, hipStream_t s) {
   });
 }
 
+// A dense product whose last round of 256 x 256 tiles would leave half of the CUs idle or more: that round's tiles are
+// cut along the contraction (last_round). The workspace has room for a part of every workgroup.
+int64_t split_bytes() { return (int64_t)round_up(device_cus(), 8) * 256 * 256 * 4; }
+
+template <int MODE>
+int run_split_pingpong(GatedArgs a, int dt, hipStream_t s) {
+  a.tiles_n = tile_columns<MODE, TilePP>(a);
+  a.wgs = (int)round_up(device_cus(), 8) / 8;
+  const unsigned g = 8 * a.wgs;
+  auto both = [&](auto x) {
+    using T = decltype(x);
+    if (int st = launch(K_EXPERT_GEMM, s, [&] { hipLaunchKernelGGL((expert_gemm_pp<MODE, T, true>), dim3(g), dim3(TilePP::NT), 0, s, a); })) return st;
+    return launch(K_EXPERT_GEMM, s, [&] { hipLaunchKernelGGL((expert_split_sum<MODE, T>), dim3(256 * (a.wgs / 2)), dim3(64), 0, s, a); });
+  };
+  return dt == BF16 ? both(__bf16{}) : both(_Float16{});
+}
+
+// Whether cutting the last round is worth its sum (about 25 us): host arithmetic on a dense product's tiles.
+template <int MODE>
+bool split_pays(const GatedArgs& a) {
+  if (MODE == EX_DW2 || !a.parts || a.offsets) return false;
+  const int wgs = (int)round_up(device_cus(), 8) / 8;
+  const int64_t tiles = (a.rows + 255) / 256 * tile_columns<MODE, TilePP>(a);
+  const LastRound last = last_round((int)((tiles + 7) / 8), wgs);
+  const int64_t stages = (a.k + 63) / 64 * (MODE == EX_DX2 ? 2 : 1);
+  return last.parts > 1 && stages >= 32;
+}
+
 int run_few(const GatedArgs& a, int dt, int fit, hipStream_t s) {
   const dim3 g((a.n + 15) / 16, (unsigned)std::min<int64_t>(a.experts, a.rows) + 1);
   return by_type(dt, [&](auto x) {
@@ -102,6 +130,8 @@ int run_product(const GatedArgs& a, int dt, bool vec, hipStream_t s) {
     if (few_rows(a, dt, fit)) return run_few(a, dt, fit, s);
   const bool whole = vec && a.c_vec && a.n % 8 == 0 && dt != F32 && a.n > (MODE == EX_GATE ? 64 : 128) && (!ex_dw(MODE) || a.m > 128);
   const int64_t high = ex_dw(MODE) ? tile_rows<MODE, TilePP>(a) : a.rows / 256 + std::min<int64_t>(a.experts, a.rows);
+  if constexpr (MODE != EX_DW2)
+    if (whole && split_pays<MODE>(a) && !split_tiles<MODE>(a, dt)) return run_split_pingpong<MODE>(a, dt, s);
   if (whole && 2 * high * tile_columns<MODE, TilePP>(a) >= device_cus()) return run_pingpong<MODE>(a, dt, s);
   if (split_tiles<MODE>(a, dt)) return run_staged<MODE, Tile64, 8>(a, dt, fit, s);
   return run_staged<MODE, Tile128, 1>(a, dt, fit, s);
@@ -154,18 +184,33 @@ int64_t inner_bytes(int64_t rows, int64_t n, int dt) { return round_up(rows * in
 // ==========================================================================================
 extern "C" {
 
+int mns_expert_gated_workspace_bytes(int64_t rows, int64_t inner, int32_t experts, int32_t dtype, size_t* forward, size_t* backward) {
+  if (!forward || !backward) return MNS_ERR_ARG;
+  if (!valid_dtype(dtype)) return MNS_ERR_DTYPE;
+  if (rows < 0 || rows > kMaxRows || inner < 1 || inner > kMaxCols || experts < 0 || experts > EXPERT_MAX) return MNS_ERR_SHAPE;
+  *forward = rows && !experts && dtype != F32 ? (size_t)split_bytes() : 0;
+  *backward = (size_t)(2 * inner_bytes(rows, inner, dtype)) + *forward;
+  return MNS_OK;
+}
+
 int expert_gated(const mns_tensor* X, const mns_tensor* Wg, const mns_tensor* Wu, const int32_t* offsets, int32_t act, const mns_tensor* H,
-                 const mns_tensor* G, const mns_tensor* U, void* stream) {
+                 const mns_tensor* G, const mns_tensor* U, void* ws, size_t ws_bytes, void* stream) {
   if (int st = check_pair(X, Wg, Wu, offsets, act)) return st;
   if ((G == nullptr) != (U == nullptr)) return MNS_ERR_ARG;
   for (const mns_tensor* t : {H, G ? G : H, U ? U : H})
     if (int st = check_inner(t, X, Wg)) return st;
   const Span none = span(static_cast<const void*>(nullptr), 0);
-  if (clash({span(H), G ? span(G) : none, U ? span(U) : none}, {span(X), span(Wg), span(Wu), offsets_span(offsets, Wg->batch)})) return MNS_ERR_ARG;
+  // the workspace is for dense calls alone, and they do without
+  const bool room = ws && !offsets && X->dtype != F32 && ws_bytes >= (size_t)split_bytes();
+  if (room && !aligned16(ws)) return MNS_ERR_WORKSPACE;
+  if (clash({span(H), G ? span(G) : none, U ? span(U) : none, room ? span(ws, split_bytes()) : none},
+            {span(X), span(Wg), span(Wu), offsets_span(offsets, Wg->batch)}))
+    return MNS_ERR_ARG;
   if (!X->rows) return MNS_OK;
   GatedArgs a = gated_args(X, Wg, Wu, H, offsets, (int)Wg->batch, X->rows);
   a.k = (int)X->cols;
   a.act = act;
+  a.parts = room ? reinterpret_cast<float*>(ws) : nullptr;
   if (G) {
     a.C2 = reinterpret_cast<char*>(G->ptr);
     a.ldc2 = G->ld;
@@ -174,14 +219,6 @@ int expert_gated(const mns_tensor* X, const mns_tensor* Wg, const mns_tensor* Wu
     a.c_vec = a.c_vec && vec_out(G) && vec_out(U);
   }
   return run_product<EX_GATE>(a, X->dtype, vec_rows(X) && vec_rows(Wg) && vec_rows(Wu), as_stream(stream));
-}
-
-int mns_expert_gated_workspace_bytes(int64_t rows, int64_t inner, int32_t dtype, size_t* bytes) {
-  if (!bytes) return MNS_ERR_ARG;
-  if (!valid_dtype(dtype)) return MNS_ERR_DTYPE;
-  if (rows < 0 || rows > kMaxRows || inner < 1 || inner > kMaxCols) return MNS_ERR_SHAPE;
-  *bytes = (size_t)(2 * inner_bytes(rows, inner, dtype));
-  return MNS_OK;
 }
 
 int expert_gated_backward(const mns_tensor* dH, const mns_tensor* X, const mns_tensor* Wg, const mns_tensor* Wu, const mns_tensor* G,
@@ -198,8 +235,9 @@ int expert_gated_backward(const mns_tensor* dH, const mns_tensor* X, const mns_t
   if ((dX && !same_rows(dX, X)) || (dWg && (!same_rows(dWg, Wg) || !same_rows(dWu, Wg)))) return MNS_ERR_SHAPE;
   const int64_t half = inner_bytes(X->rows, Wg->rows, X->dtype);
   if (X->rows && (!ws || ws_bytes < (size_t)(2 * half) || !aligned16(ws))) return MNS_ERR_WORKSPACE;
+  const bool room = X->rows && !offsets && X->dtype != F32 && ws_bytes >= (size_t)(2 * half + split_bytes());
   const Span none = span(static_cast<const void*>(nullptr), 0);
-  if (clash({dX ? span(dX) : none, dWg ? span(dWg) : none, dWu ? span(dWu) : none, X->rows ? span(ws, 2 * half) : none},
+  if (clash({dX ? span(dX) : none, dWg ? span(dWg) : none, dWu ? span(dWu) : none, X->rows ? span(ws, 2 * half + (room ? split_bytes() : 0)) : none},
             {span(dH), span(X), span(Wg), span(Wu), span(G), span(U), offsets_span(offsets, Wg->batch)}))
     return MNS_ERR_ARG;
   const hipStream_t s = as_stream(stream);
@@ -237,6 +275,7 @@ int expert_gated_backward(const mns_tensor* dH, const mns_tensor* X, const mns_t
     GatedArgs a = gated_args(&d, Wg, Wu, dX, offsets, (int)Wg->batch, X->rows);
     a.A2 = dup;
     a.k = (int)Wg->rows;
+    a.parts = room ? reinterpret_cast<float*>(dup + half) : nullptr;
     if (int st = run_product<EX_DX2>(a, X->dtype, vec_rows(Wg) && vec_rows(Wu), s)) return st;
   }
   if (!dWg) return MNS_OK;

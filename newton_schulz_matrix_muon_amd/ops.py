@@ -115,8 +115,8 @@ def declare(lib):
         "embed": [vp, i32, t, ctypes.c_float, t, vp],
         "mns_embed_workspace_bytes": [i64, i64, i64, P(sz)],
         "embed_backward": [t, vp, i32, ctypes.c_float, t, vp, sz, vp],
-        "expert_gated": [t, t, t, vp, i32, t, t, t, vp],
-        "mns_expert_gated_workspace_bytes": [i64, i64, i32, P(sz)],
+        "expert_gated": [t, t, t, vp, i32, t, t, t, vp, sz, vp],
+        "mns_expert_gated_workspace_bytes": [i64, i64, i32, i32, P(sz), P(sz)],
         "expert_gated_backward": [t, t, t, t, t, t, vp, i32, t, t, t, vp, sz, vp],
         "adamw8_step": [ctypes.c_int, pp, pp, pp, pp, pp, pp, P(i64), i32, P(MnsAdamw8Params), vp],
     }
@@ -984,27 +984,33 @@ def _check_gated(what, x, w_gate, w_up, offsets, act, **inner):
     return ACTIVATIONS[act]
 
 
-def expert_gated(x, w_gate, w_up, offsets=None, *, act: str = "silu", keep: bool = False, out=None):
+def expert_gated(x, w_gate, w_up, offsets=None, *, act: str = "silu", keep: bool = False, out=None, workspace=None):
     """act(x w_gate[e]^T) * (x w_up[e]^T) for the rows of expert e, the rows of no expert zero, in one kernel
     (C ABI ``expert_gated``). x: [rows, K] sorted by expert, w_gate and w_up: [experts, N, K] with offsets as
     expert_sort gives them, or [N, K] without offsets: a dense layer. act: silu, gelu (with erf) or relu.
     keep=True: (h, gate, up) with both projections, for expert_gated_backward."""
+    torch = _torch()
     what = "expert_gated"
     code = _check_gated(what, x, w_gate, w_up, offsets, act, out=out)
-    _check_device(what, x, w_gate=w_gate, w_up=w_up, offsets=offsets, out=out)
+    _check_workspace(what, workspace)
+    _check_device(what, x, w_gate=w_gate, w_up=w_up, offsets=offsets, out=out, workspace=workspace)
     shape = (x.shape[0], w_gate.shape[-2])
     h = x.new_empty(shape) if out is None else out
     gate, up = (x.new_empty(shape), x.new_empty(shape)) if keep else (None, None)
+    if workspace is None and offsets is None:
+        n = expert_gated_workspace_bytes(*shape, x, dense=True)[0]
+        workspace = torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
     _launch(what, x, describe(x), describe(w_gate), describe(w_up), _ptr(offsets), code, describe(h), describe(gate) if keep else None,
-            describe(up) if keep else None)
+            describe(up) if keep else None, _ptr(workspace), 0 if workspace is None else _ws_bytes(workspace))
     return (h, gate, up) if keep else h
 
 
-def expert_gated_workspace_bytes(rows: int, inner: int, like) -> int:
-    """like: a tensor of the rows' dtype."""
-    n = ctypes.c_size_t()
-    _check(_lib().mns_expert_gated_workspace_bytes(rows, inner, dtype_code(like), ctypes.byref(n)), "mns_expert_gated_workspace_bytes")
-    return n.value
+def expert_gated_workspace_bytes(rows: int, inner: int, like, *, dense: bool = False) -> tuple:
+    """(expert_gated's, expert_gated_backward's); like: a tensor of the rows' dtype; dense: without offsets."""
+    forward, backward = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(_lib().mns_expert_gated_workspace_bytes(rows, inner, 0 if dense else 1, dtype_code(like), ctypes.byref(forward), ctypes.byref(backward)),
+           "mns_expert_gated_workspace_bytes")
+    return forward.value, backward.value
 
 
 def expert_gated_backward(dh, x, w_gate, w_up, gate, up, offsets=None, *, act: str = "silu", need_input: bool = True,
@@ -1020,7 +1026,8 @@ def expert_gated_backward(dh, x, w_gate, w_up, gate, up, offsets=None, *, act: s
     _check_workspace(what, workspace)
     _check_device(what, x, dh=dh, w_gate=w_gate, w_up=w_up, gate=gate, up=up, offsets=offsets, workspace=workspace)
     if workspace is None:
-        workspace = torch.empty(expert_gated_workspace_bytes(x.shape[0], w_gate.shape[-2], x), dtype=torch.uint8, device=x.device)
+        n = expert_gated_workspace_bytes(x.shape[0], w_gate.shape[-2], x, dense=offsets is None)[1]
+        workspace = torch.empty(n, dtype=torch.uint8, device=x.device)
     dx = x.new_empty(x.shape) if need_input else None
     dwg, dwu = (w_gate.new_empty(w_gate.shape), w_gate.new_empty(w_gate.shape)) if need_weights else (None, None)
     opt = lambda t: None if t is None else describe(t)

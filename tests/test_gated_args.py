@@ -16,7 +16,7 @@ P, Q, R, S, V = 0x10000, 0x8000000, 0x10000000, 0x18000000, 0x20000000   # addre
 def test_gated_refusals(L):
     f = L.expert_gated
     x, wg, wu, h, g, u = t(P, 8, 64), t(Q, 32, 64, batch=3), t(R, 32, 64, batch=3), t(S, 8, 32), t(S + 4096, 8, 32), t(S + 8192, 8, 32)
-    args = lambda **k: (k.get("x", x), k.get("wg", wg), k.get("wu", wu), k.get("off", V), k.get("act", 0), k.get("h", h), k.get("g", g), k.get("u", u), None)
+    args = lambda **k: (k.get("x", x), k.get("wg", wg), k.get("wu", wu), k.get("off", V), k.get("act", 0), k.get("h", h), k.get("g", g), k.get("u", u), k.get("ws"), k.get("n", 0), None)
     for name in ("x", "wg", "wu", "h", "g", "u"):
         assert f(*args(**{name: None})) == ARG, name
     assert f(*args(off=None)) == ARG and f(*args(off=V + 2)) == ARG
@@ -34,6 +34,8 @@ def test_gated_refusals(L):
     assert f(*args(h=t(P + 64, 8, 32))) == ARG and f(*args(h=t(Q + 64, 8, 32))) == ARG and f(*args(g=t(R + 64, 8, 32))) == ARG
     assert f(*args(g=h)) == ARG and f(*args(u=g)) == ARG and f(*args(u=t(V, 8, 32))) == ARG
     one = dict(wg=t(Q, 32, 64), wu=t(R, 32, 64), off=None)
+    assert f(*args(**one, ws=V + 8, n=1 << 30)) == WS                        # not aligned
+    assert f(*args(**one, ws=S, n=1 << 30)) == ARG and f(*args(**one, ws=P, n=1 << 30)) == ARG
     empty = dict(x=t(None, 0, 64), h=t(None, 0, 32), g=t(None, 0, 32), u=t(None, 0, 32))
     assert f(*args(**one, **empty)) == OK and f(*args(**empty)) == OK
     assert f(*args(**one, x=t(P, 8, 63))) == SHAPE
@@ -41,13 +43,18 @@ def test_gated_refusals(L):
 
 def test_gated_backward_refusals(L):
     n = ctypes.c_size_t()
-    w = L.mns_expert_gated_workspace_bytes
-    assert w(8, 32, BF16, ctypes.byref(n)) == OK and n.value >= 2 * 8 * 32 * 2
-    assert w(8, 32, BF16, None) == ARG and w(8, 32, 5, ctypes.byref(n)) == DTYPE
-    for bad in ((-1, 32), (8, 0), ((1 << 24) + 1, 32), (8, (1 << 20) + 1)):
-        assert w(*bad, F32, ctypes.byref(n)) == SHAPE
-    assert w(1 << 24, 1 << 20, F32, ctypes.byref(n)) == OK and n.value == 1 << 47
-    assert w(8, 32, BF16, ctypes.byref(n)) == OK
+    m = ctypes.c_size_t()
+    w = lambda rows, inner, dt, e=3: L.mns_expert_gated_workspace_bytes(rows, inner, e, dt, ctypes.byref(m), ctypes.byref(n))
+    assert w(8, 32, BF16) == OK and n.value >= 2 * 8 * 32 * 2 and m.value == 0
+    assert L.mns_expert_gated_workspace_bytes(8, 32, 3, BF16, None, ctypes.byref(n)) == ARG
+    assert L.mns_expert_gated_workspace_bytes(8, 32, 3, BF16, ctypes.byref(m), None) == ARG
+    assert w(8, 32, 5) == DTYPE
+    for bad in ((-1, 32), (8, 0), ((1 << 24) + 1, 32), (8, (1 << 20) + 1), (8, 32, -1), (8, 32, 1025)):
+        assert w(bad[0], bad[1], F32, *bad[2:]) == SHAPE
+    assert w(1 << 24, 1 << 20, F32) == OK and n.value == 1 << 47
+    assert w(8, 32, BF16, 0) == OK and m.value > 0 and n.value == m.value + 2 * 8 * 32 * 2
+    assert w(8, 32, F32, 0) == OK and m.value == 0
+    assert w(8, 32, BF16) == OK
     f = L.expert_gated_backward
     x, wg, wu, dh, g, u = t(P, 8, 64), t(Q, 32, 64, batch=3), t(R, 32, 64, batch=3), t(S, 8, 32), t(S + 4096, 8, 32), t(S + 8192, 8, 32)
     dx, dwg, dwu = t(P + 65536, 8, 64), t(Q + (1 << 20), 32, 64, batch=3), t(R + (1 << 20), 32, 64, batch=3)

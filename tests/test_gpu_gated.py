@@ -149,6 +149,41 @@ def test_gated_dense(torch, ops, shape, dtype):
     assert half[0] is None and torch.equal(half[1], one[1]) and torch.equal(half[2], one[2])
 
 
+# whole rounds and a cut one, a cut one alone in two to sixteen parts, N of no whole chunk (the input gradient's contraction),
+# contractions that end inside a stage, parts that begin in the second of the input gradient's
+CUT = [(600, 2064, 2056, 0), (1030, 2064, 2056, 8), (300, 4104, 2120, 0), (2500, 4160, 2048, 0), (1290, 2047, 2056, 8), (520, 1099, 4104, 0), (770, 18440, 2056, 0)]
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+@pytest.mark.parametrize("shape", CUT, ids=str)
+def test_gated_dense_with_a_cut_last_round(torch, ops, shape, dtype):
+    rows, n, k, pad = shape
+    gen = gen_for(torch, n)
+    dt = getattr(torch, dtype)
+    x, dh, wg, wu, _ = make(torch, gen, dt, [rows], 0, n, k, pad)
+    check(torch, ops, x, dh, wg[0], wu[0], [rows], None, "silu")
+    # a workspace of its own, and one of the size of an uncut call: the same gradients up to the sums' order
+    fwd, bwd = ops.expert_gated_workspace_bytes(rows, n, x, dense=True)
+    least = ops.expert_gated_workspace_bytes(rows, n, x)[1]
+    ws = torch.full((bwd + 256,), 255, dtype=torch.uint8, device="cuda")
+    h, gate, up = ops.expert_gated(x, wg[0], wu[0], keep=True, workspace=ws[128:128 + fwd])
+    again = ops.expert_gated(x, wg[0], wu[0], keep=True)
+    assert all(torch.equal(a, b) for a, b in zip((h, gate, up), again))
+    dx = ops.expert_gated_backward(dh, x, wg[0], wu[0], gate, up, need_weights=False, workspace=ws[128:128 + bwd])[0]
+    assert torch.equal(dx, ops.expert_gated_backward(dh, x, wg[0], wu[0], gate, up, need_weights=False)[0])
+    assert (ws[:128] == 255).all() and (ws[128 + bwd:] == 255).all()
+    flat = ops.expert_gated_backward(dh, x, wg[0], wu[0], gate, up, need_weights=False, workspace=ws[128:128 + least])[0]
+    u = (2 * n + 40) * 2 * U
+    d = dh.double()
+    v, s = activate(torch, gate.double(), "silu")
+    mag = (d * up.double() * s).abs() @ wg[0].double().abs() + (d * v).abs() @ wu[0].double().abs()
+    assert ((dx.double() - flat.double()).abs() <= torch.finfo(dt).eps * flat.double().abs() + u * mag + torch.finfo(dt).tiny).all()
+    # the matrices' own rows of different length, in both halves of the contraction
+    wide = torch.cat([wu[0], wu[0]], dim=1)[:, :k]
+    assert torch.equal(ops.expert_gated(x, wg[0], wide), h)
+    assert torch.equal(ops.expert_gated_backward(dh, x, wg[0], wide, gate, up, need_weights=False)[0], dx)
+
+
 @pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
 def test_gated_matrices_of_one_buffer_and_of_different_strides(torch, ops, dtype):
     """Gate and up matrices side by side in one batch [experts, 2, N, K], and two with rows of different length."""
@@ -178,7 +213,7 @@ def test_gated_writes_nothing_outside(torch, ops):
         full[2:-2, 8:-8] = 7.0
         assert (full == 7.0).all() and torch.equal(got, ops.expert_gated(x, wg, wu, offsets))
         h, gate, up = ops.expert_gated(x, wg, wu, offsets, keep=True)
-        need = ops.expert_gated_workspace_bytes(rows, n, x)
+        need = ops.expert_gated_workspace_bytes(rows, n, x)[1]
         ws = torch.full((need + 256,), 255, dtype=torch.uint8, device="cuda")
         got = ops.expert_gated_backward(dh, x, wg, wu, gate, up, offsets, workspace=ws[128:128 + need])
         assert (ws[:128] == 255).all() and (ws[128 + need:] == 255).all()
@@ -274,3 +309,46 @@ def test_gated_offsets_in_no_order_write_nothing_outside(torch, ops):
             h, gate, up = ops.expert_gated(x, wg, wu, off, keep=True)
             ops.expert_gated_backward(dh, x, wg, wu, gate, up, off)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_gated_on_any_stream_and_in_a_graph(torch, ops, dtype):
+    """Experts and a dense layer, each path by size: eager twice, on a side stream, and replayed with other inputs in between."""
+    dt = getattr(torch, dtype)
+    gen = gen_for(torch, 33)
+    sets = []
+    for counts, rest, n, k, dense in ((uneven(60, 300, 9), 3, 264, 328, False), ([3, 0, 2], 0, 72, 136, False), ([70, 5], 1, 130, 70, False),
+                                      ([600], 0, 2064, 2056, True)):
+        x, dh, wg, wu, off = make(torch, gen, dt, counts, rest, n, k)
+        if dense:
+            wg, wu, off = wg[0], wu[0], None
+        ws = [torch.empty(b, dtype=torch.uint8, device="cuda") for b in ops.expert_gated_workspace_bytes(x.shape[0], n, x, dense=dense)]
+        sets.append((x, dh, wg, wu, off, ws))
+
+    def run(own):
+        out = []
+        for x, dh, wg, wu, off, ws in sets:
+            h, gate, up = ops.expert_gated(x, wg, wu, off, keep=True, workspace=ws[0] if own else None)
+            out += [h, *ops.expert_gated_backward(dh, x, wg, wu, gate, up, off, workspace=ws[1] if own else None)]
+        return out
+
+    want = [t.clone() for t in run(False)]
+    assert all(torch.equal(a, b) for a, b in zip(want, run(False)))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = run(True)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, other))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = run(True)
+    keep = [(s[0].clone(), s[1].clone()) for s in sets]
+    for i in range(4):
+        for (x, dh, *_), (x0, dh0) in zip(sets, keep):
+            x.copy_(x0 if i % 2 == 0 else -x0)
+            dh.copy_(dh0 if i % 2 == 0 else dh0.flip(1))
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = run(False)
+        assert all(torch.equal(a, b) for a, b in zip(held, eager)), i
