@@ -1040,11 +1040,12 @@ def expert_gated_backward(dh, x, w_gate, w_up, gate, up, offsets=None, *, act: s
 # The norm and the embeddings of the model that the layer belongs to; the conventions are the layer's.
 
 def _check_scale_vector(what, x, weight):
-    torch = _torch()
-    _check_flat(what, x, (x.dtype, torch.float32), weight=weight)
-    if weight is not None:
-        _check_shape(what, "weight", weight, x.shape[-1:])
-    return F32 if weight is None else dtype_code(weight)
+    if weight is None:
+        return F32
+    if weight.dtype != x.dtype and weight.dtype != _torch().float32 or not weight.is_contiguous():
+        _check_flat(what, x, (x.dtype, _torch().float32), weight=weight)
+    _check_shape(what, "weight", weight, x.shape[-1:])
+    return dtype_code(weight)
 
 
 def _check_like(what, x, **named):
@@ -1063,9 +1064,14 @@ def _rms_forward(what, x, weight, residual, residual_out, **more):
         raise ValueError(f"{what}: residual_out without residual")
     _check_like(what, x, residual=residual, residual_out=residual_out, out=more.get("out"))
     _check_device(what, x, weight=weight, residual=residual, residual_out=residual_out, **more)
-    h = x if residual is None else x.new_empty(x.shape) if residual_out is None else residual_out
+    h = x if residual is None else _rows_like(x) if residual_out is None else residual_out
     rstd = x.new_empty(x.shape[:-1], dtype=_torch().float32)
     return xd, code, h, rstd
+
+
+def _rows_like(x):
+    """An uninitialised buffer of x's shape with whole rows (empty_like costs 0.6 us less, and may take over strides)."""
+    return _torch().empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
 
 
 def rms_norm(x, weight=None, *, residual=None, eps: float = 1e-6, out=None, residual_out=None):
@@ -1075,7 +1081,7 @@ def rms_norm(x, weight=None, *, residual=None, eps: float = 1e-6, out=None, resi
     residual itself: the stream is then updated in place."""
     what = "rms_norm"
     xd, code, h, rstd = _rms_forward(what, x, weight, residual, residual_out, out=out)
-    y = x.new_empty(x.shape) if out is None else out
+    y = _rows_like(x) if out is None else out
     kept = residual is not None
     _launch(what, x, xd, describe(residual) if kept else None, _ptr(weight), code, eps, describe(y), describe(h) if kept else None, _ptr(rstd))
     return y, h, rstd
