@@ -293,7 +293,7 @@ int rms_norm_backward(const mns_tensor* dY, const mns_tensor* H, const float* rs
           return st;
     }
     if (!dweight) return (int)MNS_OK;
-    return launch(K_LAYER_NORM, s, [&] { hipLaunchKernelGGL((rms_dw_sum<WT>), dim3((a.cols + 63) / 64), dim3(1024), 0, s, a); });
+    return launch(K_LAYER_NORM, s, [&] { hipLaunchKernelGGL((rms_dw_sum<WT>), dim3((a.cols + 31) / 32), dim3(1024), 0, s, a); });
   });
 }
 

@@ -509,31 +509,31 @@ __global__ void __launch_bounds__(256) rms_dw_long(const RmsArgs p) {
   o.store(p.part + (int64_t)blockIdx.y * p.cols, c, p.cols);
 }
 
-// dw from the parts: 64 columns a workgroup, its 16 waves each take every 16th part, eight at a time.
+// dw from the parts: 32 columns a workgroup, whose 32 half waves each take every 32nd part, eight at a time.
 template <typename WT>
 __global__ void __launch_bounds__(1024) rms_dw_sum(const RmsArgs p) {
-  __shared__ float red[16][64];
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+  __shared__ float red[32][33];
+  const int lane = threadIdx.x & 31, half = threadIdx.x >> 5;
+  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
   float a = 0.f;
   if (c < p.cols) {
     const float* part = p.part + c;
-    int i = wv;
-    for (; i + 7 * 16 < p.nparts; i += 8 * 16) {
+    int i = half;
+    for (; i + 7 * 32 < p.nparts; i += 8 * 32) {
       float v[8];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) v[u] = part[(int64_t)(i + 16 * u) * p.cols];
+      for (int u = 0; u < 8; ++u) v[u] = part[(int64_t)(i + 32 * u) * p.cols];
 #pragma unroll
       for (int u = 0; u < 8; ++u) a += v[u];
     }
-    for (; i < p.nparts; i += 16) a += part[(int64_t)i * p.cols];
+    for (; i < p.nparts; i += 32) a += part[(int64_t)i * p.cols];
   }
-  red[wv][lane] = a;
+  red[half][lane] = a;
   __syncthreads();
-  if (wv == 0 && c < p.cols) {
+  if (half == 0 && c < p.cols) {
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s += red[i][lane];
+    for (int i = 0; i < 32; ++i) s += red[i][lane];
     reinterpret_cast<WT*>(p.dw)[c] = from_f32<WT>(s);
   }
 }

@@ -540,10 +540,6 @@ class Adamw8State(NamedTuple):
     root_scale: object
 
 
-def _dtype_of(t):
-    return t.dtype
-
-
 def adamw8_state(param) -> Adamw8State:
     """The state of a parameter before its first step (all zero)."""
     torch = _torch()
@@ -581,7 +577,7 @@ def adamw8_step(params, grads, states, *, lr: float, step: int, beta1: float = 0
     names = ("params", "grads", *Adamw8State._fields)
     own = (params[0].dtype,)
     for name, column, allowed, sizes in zip(names, columns, (own, own, codes, scales, codes, scales), (numels, numels, numels, blocks, numels, blocks)):
-        if not set(map(_dtype_of, column)).issubset(allowed):
+        if not {t.dtype for t in column}.issubset(allowed):
             i = next(i for i, t in enumerate(column) if t.dtype not in allowed)
             raise TypeError(f"{what}: {name}[{i}] is {column[i].dtype}, expected {allowed[0]}")
         if list(map(Tensor.numel, column)) != sizes:
