@@ -366,9 +366,7 @@ int embed_backward(const mns_tensor* dY, const void* tokens, int32_t id_bytes, f
     if (p.n <= EMBED_ONE)
       return launch(K_ROUTE, s, [&] {
         if (p.steps <= 1) hipLaunchKernelGGL((embed_sort_one<ID, 1>), dim3(1), dim3(EMBED_NT), 0, s, p);
-        else if (p.steps <= 4) hipLaunchKernelGGL((embed_sort_one<ID, 4>), dim3(1), dim3(EMBED_NT), 0, s, p);
-        else if (p.steps <= 8) hipLaunchKernelGGL((embed_sort_one<ID, 8>), dim3(1), dim3(EMBED_NT), 0, s, p);
-        else hipLaunchKernelGGL((embed_sort_one<ID, 16>), dim3(1), dim3(EMBED_NT), 0, s, p);
+        else hipLaunchKernelGGL((embed_sort_one<ID, 4>), dim3(1), dim3(EMBED_NT), 0, s, p);
       });
     for (int pass = 0; pass < p.passes; ++pass) {
       if (int st = launch(K_ROUTE, s, [&] { hipLaunchKernelGGL(embed_sort_count<ID>, dim3(p.nblocks), dim3(EMBED_NT), 0, s, p, pass); })) return st;
@@ -401,8 +399,14 @@ int embed_backward(const mns_tensor* dY, const void* tokens, int32_t id_bytes, f
         }))
       return st;
     if (a.tiles < 2) return (int)MNS_OK;
-    dim3 g = grid_of(a.tiles - 1);
-    g.z = (a.cols + 511) / 512;
+    a.gathered = a.tiles >= EMBED_GROUPS * EMBED_GROUP;
+    auto columns = [&](dim3 g) {
+      g.z = (a.cols + 511) / 512;
+      return g;
+    };
+    const dim3 groups = columns(grid_of((a.tiles + EMBED_GROUP - 1) / EMBED_GROUP)), g = columns(grid_of(a.tiles - 1));
+    if (a.gathered)
+      if (int st = launch(K_ROUTE, s, [&] { hipLaunchKernelGGL(embed_gather<256>, groups, dim3(256), 0, s, a); })) return st;
     return launch(K_ROUTE, s, [&] { hipLaunchKernelGGL(embed_join<T>, g, dim3(256), 0, s, a); });
   });
 }

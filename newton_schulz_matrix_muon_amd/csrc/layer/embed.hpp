@@ -9,9 +9,8 @@
 // positions are sorted by token, ties by position, and cut into tiles of 32. A thread walks a tile
 // for one 16-byte unit of columns and adds up rows of one token in order, in fp32; what lies within
 // the tile goes to the table at once, the parts of a token that crosses a tile's end go to the
-// workspace and are added up tile by tile. The work is in proportion to the positions whatever
-// their tokens, so a token that occurs everywhere costs no more than others. Equal calls give equal
-// bits.
+// workspace and are added up tile by tile, for many tiles of one token in two steps. The work is in
+// proportion to the positions whatever their tokens. Equal calls give equal bits.
 //
 // Bound by HBM: dy is read once and the table, mostly zeros, written once.
 #pragma once
@@ -88,10 +87,13 @@ __global__ void __launch_bounds__(256) embed_rows(const EmbedArgs p) {
 // ------------------------------------------------------------------------------------- sort
 // Positions by token: a radix sort from the lowest digit up, stable, in passes of up to ten bits.
 // Up to EMBED_ONE positions one workgroup takes every pass in one launch; more go in two launches a
-// pass, counts and places.
+// pass, counts and places, with one step of 64 positions a wave. A pass of one workgroup costs 3.6 us at
+// 1024 positions, 7 at 4096, 11.5 at 8192 and 21 at 16384; one of two launches 10 to 12 us at any of
+// these. The whole gradient (80 columns, 19478 rows, bf16): 30.7 us against 31.5 at 4096 positions, 36.0
+// against 32.1 at 6000, 59.5 against 33.5 at 16384.
 constexpr int EMBED_WAVES = 16, EMBED_NT = 64 * EMBED_WAVES;
 constexpr int EMBED_DIGITS = 1024;
-constexpr int64_t EMBED_ONE = 16384;
+constexpr int64_t EMBED_ONE = 4096;
 
 struct EmbedSortArgs {
   const void* tokens;
@@ -281,6 +283,7 @@ struct EmbedGradArgs {
   const uint8_t* marks;
   float* part;                     // [2 * tiles][cols]: a tile's part of the token that came in from the tile before, of the one that goes on
   int64_t n, tiles;
+  bool gathered;                   // embed_gather ran
   int64_t tile_blocks, zero_blocks;
   int vocab, cols, units;
   float scale;
@@ -368,9 +371,59 @@ __global__ void __launch_bounds__(256) embed_grad(const EmbedGradArgs p) {
   if (now < p.vocab) leave(now == after);
 }
 
+// Many tiles of one token: the parts of EMBED_GROUP tiles that lie within one token, added up into the first
+// one's, so that embed_join has fewer to go through. Workgroup (group, 512 columns), each of its four waves
+// a quarter of the tiles in turns of four. One token at all of 65536 positions of 1024 columns: 131 us
+// without, 67 with; at 2^20 positions of 64 columns 1299 and 140; with tokens that occur alike 2 to 3 us more for
+// the launch, which is why fewer groups go without.
+constexpr int EMBED_GROUP = 64;
+constexpr int64_t EMBED_GROUPS = 16;   // from so many groups on
+__device__ inline void embed_load_parts(const EmbedGradArgs& p, int64_t tile, int64_t c0, float (&v)[8]) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = p.part[2 * tile * p.cols + min(c0 + e * 64 + lane, (int64_t)p.cols - 1)];
+}
+// Sums of four waves in the first, in order.
+__device__ inline void embed_meet(float (&acc)[8], float (*sum)[8][64]) {
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  if (wv)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[wv - 1][e][lane] = acc[e];
+  __syncthreads();
+  if (wv) return;
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    for (int w = 0; w < 3; ++w) acc[e] += sum[w][e][lane];
+}
+template <int NT>
+__global__ void __launch_bounds__(NT) embed_gather(const EmbedGradArgs p) {
+  __shared__ float sum[3][8][64];
+  const int64_t t0 = block_id() * EMBED_GROUP, t1 = t0 + EMBED_GROUP - 1;
+  if (t0 == 0 || t1 >= p.tiles) return;
+  const int token = p.sorted[t1 * EMBED_TILE].x;
+  if (token >= p.vocab || p.sorted[t0 * EMBED_TILE - 1].x != token) return;
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  const int64_t c0 = (int64_t)blockIdx.z * 512;
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int i = wv; i < EMBED_GROUP; i += 16) {
+    float v[4][8];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) embed_load_parts(p, t0 + i + 4 * u, c0, v[u]);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] += v[u][e];
+  }
+  embed_meet(acc, sum);   // every load of the first tile's part has landed
+  if (wv) return;
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (c0 + e * 64 + lane < p.cols) p.part[2 * t0 * p.cols + c0 + e * 64 + lane] = acc[e];
+}
+
 // A token that crosses ends of tiles: its parts added up in the tiles' order. Workgroup (end between
 // two tiles, 512 columns) works where a token begins in the tile before the end and goes on behind it;
-// its four waves take every fourth tile.
+// its four waves take every fourth tile, or group of tiles that embed_gather has added up.
 template <typename T>
 __global__ void __launch_bounds__(256) embed_join(const EmbedGradArgs p) {
   __shared__ float sum[3][8][64];
@@ -389,36 +442,33 @@ __global__ void __launch_bounds__(256) embed_join(const EmbedGradArgs p) {
     lo += (in - 1) * step;                        // the first of them is lo itself
     end = min(lo + step, end);
   }
-  for (int64_t c0 = (int64_t)blockIdx.z * 512; c0 < p.cols; c0 += (int64_t)gridDim.z * 512) {
-    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (wv == 0) {
+  // what there is to add up: the tiles before the first whole group, the whole groups, the tiles behind
+  const int64_t g0 = min((a + EMBED_GROUP) / EMBED_GROUP * EMBED_GROUP, end), g1 = p.gathered ? max(g0, end / EMBED_GROUP * EMBED_GROUP) : g0;
+  const int64_t head = g0 - (a + 1), groups = (g1 - g0) / EMBED_GROUP, items = head + groups + (end - g1);
+  auto tile_of = [&](int64_t i) {
+    return i < head ? a + 1 + i : i < head + groups ? g0 + (i - head) * EMBED_GROUP : g1 + (i - head - groups);
+  };
+  const int64_t c0 = (int64_t)blockIdx.z * 512;
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (wv == 0) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] = p.part[(2 * a + 1) * p.cols + min(c0 + e * 64 + lane, (int64_t)p.cols - 1)];
-    }
-    // four tiles' parts in flight; the tiles behind the last read the last and are left out
-    for (int64_t t = a + 1 + wv; t < end; t += 16) {
-      float v[4][8];
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[u][e] = p.part[2 * min(t + 4 * u, end - 1) * p.cols + min(c0 + e * 64 + lane, (int64_t)p.cols - 1)];
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] += t + 4 * u < end ? v[u][e] : 0.f;
-    }
-    if (wv)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sum[wv - 1][e][lane] = acc[e];
-    __syncthreads();
-    if (wv == 0)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        for (int w = 0; w < 3; ++w) acc[e] += sum[w][e][lane];
-        if (c0 + e * 64 + lane < p.cols) reinterpret_cast<T*>(p.dt + (int64_t)token * p.dt_ld)[c0 + e * 64 + lane] = from_f32<T>(acc[e] * p.scale);
-      }
-    __syncthreads();
+    for (int e = 0; e < 8; ++e) acc[e] = p.part[(2 * a + 1) * p.cols + min(c0 + e * 64 + lane, (int64_t)p.cols - 1)];
   }
+  // four parts in flight; those behind the last read the last and are left out
+  for (int64_t i = wv; i < items; i += 16) {
+    float v[4][8];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) embed_load_parts(p, tile_of(min(i + 4 * u, items - 1)), c0, v[u]);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] += i + 4 * u < items ? v[u][e] : 0.f;
+  }
+  embed_meet(acc, sum);
+  if (wv) return;
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (c0 + e * 64 + lane < p.cols) reinterpret_cast<T*>(p.dt + (int64_t)token * p.dt_ld)[c0 + e * 64 + lane] = from_f32<T>(acc[e] * p.scale);
 }
 
 }  // namespace mns

@@ -227,7 +227,7 @@ def test_rms_norm_of_more_rows_than_a_grid_dimension(torch, ops):
 # tokens, vocabulary, cols, columns behind each row, first element
 EMBED = [
     (1, 1, 1, 0, 0), (1, 163840, 64, 0, 0), (5, 3, 7, 0, 0), (31, 40, 8, 0, 0), (32, 40, 3, 1, 1), (33, 2, 4, 0, 1), (64, 1, 65, 0, 0), (65, 300, 2047, 0, 0),
-    (100, 70000, 24, 8, 8), (1000, 1000, 512, 0, 0), (4099, 1023, 513, 0, 3), (4099, 1024, 128, 0, 0), (16384, 8191, 40, 0, 0),
+    (100, 70000, 24, 8, 8), (1000, 1000, 512, 0, 0), (4099, 1023, 513, 0, 3), (4099, 1024, 128, 0, 0), (4096, 8191, 40, 0, 0), (4097, 70000, 12, 0, 8), (16384, 8191, 40, 0, 0),
     (16385, 8191, 40, 0, 0), (50000, 120, 33, 3, 0), (70000, 1100000, 9, 0, 0), (0, 50, 64, 0, 0), (3000, 5, 1024, 0, 0), (300000, 300, 2, 0, 0),
 ]
 
@@ -288,6 +288,31 @@ def test_embed_gradient_counts_exactly(torch, ops, n):
         dy = torch.randint(-8, 9, (n, 5), generator=gen, device="cuda").float()
         ref = torch.zeros(vocab, 5, dtype=torch.float64, device="cuda").index_add_(0, tokens, dy.double())
         assert torch.equal(ops.embed_backward(dy, tokens, vocab).double(), ref)
+
+
+@pytest.mark.parametrize("n", [32736, 32737, 70001])
+def test_embed_gradient_counts_long_runs_exactly(torch, ops, n):
+    """Runs of a token over whole groups of 64 tiles, that begin and end anywhere in a group."""
+    gen = gen_for(torch, n)
+    at = torch.arange(n, device="cuda")
+    for run, first in ((2048, 0), (2048, 1), (2047, 0), (2049, 31), (2079, 0), (2080, 32), (4095, 32), (4128, 2016), (6200, 33), (30000, 2047), (n, 0), (n - 1, n - 1)):
+        tokens = (at + (run - first)) // run
+        tokens = tokens[torch.randperm(n, generator=gen, device="cuda")]
+        vocab = int(tokens.max()) + 1
+        dy = torch.randint(-8, 9, (n, 3), generator=gen, device="cuda").float()
+        ref = torch.zeros(vocab, 3, dtype=torch.float64, device="cuda").index_add_(0, tokens, dy.double())
+        assert torch.equal(ops.embed_backward(dy, tokens, vocab).double(), ref)
+
+
+@pytest.mark.parametrize("vocab", [3, (1 << 24) - 1])
+def test_embed_gradient_of_the_most_positions(torch, ops, vocab):
+    """2^24 positions of one column: sums of whole numbers below 2^24, which fp32 holds."""
+    n = 1 << 24
+    gen = gen_for(torch, vocab)
+    tokens = torch.randint(0, vocab, (n,), generator=gen, device="cuda", dtype=torch.int32)
+    dy = torch.randint(0, 2, (n, 1), generator=gen, device="cuda").float()
+    ref = torch.bincount(tokens, weights=dy[:, 0].double(), minlength=vocab)
+    assert torch.equal(ops.embed_backward(dy, tokens, vocab)[:, 0].double(), ref)
 
 
 def test_embed_shapes_out_and_nothing_outside(torch, ops):
