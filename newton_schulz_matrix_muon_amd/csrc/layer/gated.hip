@@ -77,7 +77,9 @@ int run_split_pingpong(GatedArgs a, int dt, hipStream_t s) {
   return dt == BF16 ? both(__bf16{}) : both(_Float16{});
 }
 
-// Whether cutting the last round is worth its sum (about 25 us): host arithmetic on a dense product's tiles.
+// Whether cutting the last round is worth its sum: host arithmetic on a dense product's tiles. Forward products
+// with and without (us, 128 x 64 tiles): 1000 x 2048 x 2048 (32 stages) 48 and 39, 600 x 4096 x 3000 (47) 61 and 68,
+// 600 x 7168 x 4096 (64) 103 and 145.
 template <int MODE>
 bool split_pays(const GatedArgs& a) {
   if (MODE == EX_DW2 || !a.parts || a.offsets) return false;
@@ -85,7 +87,7 @@ bool split_pays(const GatedArgs& a) {
   const int64_t tiles = (a.rows + 255) / 256 * tile_columns<MODE, TilePP>(a);
   const LastRound last = last_round((int)((tiles + 7) / 8), wgs);
   const int64_t stages = (a.k + 63) / 64 * (MODE == EX_DX2 ? 2 : 1);
-  return last.parts > 1 && stages >= 32;
+  return last.parts > 1 && stages >= 40;
 }
 
 int run_few(const GatedArgs& a, int dt, int fit, hipStream_t s) {
@@ -109,13 +111,20 @@ bool few_rows(const GatedArgs& a, int dt, int fit) {
   return a.rows <= most && a.k * dtype_size(dt) >= 512 && whole;
 }
 
+// 64 x 64 tiles whose contraction eight waves share: where larger tiles would leave CUs idle, or would be mostly
+// empty. us with these tiles and without: 16-bit forward products of 400 x 2048 x 2048 (448 tiles) 27 and 38,
+// 200 x 4096 x 3000 (512) 37 and 46, 300 x 4096 x 3000 (640) 51 and 50; input gradients of 300 x 7168 x 4096
+// (320) 110 and 85. fp32 has no larger pipelined tiles: 64 experts of 1408 x 2048 with 32 rows each 445 and
+// 760, with 64 rows 698 and 778, with 96 rows 912 and 800.
 template <int MODE>
 bool split_tiles(const GatedArgs& a, int dt) {
   const int64_t stage = 128 / dtype_size(dt);
   const int64_t some = std::min<int64_t>(a.experts, a.rows);   // experts that can have rows
-  const int64_t high = ex_dw(MODE) ? tile_rows<MODE, Tile64>(a) : std::max(some, a.rows / 64 + some / 2);
+  const int64_t high = ex_dw(MODE) ? tile_rows<MODE, Tile64>(a) : a.experts > 1 ? std::max(some, a.rows / 64 + some / 2) : (a.rows + 63) / 64;
   const int64_t tiles = high * tile_columns<MODE, Tile64>(a), deep = ex_dw(MODE) ? a.rows / a.experts : MODE == EX_DX2 ? 2 * (int64_t)a.k : a.k;
-  return deep >= 4 * stage && tiles <= (dt == F32 && !ex_dw(MODE) ? 9 : 1) * (int64_t)device_cus();
+  if (deep < 4 * stage) return false;
+  if (dt == F32 && !ex_dw(MODE)) return tiles <= 9 * (int64_t)device_cus() || a.rows <= 72 * some;
+  return tiles <= (MODE == EX_GATE ? 2 : 1) * (int64_t)device_cus();
 }
 
 // vec: operands' rows of whole aligned chunks.
@@ -132,7 +141,11 @@ int run_product(const GatedArgs& a, int dt, bool vec, hipStream_t s) {
   const int64_t high = ex_dw(MODE) ? tile_rows<MODE, TilePP>(a) : a.rows / 256 + std::min<int64_t>(a.experts, a.rows);
   if constexpr (MODE != EX_DW2)
     if (whole && split_pays<MODE>(a) && !split_tiles<MODE>(a, dt)) return run_split_pingpong<MODE>(a, dt, s);
-  if (whole && 2 * high * tile_columns<MODE, TilePP>(a) >= device_cus()) return run_pingpong<MODE>(a, dt, s);
+  // A forward product's 256 x 128 tiles of few rows are mostly empty: 64 experts of 1408 x 2048 with 64 rows each take
+  // 192 us, with 128 x 64 tiles 167; with 96 rows 198 and 177, with 128 rows 204 and 230 (gradients: none of
+  // the sort, 163 and 177 us at 64 rows).
+  const bool empty = MODE == EX_GATE && a.rows < 112 * std::min<int64_t>(a.experts, a.rows);
+  if (whole && !empty && 2 * high * tile_columns<MODE, TilePP>(a) >= device_cus()) return run_pingpong<MODE>(a, dt, s);
   if (split_tiles<MODE>(a, dt)) return run_staged<MODE, Tile64, 8>(a, dt, fit, s);
   return run_staged<MODE, Tile128, 1>(a, dt, fit, s);
 }

@@ -151,7 +151,8 @@ def test_gated_dense(torch, ops, shape, dtype):
 
 # whole rounds and a cut one, a cut one alone in two to sixteen parts, N of no whole chunk (the input gradient's contraction),
 # contractions that end inside a stage, parts that begin in the second of the input gradient's
-CUT = [(600, 2064, 2056, 0), (1030, 2064, 2056, 8), (300, 4104, 2120, 0), (2500, 4160, 2048, 0), (1290, 2047, 2056, 8), (520, 1099, 4104, 0), (770, 18440, 2056, 0)]
+CUT = [(600, 2064, 2056, 0), (1030, 2064, 2056, 8), (300, 4104, 2120, 0), (2500, 4160, 2048, 0), (1290, 2047, 2056, 8), (520, 1099, 4104, 0), (770, 18440, 2056, 0),
+       (600, 2064, 2568, 0), (1030, 2064, 2632, 8), (2500, 4160, 2616, 0), (300, 4104, 4104, 8)]
 
 
 @pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
