@@ -577,3 +577,36 @@ def test_streams_and_graphs(torch, ops):
         torch.cuda.synchronize()
         eager = run()
         assert all(torch.equal(a, b) for a, b in zip(held, eager)), i
+
+
+def test_two_streams_at_once(torch, ops):
+    """Calls of one kind on two streams, one of them replayed from a graph, with workspaces of their own: long runs of tokens among them."""
+    sets = []
+    for seed, n in ((41, 40000), (42, 70000)):
+        gen = gen_for(torch, seed)
+        tokens = torch.where(torch.rand(n, generator=gen, device="cuda") < 0.7, 11, token_ids(torch, gen, n, 3000, torch.int32))
+        dy = normal(torch, gen, n, 136).to(torch.bfloat16)
+        ws = [torch.empty(b, dtype=torch.uint8, device="cuda") for b in (ops.embed_workspace_bytes(n, 3000, 136), ops.rms_norm_workspace_bytes(dy))]
+        sets.append((tokens.to(torch.int32), dy, normal(torch, gen, 136), ws))
+
+    def run(tokens, dy, w, ws):
+        y, h, rstd = ops.rms_norm(dy, w)
+        return [y, ops.embed_backward(dy, tokens, 3000, workspace=ws[0]), *ops.rms_norm_backward(y, h, rstd, w, workspace=ws[1])]
+
+    want = [[t.clone() for t in run(*s)] for s in sets]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = run(*sets[0])
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    one.wait_stream(torch.cuda.current_stream())
+    two.wait_stream(torch.cuda.current_stream())
+    for _ in range(6):
+        with torch.cuda.stream(one):
+            graph.replay()
+        with torch.cuda.stream(two):
+            other = run(*sets[1])
+        one.synchronize()
+        two.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want[0], held))
+        assert all(torch.equal(a, b) for a, b in zip(want[1], other))

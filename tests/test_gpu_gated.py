@@ -319,7 +319,7 @@ def test_gated_on_any_stream_and_in_a_graph(torch, ops, dtype):
     gen = gen_for(torch, 33)
     sets = []
     for counts, rest, n, k, dense in ((uneven(60, 300, 9), 3, 264, 328, False), ([3, 0, 2], 0, 72, 136, False), ([70, 5], 1, 130, 70, False),
-                                      ([600], 0, 2064, 2056, True)):
+                                      ([600], 0, 2064, 2056, True), ([600], 0, 2064, 2568, True)):
         x, dh, wg, wu, off = make(torch, gen, dt, counts, rest, n, k)
         if dense:
             wg, wu, off = wg[0], wu[0], None
@@ -353,3 +353,29 @@ def test_gated_on_any_stream_and_in_a_graph(torch, ops, dtype):
         torch.cuda.synchronize()
         eager = run(False)
         assert all(torch.equal(a, b) for a, b in zip(held, eager)), i
+
+
+def test_gated_on_two_streams_at_once(torch, ops):
+    gen = gen_for(torch, 34)
+    sets = []
+    for counts, n, k, dense in (([600], 2064, 2568, True), (uneven(24, 900, 10), 264, 328, False)):
+        x, dh, wg, wu, off = make(torch, gen, torch.bfloat16, counts, 0, n, k)
+        if dense:
+            wg, wu, off = wg[0], wu[0], None
+        sets.append((x, dh, wg, wu, off, [torch.empty(b, dtype=torch.uint8, device="cuda") for b in ops.expert_gated_workspace_bytes(x.shape[0], n, x, dense=dense)]))
+
+    def run(x, dh, wg, wu, off, ws):
+        h, gate, up = ops.expert_gated(x, wg, wu, off, keep=True, workspace=ws[0])
+        return [h, *ops.expert_gated_backward(dh, x, wg, wu, gate, up, off, workspace=ws[1])]
+
+    want = [[t.clone() for t in run(*s)] for s in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(6):
+        got = []
+        for s, a in zip(streams, sets):
+            with torch.cuda.stream(s):
+                got.append(run(*a))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for g, w in zip(got, want) for a, b in zip(g, w))
