@@ -24,37 +24,47 @@ namespace {
 constexpr int held(int nt, int vpt) { return nt * vpt * 8; }
 constexpr int kRmsHeld = held(1024, 2);   // backward: longer rows take the kernels that read them again
 
-// Threads that hold a row, a chunk each: whole waves, and past 256 threads as many on each of a CU's four SIMDs,
-// so that as many workgroups fit a CU as its registers allow.
-int row_threads(int64_t cols) {
+// Threads that hold a row, a chunk each, in whole waves. whole: past 256 threads as many on each of a CU's four
+// SIMDs, so that as many workgroups fit a CU as its registers allow; 16-bit forward kernels, of which eight waves
+// fit a SIMD, do better with none idle. 16384 rows, us without and with: 16-bit forward of 4500 columns 117 and 128 (in
+// 8 bits 108 and 133), of 2500 79 and 74 (72 and 77); fp32 forward of 4500 259 and 229, backward of 2500 132 and 116.
+int row_threads(int64_t cols, bool whole) {
   const int64_t nt = (cols + 511) / 512 * 64;
-  return (int)std::min<int64_t>(1024, nt <= 256 ? nt : round_up(nt, 256));
+  return (int)std::min<int64_t>(1024, !whole || nt <= 256 ? nt : round_up(nt, 256));
 }
 
 // Workgroups that share the rows of a backward pass, each with a part of dweight: as many as the chip holds at
-// once (20 waves a CU), but at least four turns of rows each once every CU has one, because each part costs as
-// much traffic as two fp32 rows.
+// once, 20 waves a CU (65536 x 700 in bf16: 95 us, with 16 or 32 waves 109 and 114; 16384 x 7168: 189, 189 and 194).
 int rms_parts(int64_t rows, int64_t cols) {
-  const int64_t turns = cols <= held(64, 1) ? (rows + 3) / 4 : rows;   // four rows at a time where a wave holds one
-  const int64_t most = 256 * (20 / (std::max(cols <= held(64, 1) ? 256 : 64, row_threads(cols)) / 64));
-  return (int)std::max<int64_t>(1, turns <= 256 ? turns : std::min(most, std::max<int64_t>(256, turns / 4)));
+  const bool wave = cols <= held(64, 1);                 // four rows at a time where a wave holds one
+  const int64_t turns = wave ? (rows + 3) / 4 : rows;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(turns, 256 * (20 / ((wave ? 256 : row_threads(cols, true)) / 64))));
+}
+
+// Workgroups of a forward pass of `turns` rows (fours of them where a wave holds one): a row each, or as many as a CU holds
+// at once, each of which has the next row on its way. us of a workgroup a row, of 16 and of 32 waves a CU:
+//   bf16  16384 x 4500 147, 191, 128;  16384 x 7168 177, 188, 179 (in 8 bits 180, 194, 161);  8192 x 12000 203, 163, 166
+//   fp32  16384 x 2500 130, 132, 149;  16384 x 4500 226, 214, 229;  4096 x 12000 188, 156, 155;  65536 x 700 153, 166, 170
+unsigned rms_groups(int64_t turns, int nt, int64_t cols, int es) {
+  if (es == 4 && (cols <= held(64, 1) || nt < 256)) return (unsigned)turns;   // fewer than 2^32 threads: 2^24 rows of 192
+  const int waves = es == 4 || cols > held(1024, 1) ? 16 : 32;
+  return (unsigned)std::min<int64_t>(turns, (int64_t)device_cus() * (64 * waves / nt));
 }
 
 template <typename T, typename WT, bool MX>
 void launch_rms_fwd(const RmsArgs& a, hipStream_t s) {
-  // as many workgroups as the chip holds at once (32 waves a CU), or a row each
-  auto turns = [&](int64_t n, int nt) { return dim3((unsigned)std::min<int64_t>(n, (int64_t)device_cus() * std::max(1, 2048 / nt))); };
-  const int nt = row_threads(a.cols);
-  if (a.cols <= held(64, 1)) hipLaunchKernelGGL((rms_fwd_row<T, WT, true, 1, MX>), turns((a.rows + 3) / 4, 256), dim3(256), 0, s, a);
-  else if (a.cols <= held(1024, 1)) hipLaunchKernelGGL((rms_fwd_row<T, WT, false, 1, MX>), turns(a.rows, nt), dim3(nt), 0, s, a);
-  else if (a.cols <= held(1024, 2)) hipLaunchKernelGGL((rms_fwd_row<T, WT, false, 2, MX>), turns(a.rows, 1024), dim3(1024), 0, s, a);
+  const int nt = a.cols <= held(64, 1) ? 256 : row_threads(a.cols, sizeof(T) == 4);
+  const dim3 g(rms_groups(a.cols <= held(64, 1) ? (a.rows + 3) / 4 : a.rows, nt, a.cols, sizeof(T)));
+  if (a.cols <= held(64, 1)) hipLaunchKernelGGL((rms_fwd_row<T, WT, true, 1, MX>), g, dim3(nt), 0, s, a);
+  else if (a.cols <= held(1024, 1)) hipLaunchKernelGGL((rms_fwd_row<T, WT, false, 1, MX>), g, dim3(nt), 0, s, a);
+  else if (a.cols <= held(1024, 2)) hipLaunchKernelGGL((rms_fwd_row<T, WT, false, 2, MX>), g, dim3(nt), 0, s, a);
   else hipLaunchKernelGGL((rms_fwd_long<T, WT, MX>), grid_of(a.rows), dim3(1024), 0, s, a);
 }
 
 template <typename T, typename WT>
 void launch_rms_bwd(const RmsArgs& a, hipStream_t s) {
   const dim3 g((unsigned)a.nparts);
-  const int nt = row_threads(a.cols);
+  const int nt = row_threads(a.cols, true);
   if (a.cols <= held(64, 1)) hipLaunchKernelGGL((rms_bwd_row<T, WT, true, 1>), g, dim3(256), 32 * 64, s, a);
   else if (a.cols <= held(1024, 1)) hipLaunchKernelGGL((rms_bwd_row<T, WT, false, 1>), g, dim3(nt), 32 * nt, s, a);
   else hipLaunchKernelGGL((rms_bwd_row<T, WT, false, 2>), g, dim3(1024), 64 * 1024, s, a);
