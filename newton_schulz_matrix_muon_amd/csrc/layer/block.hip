@@ -34,7 +34,7 @@ int row_threads(int64_t cols, bool whole) {
 }
 
 // Workgroups that share the rows of a backward pass, each with a part of dweight: as many as the chip holds at
-// once, 20 waves a CU (65536 x 700 in bf16: 95 us, with 16 or 32 waves 109 and 114; 16384 x 7168: 189, 189 and 194).
+// once, 20 waves a CU (h as dh, 65536 x 700 in bf16: 95 us, with 16 or 32 waves 109 and 114; 16384 x 7168: 189, 189 and 194).
 int rms_parts(int64_t rows, int64_t cols) {
   const bool wave = cols <= held(64, 1);                 // four rows at a time where a wave holds one
   const int64_t turns = wave ? (rows + 3) / 4 : rows;
@@ -140,7 +140,7 @@ EmbedPlan embed_plan(int64_t n, int64_t vocab, int64_t cols) {
   e.passes = (width + 9) / 10;
   e.bits = (width + e.passes - 1) / e.passes;
   const int64_t waves = (n + EMBED_NT - 1) / EMBED_NT;   // 64-position steps per wave of one workgroup
-  e.steps = (int)(n <= EMBED_ONE ? std::max<int64_t>(1, waves) : round_up((waves + 255) / 256, EMBED_MANY));
+  e.steps = (int)(n <= EMBED_ONE ? std::max<int64_t>(1, waves) : (waves + 255) / 256);
   e.nblocks = (int)std::max<int64_t>(1, (waves + e.steps - 1) / e.steps);
   e.tiles = (n + EMBED_TILE - 1) / EMBED_TILE;
   int64_t at = 0;

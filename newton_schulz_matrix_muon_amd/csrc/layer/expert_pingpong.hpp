@@ -16,8 +16,14 @@
 //
 // The tiles of a workgroup form one stream of stages: the DMA goes on into the next tile while
 // this one's last stages and its stores run. Results leave the registers as 16-byte stores: the
-// MFMAs run with the operands swapped, so a lane holds runs of four columns of one row, and one
-// swap of lane halves makes them eight.
+// MFMAs run with the operands swapped, so a lane holds runs of four columns of one row, one swap of
+// lane halves makes them eight, and one of rows of 16 lanes puts 64 bytes of a row into four lanes
+// (weight gradient of 64 x 1408 x 2048, 384 rows each: 191 us with 32 bytes a row, 182 so).
+//
+// An XCD takes a part of the tile list. A weight gradient's tiles cost as many stages as their expert has rows, so
+// its parts have equal cost (cost_list): 27 x 2048 x 7168 of a router's 32768 rows 1044 us with equal numbers of tiles,
+// 867 so. SPLIT: the last round of a dense product (last_round), 509 rows of 18432 x 7168 forward 336 to 265 us,
+// input gradient 551 to 298.
 //
 // Bound by the board's power and LDS. 4 x 2048 rows against 2048 x 7168, bf16, held for a second:
 // 177 us (1357 TFLOP/s) at 1.59 GHz and 1330 W, 2500 cycles a stage of 2048 MFMA cycles; on zeros

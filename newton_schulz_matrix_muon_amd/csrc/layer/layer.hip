@@ -227,7 +227,7 @@ bool split_tiles(const ExpertArgs& a, int dt) {
 // extents that do not leave half of a tile empty, and enough tiles for half of the CUs. One
 // MI355X, bf16, rows per expert on average (a router's picks), 256 x 256 against 128 x 128 tiles: 27
 // experts of 2048 x 7168, 8 rows, forward 144 against 154 us, weight gradient 173 against 237; 256
-// rows 317 against 417, 380 against 496 (exactly 256 rows each: 218 against 318, 362 against 449); 64
+// rows 317 against 417, 364 against 496 (exactly 256 rows each: 218 against 318, 360 against 449); 64
 // experts of 1408 x 2048, 16 rows 100 against 100 us, weight gradient 83 against 115; 128 rows 115
 // against 132, 138 against 183; 128 experts of 512 x 512 (264 tiles), 32 rows 22 against 20 us, weight
 // gradient 20 against 22; 64 rows 24 against 22, 22 against 25; 512 rows 63 against 75; 8 experts of

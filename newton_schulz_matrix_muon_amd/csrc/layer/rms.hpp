@@ -11,7 +11,9 @@
 // the forward pass computed. Sums are fp32 in a fixed order; each result is rounded once.
 //
 // Bound by HBM: a few flops per byte, every input read once and every output written once, a row
-// held in registers.
+// held in registers. One MI355X (a large copy reaches 4.9 TB/s), with the residual: 16384 x 7168 bf16
+// forward 178 us at 5.3 TB/s, in 8 bits 160 at 5.2, backward 219 at 4.3; fp32 342, 281 and 348 (5.4 TB/s);
+// 16383 x 2047 fp16, rows at any address, 55, 52 and 66 (4.9, 4.5 and 4.1 TB/s).
 #pragma once
 
 #include "mx8.hpp"
@@ -160,7 +162,8 @@ __device__ inline void rms_store(const RmsArgs& p, int64_t r, T* y, int c, const
 
 // A row is held by a wave (WAVE: four rows a workgroup, no barrier) or by the workgroup, as many waves as it
 // takes, VPT chunks a thread. A workgroup walks every gridDim.x-th row (or four of them) with the weight
-// in registers and the next row's x and r already on their way.
+// in registers and the next row's x and r already on their way (16384 x 7168 bf16, a row a workgroup and sums through
+// LDS 190 us, in 8 bits 194). The barrier waits for the sums alone. One row of 7168 takes 3.4 us.
 template <typename T, typename WT, bool WAVE, int VPT, bool MX>
 __global__ void __launch_bounds__(WAVE ? 256 : 1024, !WAVE && VPT == 1 && sizeof(T) == 2 ? 8 : 1) rms_fwd_row(const RmsArgs p) {
   constexpr int RPW = WAVE ? 4 : 1;
@@ -236,7 +239,7 @@ __global__ void __launch_bounds__(WAVE ? 256 : 1024, !WAVE && VPT == 1 && sizeof
   }
 }
 
-// Rows longer than the kernels above hold: a workgroup of 1024 threads reads x and r twice, the
+// Rows longer than the kernels above hold (16384 columns): a workgroup of 1024 threads reads x and r twice, the
 // second time from cache. A thread writes only elements of h that it alone reads.
 template <typename T, typename WT, bool MX>
 __global__ void __launch_bounds__(1024) rms_fwd_long(const RmsArgs p) {
@@ -294,7 +297,8 @@ __global__ void __launch_bounds__(1024) rms_fwd_long(const RmsArgs p) {
 
 // Backward: a workgroup walks every gridDim.x-th row (or four of them, NT = 64) with the next
 // row's (16-bit types: the next two rows') h, dy and dh already on their way, and keeps its columns' dw in registers; they leave once,
-// as one part, for rms_dw_sum to add up.
+// as one part, for rms_dw_sum to add up. The weight waits in LDS and the row stays as it was loaded, which is what lets
+// 20 waves fit a CU: 16384 x 7168 bf16 290 us with both in registers and one row ahead, 219 so.
 template <typename T, typename WT, bool WAVE, int VPT>
 __global__ void __launch_bounds__(WAVE ? 256 : 1024, 4) rms_bwd_row(const RmsArgs p) {
   constexpr int RPW = WAVE ? 4 : 1;
@@ -509,7 +513,8 @@ __global__ void __launch_bounds__(256) rms_dw_long(const RmsArgs p) {
   o.store(p.part + (int64_t)blockIdx.y * p.cols, c, p.cols);
 }
 
-// dw from the parts: 32 columns a workgroup, whose 32 half waves each take every 32nd part, eight at a time.
+// dw from the parts: 32 columns a workgroup, whose 32 half waves each take every 32nd part, eight at a time: 5.6 us for
+// 2047 columns of 1280 parts.
 template <typename WT>
 __global__ void __launch_bounds__(1024) rms_dw_sum(const RmsArgs p) {
   __shared__ float red[32][33];
