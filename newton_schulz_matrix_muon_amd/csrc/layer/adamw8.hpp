@@ -12,8 +12,8 @@
 // alone; m / r stays within its block's range.
 //
 // Bound by HBM: 3 elements, 4 bytes of codes and an eighth of a byte of powers per parameter (10.1 bytes
-// in bf16, 22 with moments in fp32). One MI355X, bf16: 20480 x 7168 and eight 384 x 7168 (169 M) 312 us at 5.5 TB/s; 122 tensors of 7168 in three
-// launches of 8 to 9 us. The arithmetic had to become small for that: 425 us with each code rounded on its own bits
+// in bf16, 22 with moments in fp32). One MI355X, bf16: 20480 x 7168 and eight
+// 384 x 7168 (169 M) 312 us at 5.5 TB/s; 122 tensors of 7168 in three launches of 8 to 9 us. The arithmetic had to become small for that: 425 us with each code rounded on its own bits
 // and a full-precision quotient, 340 with the rounding as an addition and the reciprocal in one instruction.
 #pragma once
 
