@@ -334,10 +334,35 @@ __device__ inline void store_eight(T* out, int c, int n, const f32x4& a, const f
 }
 
 // The activation of a gate's value.
-__device__ inline float activate(float g, int act) {
-  if (act == ACT_SILU) return g / (1.f + __expf(-g));
-  if (act == ACT_GELU) return 0.5f * g * (1.f + erff(g * 0.70710678118654752f));
-  return fmaxf(g, 0.f);
+// For results of 16 bits, whose half step is 2^-12 of the value at least, quotients by the reciprocal to 1 ulp, and the normal
+// distribution below -|g| as t P(t) exp(-g^2 / 2) with t = 1 / (1 + 0.3 |g| / sqrt 2): the polynomial is fitted
+// to erfcx by reweighted least squares (2e-8 off, 5e-7 as evaluated near 0). With erff, which is two branches of
+// polynomials, a forward product of 64 x 1408 x 2048 with 384 rows each took 431 us for gelu, 375 for relu.
+template <typename T, int ACT>
+__device__ inline float activated(float g) {
+  if constexpr (ACT == ACT_RELU) {
+    return fmaxf(g, 0.f);
+  } else if constexpr (ACT == ACT_SILU) {
+    const float d = 1.f + __expf(-g);
+    return sizeof(T) == 2 ? g * __builtin_amdgcn_rcpf(d) : g / d;
+  } else if constexpr (sizeof(T) == 4) {
+    return 0.5f * g * (1.f + erff(g * 0.70710678118654752f));
+  } else {
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.21213204f, __builtin_fabsf(g), 1.f));
+    constexpr float P[9] = {0.084594116f, 0.085356005f, 0.074179493f, 0.10742909f, -0.047254566f, 0.27376783f, -0.25606576f, 0.24274902f, -0.064755239f};
+    float s = P[8];
+#pragma unroll
+    for (int i = 7; i >= 0; --i) s = __builtin_fmaf(s, t, P[i]);
+    s *= t * __expf(-0.5f * g * g);
+    return g * (g < 0.f ? s : 1.f - s);
+  }
+}
+// f(the activation as a constant): chosen once, not once a value.
+template <class F>
+__device__ inline void with_activation(int act, F&& f) {
+  if (act == ACT_SILU) f(std::integral_constant<int, ACT_SILU>{});
+  else if (act == ACT_GELU) f(std::integral_constant<int, ACT_GELU>{});
+  else f(std::integral_constant<int, ACT_RELU>{});
 }
 
 // Columns lc .. lc + 7 of row lr of a slab's tile to C (EX_GATE: from blocks of 32 columns of both products, to C and
@@ -348,11 +373,13 @@ __device__ inline void store_from(const P& p, const ExpertTile& x, int r, int c,
     const int at = (lc >> 5) * 64 + (lc & 31);
     const f32x4 g0 = read(at), g1 = read(at + 4), u0 = read(at + 32), u1 = read(at + 36);
     f32x4 h0, h1;
+    with_activation(p.act, [&](auto act) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      h0[e] = activate(g0[e], p.act) * u0[e];
-      h1[e] = activate(g1[e], p.act) * u1[e];
-    }
+      for (int e = 0; e < 4; ++e) {
+        h0[e] = activated<T, act.value>(g0[e]) * u0[e];
+        h1[e] = activated<T, act.value>(g1[e]) * u1[e];
+      }
+    });
     store_eight(reinterpret_cast<T*>(x.c) + (int64_t)r * p.ldc, c, p.n, h0, h1);
     if (x.c2) {
       store_eight(reinterpret_cast<T*>(x.c2) + (int64_t)r * p.ldc2, c, p.n, g0, g1);

@@ -420,7 +420,9 @@ __global__ void __launch_bounds__(TilePP::NT, TilePP::OCC) expert_gemm_pp(const 
         each(x.c2, p.ldc2, [&](int i, int e) { return acc[i][0][e]; });
         each(x.c3, p.ldc3, [&](int i, int e) { return acc[i][1][e]; });
       }
-      each(x.c, p.ldc, [&](int i, int e) { return activate(acc[i][0][e], p.act) * acc[i][1][e]; });
+      with_activation(p.act, [&](auto act) {
+        each(x.c, p.ldc, [&](int i, int e) { return activated<T, act.value>(acc[i][0][e]) * acc[i][1][e]; });
+      });
     } else {
       const int64_t ldc = row_step<MODE>(p, x);
       const __amdgpu_buffer_rsrc_t rs = result(x.c, ldc, x);
@@ -545,8 +547,10 @@ __global__ void __launch_bounds__(64) expert_split_sum(const typename ArgsOf<MOD
       store_block<T>(lane, result(x.c2, p.ldc2), r0, wn * 32, (int)p.ldc2, x, p.n, [&](int e) { return acc[0][e >> 2][e & 3]; });
       store_block<T>(lane, result(x.c3, p.ldc3), r0, wn * 32, (int)p.ldc3, x, p.n, [&](int e) { return acc[1][e >> 2][e & 3]; });
     }
-    store_block<T>(lane, result(x.c, p.ldc), r0, wn * 32, (int)p.ldc, x, p.n,
-                   [&](int e) { return activate(acc[0][e >> 2][e & 3], p.act) * acc[1][e >> 2][e & 3]; });
+    with_activation(p.act, [&](auto act) {
+      store_block<T>(lane, result(x.c, p.ldc), r0, wn * 32, (int)p.ldc, x, p.n,
+                     [&](int e) { return activated<T, act.value>(acc[0][e >> 2][e & 3]) * acc[1][e >> 2][e & 3]; });
+    });
   } else {
 #pragma unroll
     for (int j = 0; j < 2; ++j)

@@ -160,9 +160,11 @@ __global__ void __launch_bounds__(256, 2) expert_few_gated(const GatedArgs p) {
       if (r < hi) {
         const int c = n0 + 4 * q;
         T* y = reinterpret_cast<T*>(p.C) + (int64_t)r * p.ldc + c;
+        with_activation(p.act, [&](auto act) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (c + i < p.n) y[i] = from_f32<T>(activate(gate[i], p.act) * up[i]);
+          for (int i = 0; i < 4; ++i)
+            if (c + i < p.n) y[i] = from_f32<T>(activated<T, act.value>(gate[i]) * up[i]);
+        });
         if (p.C2) {
           T* g = reinterpret_cast<T*>(p.C2) + (int64_t)r * p.ldc2 + c;
           T* w = reinterpret_cast<T*>(p.C3) + (int64_t)r * p.ldc3 + c;
