@@ -78,8 +78,8 @@ int run_split_pingpong(GatedArgs a, int dt, hipStream_t s) {
 }
 
 // Whether cutting the last round is worth its sum: host arithmetic on a dense product's tiles. Forward products
-// with and without (us, 128 x 64 tiles): 1000 x 2048 x 2048 (32 stages) 48 and 39, 600 x 4096 x 3000 (47) 61 and 68,
-// 600 x 7168 x 4096 (64) 103 and 145.
+// with and without (us, 128 x 64 tiles): 1000 x 2048 x 2048 (32 stages) 46 and 36, 600 x 4096 x 3000 (47) 58 and 61,
+// 400 x 7168 x 4096 (64) 73 and 83.
 template <int MODE>
 bool split_pays(const GatedArgs& a) {
   if (MODE == EX_DW2 || !a.parts || a.offsets) return false;
@@ -116,8 +116,8 @@ bool few_rows(const GatedArgs& a, int dt, int fit) {
 }
 
 // 64 x 64 tiles whose contraction eight waves share: where larger tiles would leave CUs idle, or would be mostly
-// empty. us with these tiles and without: 16-bit forward products of 400 x 2048 x 2048 (448 tiles) 27 and 38,
-// 200 x 4096 x 3000 (512) 37 and 46, 300 x 4096 x 3000 (640) 51 and 50; input gradients of 300 x 7168 x 4096
+// empty. us with these tiles and without: 16-bit forward products of 400 x 2048 x 2048 (448 tiles) 26 and 34,
+// 200 x 4096 x 3000 (512) 36 and 45, 300 x 4096 x 3000 (640) 49 and 48; input gradients of 300 x 7168 x 4096
 // (320) 110 and 85. fp32 has no larger pipelined tiles: 64 experts of 1408 x 2048 with 32 rows each 445 and
 // 760, with 64 rows 698 and 778, with 96 rows 912 and 800.
 template <int MODE>
@@ -145,11 +145,9 @@ int run_product(const GatedArgs& a, int dt, bool vec, hipStream_t s) {
   const int64_t high = ex_dw(MODE) ? tile_rows<MODE, TilePP>(a) : a.rows / 256 + std::min<int64_t>(a.experts, a.rows);
   if constexpr (MODE != EX_DW2)
     if (whole && split_pays<MODE>(a) && !split_tiles<MODE>(a, dt)) return run_split_pingpong<MODE>(a, dt, s);
-  // A forward product's 256 x 128 tiles of few rows are mostly empty: 64 experts of 1408 x 2048 with 64 rows each take
-  // 192 us, with 128 x 64 tiles 167; with 96 rows 198 and 177, with 128 rows 204 and 230 (gradients: none of
-  // the sort, 163 and 177 us at 64 rows).
-  const bool empty = MODE == EX_GATE && a.rows < 112 * std::min<int64_t>(a.experts, a.rows);
-  if (whole && !empty && 2 * high * tile_columns<MODE, TilePP>(a) >= device_cus()) return run_pingpong<MODE>(a, dt, s);
+  // With as few rows as there are these tiles lose little: 64 experts of 1408 x 2048, 24 rows each, forward 154 us, with 128 x 64 tiles
+  // 149; 64 rows 161 and 159, 128 rows 173 and 228; 27 experts of 2048 x 7168 291 and 295, 300 and 313, 346 and 460.
+  if (whole && 2 * high * tile_columns<MODE, TilePP>(a) >= device_cus()) return run_pingpong<MODE>(a, dt, s);
   if (split_tiles<MODE>(a, dt)) return run_staged<MODE, Tile64, 8>(a, dt, fit, s);
   return run_staged<MODE, Tile128, 1>(a, dt, fit, s);
 }
