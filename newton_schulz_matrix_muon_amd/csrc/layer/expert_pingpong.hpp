@@ -23,7 +23,8 @@
 // An XCD takes a part of the tile list. A weight gradient's tiles cost as many stages as their expert has rows, so
 // its parts have equal cost (cost_list): 27 x 2048 x 7168 of a router's 32768 rows 1044 us with equal numbers of tiles,
 // 867 so. SPLIT: the last round of a dense product (last_round), 509 rows of 18432 x 7168 forward 336 to 265 us,
-// input gradient 551 to 298.
+// input gradient 551 to 298. The gated block's activation is chosen once a tile: chosen value by value, its code came three
+// times for each and the instructions were fetched again and again (384 rows each over 64 x 1408 x 2048, silu, 383 us, 326 so).
 //
 // Bound by the board's power and LDS. 4 x 2048 rows against 2048 x 7168, bf16, held for a second:
 // 177 us (1357 TFLOP/s) at 1.59 GHz and 1330 W, 2500 cycles a stage of 2048 MFMA cycles; on zeros

@@ -13,9 +13,9 @@
 // product holds 32 columns of either matrix side by side, so that a lane has gate and up of the same element; the
 // input gradient's contraction runs through one matrix and on through the other; the weight gradients' tiles
 // are those of both matrices, so X and its rows are shared in L2. Bound by MFMA and the board's power, by HBM where there
-// are few rows. One MI355X: 32768 rows over 27 experts of 2048 x 7168 bf16, gate and up kept, 1850 us (1042
-// TFLOP/s; a large plain product of the vendor's library 1360 to 1580); 24594 rows over 64 experts of 1408 x 2048 fp16, backward 790:
-// gated_grad 70, input gradient 305 to 330, weight gradients 390 to 440; one token of 6 such experts 16.4 us (4.2
+// are few rows. One MI355X: 32768 rows over 27 experts of 2048 x 7168 bf16, gate and up kept, 1760 us (1093
+// TFLOP/s; a large plain product of the vendor's library 1360 to 1600); 24594 rows over 64 experts of 1408 x 2048 fp16, backward 790:
+// gated_grad 70, input gradient 305 to 330, weight gradients 390 to 440; one token of 6 such experts 16.0 us (4.3
 // TB/s with the launch).
 //
 // The activation takes the fp32 sums. What the backward pass needs is gate and up, kept in the rows' type.
