@@ -433,6 +433,7 @@ MNS_API int adamw8_step(int ntensors, void* const* params, const void* const* gr
  * ws: a dense call (offsets NULL) in 16 bits may take a workspace, in which the tiles of a last round that would leave
  * most CUs idle are cut along the contraction; without it, or with a smaller one, the call runs uncut.
  *   MNS_ACT_SILU  g / (1 + exp(-g));  MNS_ACT_GELU  g (1 + erf(g / sqrt(2))) / 2;  MNS_ACT_RELU  max(g, 0)
+ * A gate that is NaN gives NaN with every activation.
  */
 #define MNS_ACT_SILU 0
 #define MNS_ACT_GELU 1

@@ -341,7 +341,7 @@ __device__ inline void store_eight(T* out, int c, int n, const f32x4& a, const f
 template <typename T, int ACT>
 __device__ inline float activated(float g) {
   if constexpr (ACT == ACT_RELU) {
-    return fmaxf(g, 0.f);
+    return g <= 0.f ? 0.f : g;   // a maximum instruction would turn a NaN into 0
   } else if constexpr (ACT == ACT_SILU) {
     const float d = 1.f + __expf(-g);
     return sizeof(T) == 2 ? g * __builtin_amdgcn_rcpf(d) : g / d;

@@ -7,7 +7,9 @@
 //
 //   silu  g s(g), s(g) = 1 / (1 + exp(-g));  slope s (1 + g (1 - s))
 //   gelu  g F(g), F(g) = (1 + erf(g / sqrt 2)) / 2;  slope F + g exp(-g^2 / 2) / sqrt(2 pi)
-//   relu  max(g, 0);  slope 1 where g > 0
+//   relu  max(g, 0);  slope 1 where g > 0, else 0
+//
+// A gate that is no number stays one in every activation, so that H, dup and what they reach show it.
 //
 // The products are the experts' (expert_gemm.hpp, expert_pingpong.hpp) with two matrices each: a tile of the forward
 // product holds 32 columns of either matrix side by side, so that a lane has gate and up of the same element; the
@@ -38,7 +40,7 @@ __device__ inline void activate_slope(float g, int act, float* a, float* slope) 
     *a = g * f;
     *slope = f + g * __expf(-0.5f * g * g) * 0.39894228040143268f;
   } else {
-    *a = fmaxf(g, 0.f);
+    *a = g <= 0.f ? 0.f : g;   // NaN stays
     *slope = g > 0.f ? 1.f : 0.f;
   }
 }

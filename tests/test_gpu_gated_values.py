@@ -1,0 +1,63 @@
+"""The gated block's values away from ordinary ones: gates that are infinite or no numbers."""
+import pytest
+
+from test_gpu_gated import ACTS, activate, make
+from test_gpu_layer import gen_for, normal, ops, torch, uneven  # noqa: F401 (fixtures)
+
+pytestmark = pytest.mark.gpu
+
+# the kernel for few rows, 64 x 64 tiles split over waves, 128 x 64 tiles, 256 x 256 tiles, a dense layer's cut last round
+PATHS = [([2, 0, 1], 136, 264, False), ([40, 0, 70], 72, 328, False), ([300, 0, 200], 130, 136, False), (uneven(60, 300, 9), 264, 328, False),
+         ([600], 2064, 2568, True)]
+name = lambda p: f"{len(p[0])}x{sum(p[0])}_{p[1]}x{p[2]}"  # noqa: E731
+
+
+def same_kind(torch, got, want, what):
+    """NaN where the definition has one, and its infinities; the rest within 1/16 (its accuracy is measured elsewhere)."""
+    got = got.double()
+    assert torch.equal(torch.isnan(got), torch.isnan(want)), (what, int((torch.isnan(got) != torch.isnan(want)).sum()))
+    assert torch.equal(got.isinf() * got.sign().nan_to_num(), want.isinf() * want.sign().nan_to_num()), what
+    fine = want.isfinite()
+    a, b = got[fine], want[fine]
+    assert float((a - b).norm()) <= float(b.norm()) / 16, what
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16", "float32"])
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("path", PATHS, ids=name)
+def test_gates_that_are_no_numbers_or_infinite(torch, ops, path, act, dtype):
+    counts, n, k, dense = path
+    dt = getattr(torch, dtype)
+    gen = gen_for(torch, n + 1)
+    x, dh, wg, wu, offsets = make(torch, gen, dt, counts, 0, n, k)
+    rows = sum(counts)
+    expert = torch.repeat_interleave(torch.arange(len(counts), device="cuda"), torch.tensor(counts, device="cuda"))
+    args = (wg[0], wu[0], None) if dense else (wg, wu, offsets)
+    # forward: a column of gates that are NaN, one of infinities of both signs
+    x[:, 0] = 1 - 2.0 * (torch.arange(rows, device="cuda") % 2)
+    good = wg.clone()
+    wg[:, 1, 3] = float("nan")
+    wg[:, n - 1] = 0
+    wg[:, n - 1, 0] = float("inf")
+    h, gate, up = ops.expert_gated(x, *args, act=act, keep=True)
+    assert torch.equal(h.isnan(), ops.expert_gated(x, *args, act=act).isnan())
+    assert gate[:, 1].isnan().all() and (gate[:, n - 1] == x[:, 0] * float("inf")).all()
+    g, u = gate.double(), up.double()
+    same_kind(torch, h, activate(torch, g, act)[0] * u, "h")
+    # backward: such gates in some rows, every matrix finite
+    wg.copy_(good)
+    _, gate, up = ops.expert_gated(x, *args, act=act, keep=True)
+    gate[0::7, 1] = float("nan")
+    gate[1::7, n - 1] = float("inf")
+    gate[2::7, 5] = float("-inf")
+    v, s = activate(torch, gate.double(), act)
+    dg, du = dh.double() * up.double() * s, dh.double() * v
+    dx, dwg, dwu = ops.expert_gated_backward(dh, x, *args[:2], gate, up, args[2], act=act)
+    dwg, dwu = dwg.view(wg.shape), dwu.view(wu.shape)
+    assert dwu[:, 1].isnan().any() and dx[0::7].isnan().all()
+    for e in range(len(counts)):
+        r = expert == e
+        a, b = dg[r], du[r]
+        same_kind(torch, dx[r], a @ wg[e].double() + b @ wu[e].double(), f"dx of expert {e}")
+        same_kind(torch, dwg[e], a.T @ x[r].double(), f"dw_gate of expert {e}")
+        same_kind(torch, dwu[e], b.T @ x[r].double(), f"dw_up of expert {e}")
