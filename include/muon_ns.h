@@ -412,12 +412,18 @@ MNS_API int embed_backward(const mns_tensor* dY, const void* tokens, int32_t id_
  * ap->step (count it up), the tensor's place in the list and the element's in the tensor.
  * params and grads as for adamw_step, at most 2^34 elements a tensor; no two buffers may overlap. The
  * hyper-parameters are doubles: 1 - beta is rounded to fp32 once.
+ * device_step: NULL, or a device int64 from which the kernels read the step when they run (it is not written; a value
+ * outside 1 .. 2^31 - 1 counts as the nearest of them, and `step` is not read). A call that is captured into a graph
+ * needs it: with `step` from the host every replay rounds with the captured step's random numbers, so that a state
+ * whose change is below a code's step never moves, and keeps that step's bias corrections. With device_step, advanced
+ * before each replay (in the graph, for one), replays give the bits of calls whose step counts up.
  */
 typedef struct mns_adamw8_params {
   double lr, beta1, beta2, eps, weight_decay;
   int32_t step;             /* >= 1 */
   int32_t bias_correction;  /* 0 or 1 */
   uint64_t seed;
+  const int64_t* device_step; /* or NULL: `step` counts */
 } mns_adamw8_params;
 MNS_API int adamw8_step(int ntensors, void* const* params, const void* const* grads, uint8_t* const* exp_avg,
                         uint8_t* const* exp_avg_scale, uint8_t* const* root, uint8_t* const* root_scale, const int64_t* numels,

@@ -35,11 +35,16 @@ struct Adam8Table {
   uint8_t* rs[ADAM8_MAXT];
   int64_t numel[ADAM8_MAXT];
   int blk_start[ADAM8_MAXT + 1];              // first workgroup of each tensor
-  uint32_t key[ADAM8_MAXT];                   // of the tensor's random numbers
+  uint32_t key[ADAM8_MAXT];                   // of the tensor's random numbers; its place in the list where the step lies on the device
   int nt;
   float lr, beta1, beta2, eps, wd_mul;        // wd_mul = 1 - lr * weight_decay
   float one_beta1, one_beta2;                 // 1 - beta1, 1 - beta2, rounded once
   float bc1, bc2;                             // bias correction of m and of r (1 when off)
+  // the step on the device (DEV): read when the kernel runs, so that a captured call's replays go on counting
+  const int64_t* step;
+  uint32_t seed;                              // adam8_seed
+  int correct;                                // bias corrections of the step read
+  double wide1, wide2;                        // beta1, beta2 for them
 };
 
 // Random bits: a number's bits mixed, which the tensor's key and an element's place go through.
@@ -50,6 +55,16 @@ __host__ __device__ inline uint32_t adam8_mix(uint32_t x) {
   x ^= x >> 15;
   x *= ADAM8_MIX2;
   return x ^ (x >> 16);
+}
+__host__ __device__ inline uint32_t adam8_seed(uint64_t seed) { return adam8_mix(adam8_mix((uint32_t)seed) ^ (uint32_t)(seed >> 32)); }
+__host__ __device__ inline uint32_t adam8_key(uint32_t seed, uint32_t step, uint32_t place) { return adam8_mix(adam8_mix(seed ^ step) ^ place); }
+// 1 / (1 - beta^step), the power by squaring: the same bits from the host and from the kernel.
+__host__ __device__ inline double adam8_correction(double beta, uint32_t step) {
+#pragma clang fp contract(off)
+  double power = 1.0;
+  for (; step; step >>= 1, beta *= beta)
+    if (step & 1) power *= beta;
+  return 1.0 / (1.0 - power);
 }
 // Elements i .. i + 7 (i a multiple of 8): 16 bits for m (low) and 16 for r (high) each.
 __device__ inline void adam8_bits(uint32_t key, int64_t i, uint32_t (&rnd)[8]) {
@@ -167,7 +182,8 @@ struct Adam8Vec {
   }
 };
 
-template <typename T>
+// DEV: the step, and with it the random numbers and the bias corrections, comes from the device's memory.
+template <typename T, bool DEV>
 __global__ void __launch_bounds__(ADAM8_BLOCK) adamw8_kernel(const Adam8Table t) {
   int ti = 0;
   while (ti + 1 < t.nt && (int)blockIdx.x >= t.blk_start[ti + 1]) ++ti;
@@ -192,6 +208,25 @@ __global__ void __launch_bounds__(ADAM8_BLOCK) adamw8_kernel(const Adam8Table t)
     mb[it] = t.ms[ti][i / MX_BLOCK];
     rb[it] = t.rs[ti][i / MX_BLOCK];
   }
+  uint32_t key = t.key[ti];
+  float bc1 = t.bc1, bc2 = t.bc2;
+  if constexpr (DEV) {
+    const uint32_t step = (uint32_t)max((int64_t)1, min(*t.step, (int64_t)0x7fffffff));
+    key = adam8_key(t.seed, step, key);
+    if (t.correct) {                          // one wave works them out
+      __shared__ float fix[2];
+      if (threadIdx.x < 64) {
+        const double c1 = adam8_correction(t.wide1, step), c2 = __builtin_sqrt(adam8_correction(t.wide2, step));
+        if (threadIdx.x == 0) {
+          fix[0] = (float)c1;
+          fix[1] = (float)c2;
+        }
+      }
+      __syncthreads();
+      bc1 = fix[0];
+      bc2 = fix[1];
+    }
+  }
 #pragma unroll
   for (int it = 0; it < ADAM8_ITERS; ++it) {
     const int64_t i = base + ((int64_t)it * ADAM8_BLOCK + threadIdx.x) * 8;
@@ -211,10 +246,10 @@ __global__ void __launch_bounds__(ADAM8_BLOCK) adamw8_kernel(const Adam8Table t)
         mf[e] = adam8_sum<T>(t.beta1, mf[e], t.one_beta1, gf[e]);
         rf[e] = adam8_sqrt<T>(adam8_sum<T>(t.beta2, rf[e] * rf[e], t.one_beta2, gf[e] * gf[e]));
         // the reciprocal to 1 ulp: its error in p is 2^-23 of the step
-        pf[e] = t.wd_mul * pf[e] - t.lr * ((mf[e] * t.bc1) * __builtin_amdgcn_rcpf(rf[e] * t.bc2 + t.eps));
+        pf[e] = t.wd_mul * pf[e] - t.lr * ((mf[e] * bc1) * __builtin_amdgcn_rcpf(rf[e] * bc2 + t.eps));
       }
     }
-    adam8_bits(t.key[ti], i, rnd);
+    adam8_bits(key, i, rnd);
     if (i + 8 > n) {
 #pragma unroll
       for (int e = 0; e < 8; ++e)

@@ -169,9 +169,14 @@ int run_adamw8(int nt, void* const* params, const void* const* grads, uint8_t* c
   t.one_beta2 = (float)(1.0 - ap->beta2);
   t.eps = (float)ap->eps;
   t.wd_mul = (float)(1.0 - ap->lr * ap->weight_decay);
-  t.bc1 = ap->bias_correction ? (float)(1.0 / (1.0 - std::pow(ap->beta1, ap->step))) : 1.f;
-  t.bc2 = ap->bias_correction ? (float)std::sqrt(1.0 / (1.0 - std::pow(ap->beta2, ap->step))) : 1.f;
-  const uint32_t key = adam8_mix(adam8_mix(adam8_mix((uint32_t)ap->seed) ^ (uint32_t)(ap->seed >> 32)) ^ (uint32_t)ap->step);
+  const bool dev = ap->device_step != nullptr;
+  t.bc1 = ap->bias_correction && !dev ? (float)adam8_correction(ap->beta1, (uint32_t)ap->step) : 1.f;
+  t.bc2 = ap->bias_correction && !dev ? (float)std::sqrt(adam8_correction(ap->beta2, (uint32_t)ap->step)) : 1.f;
+  t.step = ap->device_step;
+  t.seed = adam8_seed(ap->seed);
+  t.correct = ap->bias_correction;
+  t.wide1 = ap->beta1;
+  t.wide2 = ap->beta2;
   int i = 0;
   while (i < nt) {
     int k = 0;
@@ -188,7 +193,7 @@ int run_adamw8(int nt, void* const* params, const void* const* grads, uint8_t* c
       t.rs[k] = rs[i];
       t.numel[k] = numels[i];
       t.blk_start[k] = (int)blocks;
-      t.key[k] = adam8_mix(key ^ (uint32_t)i);
+      t.key[k] = dev ? (uint32_t)i : adam8_key(t.seed, (uint32_t)ap->step, (uint32_t)i);
       blocks += b;
       ++k;
     }
@@ -197,7 +202,10 @@ int run_adamw8(int nt, void* const* params, const void* const* grads, uint8_t* c
     t.nt = k;
     if (int st = by_type(dt, [&](auto x) {
           using T = decltype(x);
-          return launch(K_ADAMW, s, [&] { hipLaunchKernelGGL(adamw8_kernel<T>, dim3((unsigned)blocks), dim3(ADAM8_BLOCK), 0, s, t); });
+          return launch(K_ADAMW, s, [&] {
+            if (dev) hipLaunchKernelGGL((adamw8_kernel<T, true>), dim3((unsigned)blocks), dim3(ADAM8_BLOCK), 0, s, t);
+            else hipLaunchKernelGGL((adamw8_kernel<T, false>), dim3((unsigned)blocks), dim3(ADAM8_BLOCK), 0, s, t);
+          });
         }))
       return st;
   }
@@ -429,9 +437,11 @@ int adamw8_step(int ntensors, void* const* params, const void* const* grads, uin
   for (double x : {ap->lr, ap->beta1, ap->beta2, ap->eps, ap->weight_decay})
     if (!std::isfinite((float)x)) return MNS_ERR_ARG;
   if (ap->beta1 < 0. || ap->beta1 >= 1. || ap->beta2 < 0. || ap->beta2 >= 1. || ap->eps < 0.) return MNS_ERR_ARG;
-  if ((ap->bias_correction != 0 && ap->bias_correction != 1) || ap->step < 1) return MNS_ERR_ARG;
+  if ((ap->bias_correction != 0 && ap->bias_correction != 1) || (!ap->device_step && ap->step < 1)) return MNS_ERR_ARG;
+  if (reinterpret_cast<uintptr_t>(ap->device_step) % 8) return MNS_ERR_ARG;
   // every buffer there (unless empty) and aligned to its elements, no two of them overlapping
   std::vector<std::pair<uintptr_t, uintptr_t>> iv;
+  if (const uintptr_t at = reinterpret_cast<uintptr_t>(ap->device_step)) iv.push_back({at, at + 8});
   const uintptr_t es = (uintptr_t)dtype_size(dtype);
   for (int i = 0; i < ntensors; ++i) {
     if (numels[i] < 0) return MNS_ERR_ARG;

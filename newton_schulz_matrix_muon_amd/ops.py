@@ -10,6 +10,7 @@ from __future__ import annotations
 import array
 import ctypes
 import os
+import warnings
 from typing import NamedTuple, Optional, Sequence
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -525,7 +526,7 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, *, lr: float, beta1: float 
 class MnsAdamw8Params(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
                 ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("step", ctypes.c_int32),
-                ("bias_correction", ctypes.c_int32), ("seed", ctypes.c_uint64)]
+                ("bias_correction", ctypes.c_int32), ("seed", ctypes.c_uint64), ("device_step", ctypes.c_void_p)]
 
 
 MX_BLOCK = 32   # elements that share a power of two in 8-bit values
@@ -550,17 +551,25 @@ def adamw8_state(param) -> Adamw8State:
                        zeros(n, torch.float8_e4m3fn), zeros(blocks, torch.float8_e8m0fnu))
 
 
-def adamw8_step(params, grads, states, *, lr: float, step: int, beta1: float = 0.9, beta2: float = 0.95, eps: float = 1e-8,
+def adamw8_step(params, grads, states, *, lr: float, step, beta1: float = 0.9, beta2: float = 0.95, eps: float = 1e-8,
                 weight_decay: float = 0.1, bias_correction: bool = False, seed: int = 0):
     """One AdamW step over lists of contiguous tensors with their moments in 8 bits (C ABI ``adamw8_step``);
     params and states (adamw8_state's, or tuples like it) are updated in place. The states are rounded at
-    random: the numbers depend on seed, step (count it up), a tensor's place in the list and the element's."""
+    random: the numbers depend on seed, step (count it up), a tensor's place in the list and the element's.
+    step: an int, or a device tensor of one int64 that is read when the kernels run. A call captured into a graph
+    needs the tensor, advanced in the graph or before each replay (``step.add_(1)``): replays of a captured int round
+    with the same numbers every time, and moments whose change is below a code's step stand still."""
     torch = _torch()
     what = "adamw8_step"
     n = len(params)
     if not (len(grads) == len(states) == n) or n == 0:
         raise ValueError(f"{what}: params, grads and states must be non-empty lists of equal length")
-    if not 1 <= step < 2 ** 31:
+    device_step = step if isinstance(step, torch.Tensor) else None
+    if device_step is not None:
+        _check_flat(what, params[0], (torch.int64,), step=device_step)
+        if device_step.numel() != 1:
+            raise ValueError(f"{what}: a step on the device must be one number, got {device_step.numel()}")
+    elif not 1 <= step < 2 ** 31:
         raise ValueError(f"{what}: step must count from 1, got {step}")
     if not 0 <= seed < 2 ** 64:
         raise ValueError(f"{what}: seed must fit 64 bits, got {seed}")
@@ -594,10 +603,16 @@ def adamw8_step(params, grads, states, *, lr: float, step: int, beta1: float = 0
         if set(map(Tensor.get_device, column)) != {index}:
             i = next(i for i, t in enumerate(column) if t.get_device() != index)
             raise ValueError(f"{what}: {name}[{i}] is on {column[i].device}, expected {device}")
+    if device_step is not None and device_step.get_device() != index:
+        raise ValueError(f"{what}: step is on {device_step.device}, expected {device}")
+    if device_step is None and torch.cuda.is_current_stream_capturing():
+        warnings.warn(f"{what}: captured with a step from the host, whose random numbers every replay uses again; give step as a "
+                      "device tensor", stacklevel=2)
     pointers = ctypes.c_void_p * n
     lists = [pointers.from_buffer(array.array("Q", map(Tensor.data_ptr, column))) for column in columns]
     sizes = (ctypes.c_int64 * n).from_buffer(array.array("q", numels))
-    ap = MnsAdamw8Params(lr, beta1, beta2, eps, weight_decay, step, 1 if bias_correction else 0, seed)
+    ap = MnsAdamw8Params(lr, beta1, beta2, eps, weight_decay, 1 if device_step is not None else step, 1 if bias_correction else 0, seed,
+                         _ptr(device_step))
     _launch(what, params[0], n, *lists, sizes, code, ctypes.byref(ap))
     return params
 
@@ -607,7 +622,13 @@ def hybrid_step(matrix_groups, vector_params, *, muon: dict, adamw: dict, seed: 
     (W, G, M) batches, one grouped call) and AdamW for everything else (``vector_params``:
     list of (param, grad, exp_avg, exp_avg_sq), or (param, grad, adamw8_state(param)) where the
     moments are held in 8 bits; those need ``step`` in ``adamw`` and take ``seed``), enqueued on the
-    current stream."""
+    current stream. A step on the device (adamw8_step) goes with moments in 32 bits only without their
+    bias correction, which adamw_step works out on the host."""
+    adamw32 = adamw
+    if isinstance(adamw.get("step"), _torch().Tensor):
+        if adamw.get("bias_correction") and any(len(v) == 4 for v in vector_params or ()):
+            raise ValueError("hybrid_step: adamw_step corrects its bias by a step on the host, got one on the device")
+        adamw32 = {k: v for k, v in adamw.items() if k != "step"}
     if matrix_groups:
         Ws, Gs, Ms = (list(x) for x in zip(*matrix_groups))
         muon_step_grouped(Ws, Gs, Ms, **muon)
@@ -615,7 +636,7 @@ def hybrid_step(matrix_groups, vector_params, *, muon: dict, adamw: dict, seed: 
     in8 = [v for v in vector_params or () if len(v) != 4]
     if in32:
         ps, gs, ms, vs = (list(x) for x in zip(*in32))
-        adamw_step(ps, gs, ms, vs, **adamw)
+        adamw_step(ps, gs, ms, vs, **adamw32)
     if in8:
         ps, gs, ss = (list(x) for x in zip(*in8))
         adamw8_step(ps, gs, ss, seed=seed, **adamw)
