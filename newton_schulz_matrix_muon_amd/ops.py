@@ -624,16 +624,22 @@ def hybrid_step(matrix_groups, vector_params, *, muon: dict, adamw: dict, seed: 
     moments are held in 8 bits; those need ``step`` in ``adamw`` and take ``seed``), enqueued on the
     current stream. A step on the device (adamw8_step) goes with moments in 32 bits only without their
     bias correction, which adamw_step works out on the host."""
+    entries = list(vector_params or ())   # may be an iterator, which is gone through once
+    for i, v in enumerate(entries):
+        if len(v) not in (3, 4):
+            raise ValueError(f"hybrid_step: entry {i} of vector_params holds {len(v)} things, expected 3 or 4")
+    in32 = [v for v in entries if len(v) == 4]
+    in8 = [v for v in entries if len(v) == 3]
+    if in8 and "step" not in adamw:
+        raise TypeError("hybrid_step: moments in 8 bits need step in adamw")
     adamw32 = adamw
     if isinstance(adamw.get("step"), _torch().Tensor):
-        if adamw.get("bias_correction") and any(len(v) == 4 for v in vector_params or ()):
+        if adamw.get("bias_correction") and in32:
             raise ValueError("hybrid_step: adamw_step corrects its bias by a step on the host, got one on the device")
         adamw32 = {k: v for k, v in adamw.items() if k != "step"}
     if matrix_groups:
         Ws, Gs, Ms = (list(x) for x in zip(*matrix_groups))
         muon_step_grouped(Ws, Gs, Ms, **muon)
-    in32 = [v for v in vector_params or () if len(v) == 4]
-    in8 = [v for v in vector_params or () if len(v) != 4]
     if in32:
         ps, gs, ms, vs = (list(x) for x in zip(*in32))
         adamw_step(ps, gs, ms, vs, **adamw32)
