@@ -63,7 +63,16 @@ __global__ void __launch_bounds__(256) gated_grad(const GatedGradArgs p, int act
   const unsigned x = (unsigned)(first - r0 * p.units) + threadIdx.x;
   const unsigned q = x / (unsigned)p.units;
   const int64_t r = r0 + q;
-  if (r >= p.rows || (p.offsets && r >= p.offsets[p.experts])) return;
+  bool own = r < p.rows && (!p.offsets || r < p.offsets[p.experts]);
+  if (__any(!own && r < p.rows)) {
+    // behind the last offset, which need not be the largest (expert_rows): no expert ends behind `end`
+    int end = 0;
+    for (int e = threadIdx.x & 63; e < p.experts; e += 64) end = max(end, p.offsets[e + 1] > p.offsets[e] ? p.offsets[e + 1] : 0);
+#pragma unroll
+    for (int o = 32; o; o >>= 1) end = max(end, __shfl_xor(end, o));
+    own = r < min((int64_t)end, p.rows);
+  }
+  if (!own) return;
   const int c = (int)(x - q * (unsigned)p.units) * 8;
   auto load = [&](const char* base, int64_t ld, float (&f)[8]) {
     const T* row = reinterpret_cast<const T*>(base) + r * ld;

@@ -61,3 +61,18 @@ def test_gates_that_are_no_numbers_or_infinite(torch, ops, path, act, dtype):
         same_kind(torch, dx[r], a @ wg[e].double() + b @ wu[e].double(), f"dx of expert {e}")
         same_kind(torch, dwg[e], a.T @ x[r].double(), f"dw_gate of expert {e}")
         same_kind(torch, dwu[e], b.T @ x[r].double(), f"dw_up of expert {e}")
+
+
+def test_offsets_whose_last_is_not_their_largest_read_no_stale_workspace(torch, ops):
+    """[0, rows, 3]: every row is the first expert's, whose weights' gradients are those of [0, rows, rows], whatever the workspace held."""
+    gen = gen_for(torch, 15)
+    for rows, n, k, dt in ((10, 64, 64, torch.float32), (300, 264, 328, torch.bfloat16), (2000, 520, 136, torch.float16)):
+        x, dh, wg, wu, ordered = make(torch, gen, dt, [rows, 0], 0, n, k)
+        _, gate, up = ops.expert_gated(x, wg, wu, ordered, keep=True)
+        want = ops.expert_gated_backward(dh, x, wg, wu, gate, up, ordered)
+        falls = torch.tensor([0, rows, 3], dtype=torch.int32, device="cuda")
+        for byte in (0, 255):
+            ws = torch.full((ops.expert_gated_workspace_bytes(rows, n, x)[1],), byte, dtype=torch.uint8, device="cuda")
+            got = ops.expert_gated_backward(dh, x, wg, wu, gate, up, falls, workspace=ws)
+            assert all(torch.equal(a, b) for a, b in zip(got[1:], want[1:])), (rows, byte)
+            assert torch.equal(got[0][:3], want[0][:3]) and not got[0].isnan().any()
