@@ -333,6 +333,13 @@ __device__ inline void store_eight(T* out, int c, int n, const f32x4& a, const f
   }
 }
 
+// exp(x) for rows of T: fp32 to an ulp; for 16 bits as exp2 of a rounded argument, off by |x| 2^-24 of it, which is far below
+// the rows' half step wherever the activation is not 0 in them.
+template <typename T>
+__device__ inline float row_exp(float x) {
+  return sizeof(T) == 4 ? expf(x) : __expf(x);
+}
+
 // The activation of a gate's value.
 // For results of 16 bits, whose half step is 2^-12 of the value at least, quotients by the reciprocal to 1 ulp, and the normal
 // distribution below -|g| as t P(t) exp(-g^2 / 2) with t = 1 / (1 + 0.3 |g| / sqrt 2): the polynomial is fitted
@@ -343,7 +350,7 @@ __device__ inline float activated(float g) {
   if constexpr (ACT == ACT_RELU) {
     return g <= 0.f ? 0.f : g;   // a maximum instruction would turn a NaN into 0
   } else if constexpr (ACT == ACT_SILU) {
-    const float d = 1.f + __expf(-g);
+    const float d = 1.f + row_exp<T>(-g);
     return sizeof(T) == 2 ? g * __builtin_amdgcn_rcpf(d) : g / d;
   } else if constexpr (sizeof(T) == 4) {
     return 0.5f * g * (1.f + erff(g * 0.70710678118654752f));

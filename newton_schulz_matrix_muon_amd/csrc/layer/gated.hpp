@@ -30,15 +30,17 @@
 namespace mns {
 
 // The activation's value and slope.
+template <typename T>
 __device__ inline void activate_slope(float g, int act, float* a, float* slope) {
   if (act == ACT_SILU) {
-    const float s = 1.f / (1.f + __expf(-g));
+    // 1 - s as t s: as a difference it is off by 2^-24, which g multiplies
+    const float t = row_exp<T>(-g), s = 1.f / (1.f + t), rest = s > 0.f ? t * s : 1.f;
     *a = g * s;
-    *slope = s * (1.f + g * (1.f - s));
+    *slope = s * (1.f + g * rest);
   } else if (act == ACT_GELU) {
     const float f = 0.5f * (1.f + erff(g * 0.70710678118654752f));
     *a = g * f;
-    *slope = f + g * __expf(-0.5f * g * g) * 0.39894228040143268f;
+    *slope = f + g * row_exp<T>(-0.5f * g * g) * 0.39894228040143268f;
   } else {
     *a = g <= 0.f ? 0.f : g;   // NaN stays
     *slope = g > 0.f ? 1.f : 0.f;
@@ -96,7 +98,7 @@ __global__ void __launch_bounds__(256) gated_grad(const GatedGradArgs p, int act
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     float a, slope;
-    activate_slope(g[e], act, &a, &slope);
+    activate_slope<T>(g[e], act, &a, &slope);
     dg[e] = c + e < p.n ? d[e] * u[e] * slope : 0.f;
     du[e] = c + e < p.n ? d[e] * a : 0.f;
   }

@@ -76,3 +76,35 @@ def test_offsets_whose_last_is_not_their_largest_read_no_stale_workspace(torch, 
             got = ops.expert_gated_backward(dh, x, wg, wu, gate, up, falls, workspace=ws)
             assert all(torch.equal(a, b) for a, b in zip(got[1:], want[1:])), (rows, byte)
             assert torch.equal(got[0][:3], want[0][:3]) and not got[0].isnan().any()
+
+
+U = 2.0 ** -24
+
+
+@pytest.mark.parametrize("act", ["silu"])
+def test_activation_of_fp32_rows_over_its_range(torch, ops, act):
+    """The activation and its slope as fp32 functions evaluated to a few roundings, wherever the gate lies: up = 1 and one column of
+    x, so that gate, h and both gradients are exact but for them."""
+    n = 4096
+    gates = torch.linspace(-80.0, 80.0, n, device="cuda") + 0.013
+    if act == "gelu":
+        gates /= 8                            # its tail ends at -13 in fp32
+    x = torch.ones(1, 1, device="cuda")
+    wg, wu = gates[:, None].clone(), torch.ones(n, 1, device="cuda")
+    h, gate, up = ops.expert_gated(x, wg, wu, act=act, keep=True)
+    assert torch.equal(gate[0], gates) and (up == 1).all()
+    g = gates.double()
+    v, s = activate(torch, g, act)
+    if act == "silu":
+        # exp to an ulp (2 U), 1 + exp, the quotient and the product a rounding each; the slope a few more of terms up to |g| s
+        ev, es = 6 * U * v.abs(), 12 * U * (torch.sigmoid(g) * (1 + g.abs() * torch.sigmoid(-g)))
+    else:
+        # erfc's argument is rounded: 2 t^2 = g^2 of it in the tail, to 8 ulp; exp(-g^2 / 2) likewise
+        f = 0.5 * torch.erfc(-g / 2 ** 0.5)
+        tail = torch.where(g < 0, g * g, torch.zeros_like(g))
+        ev = (20 + 2 * tail) * U * v.abs()
+        es = (20 + 2 * tail) * U * f + (6 + 2 * g * g) * U * g.abs() * torch.exp(-g * g / 2) * 0.4
+    assert ((h[0].double() - v).abs() <= ev + 1e-37).all(), ((h[0].double() - v).abs() / (v.abs() * U)).max()
+    _, dwg, dwu = ops.expert_gated_backward(torch.ones(1, n, device="cuda"), x, wg, wu, gate, up, act=act)
+    assert ((dwu[:, 0].double() - v).abs() <= ev + 1e-37).all(), ((dwu[:, 0].double() - v).abs() / (v.abs() * U)).max()
+    assert ((dwg[:, 0].double() - s).abs() <= es + 1e-37).all(), ((dwg[:, 0].double() - s).abs() / (s.abs() * U)).max()
