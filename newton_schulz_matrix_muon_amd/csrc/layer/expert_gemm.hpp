@@ -340,11 +340,25 @@ __device__ inline float row_exp(float x) {
   return sizeof(T) == 4 ? expf(x) : __expf(x);
 }
 
-// The activation of a gate's value.
-// For results of 16 bits, whose half step is 2^-12 of the value at least, quotients by the reciprocal to 1 ulp, and the normal
-// distribution below -|g| as t P(t) exp(-g^2 / 2) with t = 1 / (1 + 0.3 |g| / sqrt 2): the polynomial is fitted
-// to erfcx by reweighted least squares (2e-8 off, 5e-7 as evaluated near 0). With erff, which is two branches of
-// polynomials, a forward product of 64 x 1408 x 2048 with 384 rows each took 431 us for gelu, 375 for relu.
+// F(g), the normal distribution's part below g, and exp(-g^2 / 2). By erfc, not 1 + erf, which has lost the digits of a part
+// near 0 (all of them from g = -5.4 on). For rows of 16 bits, whose half step is 2^-12 of the value at least, the part below -|g| as
+// t P(t) exp(-g^2 / 2) with t = 1 / (1 + 0.3 |g| / sqrt 2): the polynomial is fitted to erfcx by reweighted least
+// squares (2e-8 off, 5e-7 as evaluated near 0). With erff, which is two branches of polynomials, a forward product of
+// 64 x 1408 x 2048 with 384 rows each took 431 us for gelu, 375 for relu.
+template <typename T>
+__device__ inline float normal_part(float g, float* density) {
+  *density = row_exp<T>(-0.5f * g * g);
+  if constexpr (sizeof(T) == 4) return 0.5f * erfcf(-0.70710678118654752f * g);
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.21213204f, __builtin_fabsf(g), 1.f));
+  constexpr float P[9] = {0.084594116f, 0.085356005f, 0.074179493f, 0.10742909f, -0.047254566f, 0.27376783f, -0.25606576f, 0.24274902f, -0.064755239f};
+  float s = P[8];
+#pragma unroll
+  for (int i = 7; i >= 0; --i) s = __builtin_fmaf(s, t, P[i]);
+  s *= t * *density;
+  return g < 0.f ? s : 1.f - s;
+}
+
+// The activation of a gate's value; for results of 16 bits quotients by the reciprocal to 1 ulp.
 template <typename T, int ACT>
 __device__ inline float activated(float g) {
   if constexpr (ACT == ACT_RELU) {
@@ -352,16 +366,9 @@ __device__ inline float activated(float g) {
   } else if constexpr (ACT == ACT_SILU) {
     const float d = 1.f + row_exp<T>(-g);
     return sizeof(T) == 2 ? g * __builtin_amdgcn_rcpf(d) : g / d;
-  } else if constexpr (sizeof(T) == 4) {
-    return 0.5f * g * (1.f + erff(g * 0.70710678118654752f));
   } else {
-    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.21213204f, __builtin_fabsf(g), 1.f));
-    constexpr float P[9] = {0.084594116f, 0.085356005f, 0.074179493f, 0.10742909f, -0.047254566f, 0.27376783f, -0.25606576f, 0.24274902f, -0.064755239f};
-    float s = P[8];
-#pragma unroll
-    for (int i = 7; i >= 0; --i) s = __builtin_fmaf(s, t, P[i]);
-    s *= t * __expf(-0.5f * g * g);
-    return g * (g < 0.f ? s : 1.f - s);
+    float density;
+    return g * normal_part<T>(g, &density);
   }
 }
 // f(the activation as a constant): chosen once, not once a value.

@@ -38,9 +38,10 @@ __device__ inline void activate_slope(float g, int act, float* a, float* slope) 
     *a = g * s;
     *slope = s * (1.f + g * rest);
   } else if (act == ACT_GELU) {
-    const float f = 0.5f * (1.f + erff(g * 0.70710678118654752f));
+    float density;
+    const float f = normal_part<T>(g, &density);
     *a = g * f;
-    *slope = f + g * row_exp<T>(-0.5f * g * g) * 0.39894228040143268f;
+    *slope = f + g * density * 0.39894228040143268f;
   } else {
     *a = g <= 0.f ? 0.f : g;   // NaN stays
     *slope = g > 0.f ? 1.f : 0.f;

@@ -81,7 +81,7 @@ def test_offsets_whose_last_is_not_their_largest_read_no_stale_workspace(torch, 
 U = 2.0 ** -24
 
 
-@pytest.mark.parametrize("act", ["silu"])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
 def test_activation_of_fp32_rows_over_its_range(torch, ops, act):
     """The activation and its slope as fp32 functions evaluated to a few roundings, wherever the gate lies: up = 1 and one column of
     x, so that gate, h and both gradients are exact but for them."""
@@ -108,3 +108,22 @@ def test_activation_of_fp32_rows_over_its_range(torch, ops, act):
     _, dwg, dwu = ops.expert_gated_backward(torch.ones(1, n, device="cuda"), x, wg, wu, gate, up, act=act)
     assert ((dwu[:, 0].double() - v).abs() <= ev + 1e-37).all(), ((dwu[:, 0].double() - v).abs() / (v.abs() * U)).max()
     assert ((dwg[:, 0].double() - s).abs() <= es + 1e-37).all(), ((dwg[:, 0].double() - s).abs() / (s.abs() * U)).max()
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+def test_gelu_of_16_bit_rows_in_its_lower_tail(torch, ops, dtype):
+    """dup = dh gelu(gate) is the forward's gelu of the kept gate, rounded once: right to its last bit or next to it down to where it
+    underflows, as the forward result is."""
+    dt = getattr(torch, dtype)
+    n = 2048
+    gates = torch.linspace(-4.6 if dtype == "float16" else -12.0, 4.0, n, device="cuda").to(dt)
+    x, wg, wu = torch.ones(1, 1, dtype=dt, device="cuda"), gates[:, None].clone(), torch.ones(n, 1, dtype=dt, device="cuda")
+    h, gate, up = ops.expert_gated(x, wg, wu, act="gelu", keep=True)
+    _, _, dwu = ops.expert_gated_backward(torch.ones(1, n, dtype=dt, device="cuda"), x, wg, wu, gate, up, act="gelu")
+    assert torch.equal(gate[0], gates)
+    v = activate(torch, gates.double(), "gelu")[0]
+    info = torch.finfo(dt)
+    # half a step of the type (of its smallest numbers below its normal range), and 4e-6 + g^2 2^-24 of the value in fp32 before it
+    bound = info.eps / 2 * v.abs().clamp(min=info.tiny) + (4e-6 + gates.double() ** 2 * 4 * U) * v.abs()
+    for got in (h[0], dwu[:, 0]):
+        assert ((got.double() - v).abs() <= bound).all(), ((got.double() - v).abs() / bound).max()
