@@ -12,9 +12,9 @@
 // alone; m / r stays within its block's range.
 //
 // Bound by HBM: 3 elements, 4 bytes of codes and an eighth of a byte of powers per parameter (10.1 bytes
-// in bf16, 22 with moments in fp32). One MI355X, bf16: 20480 x 7168 and eight
-// 384 x 7168 (169 M) 312 us at 5.5 TB/s; 122 tensors of 7168 in three launches of 8 to 9 us. The arithmetic had to become small for that: 425 us with each code rounded on its own bits
-// and a full-precision quotient, 340 with the rounding as an addition and the reciprocal in one instruction.
+// in bf16, 22 with moments in fp32) and, in 16 bits, as much by its arithmetic. One MI355X: 20480 x 7168 and eight
+// 384 x 7168 (169 M) 328 us in bf16 at 5.2 TB/s, 498 in fp32 at 5.5; 122 tensors of 7168 in three launches of 8 to 9 us.
+// With each code rounded on its own bits and a full-precision quotient it was 425 in bf16.
 #pragma once
 
 #include "../adamw.hpp"
@@ -23,8 +23,8 @@
 namespace mns {
 
 constexpr int ADAM8_MAXT = 48;                // tensors per launch (kernel-argument table)
-constexpr int ADAM8_BLOCK = 256, ADAM8_ITERS = 2;
-constexpr int ADAM8_CHUNK = ADAM8_BLOCK * 8 * ADAM8_ITERS;   // elements per workgroup
+constexpr int ADAM8_BLOCK = 256;
+constexpr int ADAM8_CHUNK = ADAM8_BLOCK * 8;  // elements per workgroup (16 a thread: 169 M in bf16 337 us)
 
 struct Adam8Table {
   void* p[ADAM8_MAXT];
@@ -99,25 +99,21 @@ __device__ inline u32x2 adam8_codes(const float (&v)[8], const uint32_t (&rnd)[8
   return mx_codes(v, q, odd);
 }
 
-// A moment's sum and the square root. fp32 parameters: every operation rounded and none contracted, so that the states
-// follow the formula bit for bit, since a last bit that differs moves one in some million roundings to the next
-// code. 16-bit parameters, whose own rounding is 2^13 times coarser: contracted, and the root to 1 ulp in one instruction,
-// which takes no denormals (small numbers are moved up by 2^64 first): 169 M in bf16 318 us, 337 with a root to half a step.
-template <typename T>
+// A moment's sum: every operation rounded and none contracted, and the root to half a step, so that the states of parameters
+// of any type follow the formula in fp32 bit for bit. A last bit that differs moves one in some million roundings to the
+// next code. The root is one correction of an estimate to an ulp, and right for every non-negative float (all 2^31 compared); small
+// numbers are moved up by 2^64 first, which keeps the correction's rest exact. 169 M in bf16 328 us; 314 with
+// contracted sums and a root to an ulp.
 __device__ inline float adam8_sum(float a, float x, float b, float y) {
-  if constexpr (sizeof(T) == 4) {
 #pragma clang fp contract(off)
-    return a * x + b * y;
-  } else {
-    return a * x + b * y;
-  }
+  return a * x + b * y;
 }
-template <typename T>
 __device__ inline float adam8_sqrt(float v) {
-  if constexpr (sizeof(T) == 4) return __builtin_sqrtf(v);
   const bool small = v < 0x1p-64f;
-  const float r = __builtin_amdgcn_sqrtf(small ? v * 0x1p64f : v);
-  return small ? r * 0x1p-32f : r;
+  const float x = v * (small ? 0x1p64f : 1.f);
+  const float y = __builtin_amdgcn_rsqf(x), root = x * y;
+  const float s = __builtin_fmaf(__builtin_fmaf(-root, root, x), 0.5f * y, root) * (small ? 0x1p-32f : 1.f);
+  return __builtin_amdgcn_classf(v, 0x180) ? s : v;   // positive and finite; 0, infinity and NaN are their own roots
 }
 
 __device__ inline u32x2 adam8_load(const uint8_t* p, int64_t i, int64_t n) {
@@ -194,19 +190,18 @@ __global__ void __launch_bounds__(ADAM8_BLOCK) adamw8_kernel(const Adam8Table t)
   uint8_t* m = t.m[ti];
   uint8_t* r = t.r[ti];
   // all loads of the thread first, then the arithmetic
-  Adam8Vec<T> pv[ADAM8_ITERS], gv[ADAM8_ITERS];
-  u32x2 mc[ADAM8_ITERS], rc[ADAM8_ITERS];
-  int mb[ADAM8_ITERS], rb[ADAM8_ITERS];
-#pragma unroll
-  for (int it = 0; it < ADAM8_ITERS; ++it) {
-    const int64_t i = base + ((int64_t)it * ADAM8_BLOCK + threadIdx.x) * 8;
-    if (i >= n) continue;
-    pv[it].load(p, i, n);
-    gv[it].load(g, i, n);
-    mc[it] = adam8_load(m, i, n);
-    rc[it] = adam8_load(r, i, n);
-    mb[it] = t.ms[ti][i / MX_BLOCK];
-    rb[it] = t.rs[ti][i / MX_BLOCK];
+  const int64_t i = base + (int64_t)threadIdx.x * 8;
+  const bool in = i < n;
+  Adam8Vec<T> pv, gv;
+  u32x2 mc, rc;
+  int mb, rb;
+  if (in) {
+    pv.load(p, i, n);
+    gv.load(g, i, n);
+    mc = adam8_load(m, i, n);
+    rc = adam8_load(r, i, n);
+    mb = t.ms[ti][i / MX_BLOCK];
+    rb = t.rs[ti][i / MX_BLOCK];
   }
   uint32_t key = t.key[ti];
   float bc1 = t.bc1, bc2 = t.bc2;
@@ -227,45 +222,40 @@ __global__ void __launch_bounds__(ADAM8_BLOCK) adamw8_kernel(const Adam8Table t)
       bc2 = fix[1];
     }
   }
+  float pf[8], mf[8], rf[8];
+  uint32_t rnd[8];
 #pragma unroll
-  for (int it = 0; it < ADAM8_ITERS; ++it) {
-    const int64_t i = base + ((int64_t)it * ADAM8_BLOCK + threadIdx.x) * 8;
-    const bool in = i < n;
-    float pf[8], mf[8], rf[8];
-    uint32_t rnd[8];
+  for (int e = 0; e < 8; ++e) pf[e] = mf[e] = rf[e] = 0.f;
+  if (in) {
+    float gf[8];
+    pv.unpack(pf);
+    gv.unpack(gf);
+    mx_values(mc, mx_factor(mb), mf);
+    mx_values(rc, mx_factor(rb), rf);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) pf[e] = mf[e] = rf[e] = 0.f;
-    if (in) {
-      float gf[8];
-      pv[it].unpack(pf);
-      gv[it].unpack(gf);
-      mx_values(mc[it], mx_factor(mb[it]), mf);
-      mx_values(rc[it], mx_factor(rb[it]), rf);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        mf[e] = adam8_sum<T>(t.beta1, mf[e], t.one_beta1, gf[e]);
-        rf[e] = adam8_sqrt<T>(adam8_sum<T>(t.beta2, rf[e] * rf[e], t.one_beta2, gf[e] * gf[e]));
-        // the reciprocal to 1 ulp: its error in p is 2^-23 of the step
-        pf[e] = t.wd_mul * pf[e] - t.lr * ((mf[e] * bc1) * __builtin_amdgcn_rcpf(rf[e] * bc2 + t.eps));
-      }
+    for (int e = 0; e < 8; ++e) {
+      mf[e] = adam8_sum(t.beta1, mf[e], t.one_beta1, gf[e]);
+      rf[e] = adam8_sqrt(adam8_sum(t.beta2, rf[e] * rf[e], t.one_beta2, gf[e] * gf[e]));
+      // the reciprocal to 1 ulp: its error in p is 2^-23 of the step
+      pf[e] = t.wd_mul * pf[e] - t.lr * ((mf[e] * bc1) * __builtin_amdgcn_rcpf(rf[e] * bc2 + t.eps));
     }
-    adam8_bits(key, i, rnd);
-    if (i + 8 > n) {
+  }
+  adam8_bits(key, i, rnd);
+  if (i + 8 > n) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (i + e >= n) mf[e] = rf[e] = 0.f;   // behind the end nothing counts for the block
-    }
-    // the quads' lanes meet here, those behind the end with zeros
-    int bm, br;
-    const u32x2 cm = adam8_codes<false>(mf, rnd, &bm), cr = adam8_codes<true>(rf, rnd, &br);
-    if (!in) continue;
-    Adam8Vec<T>::store(p, i, n, pf);
-    adam8_store(m, i, n, cm);
-    adam8_store(r, i, n, cr);
-    if (i % MX_BLOCK == 0) {
-      t.ms[ti][i / MX_BLOCK] = (uint8_t)bm;
-      t.rs[ti][i / MX_BLOCK] = (uint8_t)br;
-    }
+    for (int e = 0; e < 8; ++e)
+      if (i + e >= n) mf[e] = rf[e] = 0.f;   // behind the end nothing counts for the block
+  }
+  // the quads' lanes meet here, those behind the end with zeros
+  int bm, br;
+  const u32x2 cm = adam8_codes<false>(mf, rnd, &bm), cr = adam8_codes<true>(rf, rnd, &br);
+  if (!in) return;
+  Adam8Vec<T>::store(p, i, n, pf);
+  adam8_store(m, i, n, cm);
+  adam8_store(r, i, n, cr);
+  if (i % MX_BLOCK == 0) {
+    t.ms[ti][i / MX_BLOCK] = (uint8_t)bm;
+    t.rs[ti][i / MX_BLOCK] = (uint8_t)br;
   }
 }
 

@@ -184,7 +184,9 @@ int run_adamw8(int nt, void* const* params, const void* const* grads, uint8_t* c
     for (; i < nt && k < ADAM8_MAXT; ++i) {
       if (numels[i] == 0) continue;
       const int64_t b = (numels[i] + ADAM8_CHUNK - 1) / ADAM8_CHUNK;
-      if (blocks + b > INT32_MAX / ADAM8_BLOCK) break;   // a grid holds fewer than 2^32 threads
+      // a grid holds fewer than 2^32 threads; the largest tensor, 2^34 elements, takes half of them
+      static_assert((int64_t(1) << 34) / ADAM8_CHUNK <= UINT32_MAX / ADAM8_BLOCK, "a tensor fits a launch");
+      if (blocks + b > UINT32_MAX / ADAM8_BLOCK) break;
       t.p[k] = params[i];
       t.g[k] = grads[i];
       t.m[k] = m[i];
