@@ -453,6 +453,9 @@ MNS_API int expert_gated(const mns_tensor* X, const mns_tensor* Wg, const mns_te
  */
 MNS_API int mns_expert_gated_workspace_bytes(int64_t rows, int64_t inner, int32_t experts, int32_t dtype, size_t* forward, size_t* backward);
 
+/* The same of a dense call whose K (cols) is known: without the split's part where the call cuts no round. */
+MNS_API int mns_expert_gated_dense_workspace_bytes(int64_t rows, int64_t inner, int64_t cols, int32_t dtype, size_t* forward, size_t* backward);
+
 /*
  * Its gradients, from gate and up as kept: dgate = dH * up * act'(gate), dup = dH * act(gate), rounded to the
  * rows' dtype in the workspace (relu's slope at 0 is 0);

@@ -131,6 +131,26 @@ bool split_tiles(const GatedArgs& a, int dt) {
   return tiles <= (MODE == EX_GATE ? 2 : 1) * (int64_t)device_cus();
 }
 
+// Whether the 256 x 256 tiles fit a product's types, rows and extents.
+template <int MODE>
+bool whole_tiles(const GatedArgs& a, int dt, bool vec) {
+  return vec && a.c_vec && a.n % 8 == 0 && dt != F32 && a.n > (MODE == EX_GATE ? 64 : 128) && (!ex_dw(MODE) || a.m > 128);
+}
+
+// Whether a dense product of rows x n results and contractions of k takes the cut last round if it has room for it.
+template <int MODE>
+bool takes_split(int64_t rows, int64_t n, int64_t k, int dt) {
+  GatedArgs a{};
+  float room;
+  a.parts = &room;
+  a.c_vec = 1;
+  a.experts = 1;
+  a.rows = rows;
+  a.n = (int)n;
+  a.k = (int)k;
+  return whole_tiles<MODE>(a, dt, true) && !(MODE == EX_GATE && few_rows(a, dt, CHUNK_ALIGNED)) && split_pays<MODE>(a) && !split_tiles<MODE>(a, dt);
+}
+
 // vec: operands' rows of whole aligned chunks.
 template <int MODE>
 int run_product(const GatedArgs& a, int dt, bool vec, hipStream_t s) {
@@ -141,7 +161,7 @@ int run_product(const GatedArgs& a, int dt, bool vec, hipStream_t s) {
   const int fit = vec ? CHUNK_ALIGNED : tiny ? CHUNK_TINY : CHUNK_ANY;
   if constexpr (MODE == EX_GATE)
     if (few_rows(a, dt, fit)) return run_few(a, dt, fit, s);
-  const bool whole = vec && a.c_vec && a.n % 8 == 0 && dt != F32 && a.n > (MODE == EX_GATE ? 64 : 128) && (!ex_dw(MODE) || a.m > 128);
+  const bool whole = whole_tiles<MODE>(a, dt, vec);
   const int64_t high = ex_dw(MODE) ? tile_rows<MODE, TilePP>(a) : a.rows / 256 + std::min<int64_t>(a.experts, a.rows);
   if constexpr (MODE != EX_DW2)
     if (whole && split_pays<MODE>(a) && !split_tiles<MODE>(a, dt)) return run_split_pingpong<MODE>(a, dt, s);
@@ -205,6 +225,15 @@ int mns_expert_gated_workspace_bytes(int64_t rows, int64_t inner, int32_t expert
   if (rows < 0 || rows > kMaxRows || inner < 1 || inner > kMaxCols || experts < 0 || experts > EXPERT_MAX) return MNS_ERR_SHAPE;
   *forward = rows && !experts && dtype != F32 ? (size_t)split_bytes() : 0;
   *backward = (size_t)(2 * inner_bytes(rows, inner, dtype)) + *forward;
+  return MNS_OK;
+}
+
+int mns_expert_gated_dense_workspace_bytes(int64_t rows, int64_t inner, int64_t cols, int32_t dtype, size_t* forward, size_t* backward) {
+  if (cols < 1 || cols > kMaxCols) return MNS_ERR_SHAPE;
+  if (int st = mns_expert_gated_workspace_bytes(rows, inner, 0, dtype, forward, backward)) return st;
+  if (!*forward) return MNS_OK;
+  if (!takes_split<EX_DX2>(rows, cols, inner, dtype)) *backward -= *forward;
+  if (!takes_split<EX_GATE>(rows, inner, cols, dtype)) *forward = 0;
   return MNS_OK;
 }
 

@@ -118,6 +118,7 @@ def declare(lib):
         "embed_backward": [t, vp, i32, ctypes.c_float, t, vp, sz, vp],
         "expert_gated": [t, t, t, vp, i32, t, t, t, vp, sz, vp],
         "mns_expert_gated_workspace_bytes": [i64, i64, i32, i32, P(sz), P(sz)],
+        "mns_expert_gated_dense_workspace_bytes": [i64, i64, i64, i32, P(sz), P(sz)],
         "expert_gated_backward": [t, t, t, t, t, t, vp, i32, t, t, t, vp, sz, vp],
         "adamw8_step": [ctypes.c_int, pp, pp, pp, pp, pp, pp, P(i64), i32, P(MnsAdamw8Params), vp],
     }
@@ -1021,16 +1022,21 @@ def expert_gated(x, w_gate, w_up, offsets=None, *, act: str = "silu", keep: bool
     h = x.new_empty(shape) if out is None else out
     gate, up = (x.new_empty(shape), x.new_empty(shape)) if keep else (None, None)
     if workspace is None and offsets is None:
-        n = expert_gated_workspace_bytes(*shape, x, dense=True)[0]
+        n = expert_gated_workspace_bytes(*shape, x, dense=True, cols=x.shape[1])[0]
         workspace = torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
     _launch(what, x, describe(x), describe(w_gate), describe(w_up), _ptr(offsets), code, describe(h), describe(gate) if keep else None,
             describe(up) if keep else None, _ptr(workspace), 0 if workspace is None else _ws_bytes(workspace))
     return (h, gate, up) if keep else h
 
 
-def expert_gated_workspace_bytes(rows: int, inner: int, like, *, dense: bool = False) -> tuple:
-    """(expert_gated's, expert_gated_backward's); like: a tensor of the rows' dtype; dense: without offsets."""
+def expert_gated_workspace_bytes(rows: int, inner: int, like, *, dense: bool = False, cols: Optional[int] = None) -> tuple:
+    """(expert_gated's, expert_gated_backward's); like: a tensor of the rows' dtype; dense: without offsets, of which calls
+    that cut no round need less: cols (K) tells them apart."""
     forward, backward = ctypes.c_size_t(), ctypes.c_size_t()
+    if dense and cols is not None:
+        _check(_lib().mns_expert_gated_dense_workspace_bytes(rows, inner, cols, dtype_code(like), ctypes.byref(forward), ctypes.byref(backward)),
+               "mns_expert_gated_dense_workspace_bytes")
+        return forward.value, backward.value
     _check(_lib().mns_expert_gated_workspace_bytes(rows, inner, 0 if dense else 1, dtype_code(like), ctypes.byref(forward), ctypes.byref(backward)),
            "mns_expert_gated_workspace_bytes")
     return forward.value, backward.value
@@ -1049,7 +1055,7 @@ def expert_gated_backward(dh, x, w_gate, w_up, gate, up, offsets=None, *, act: s
     _check_workspace(what, workspace)
     _check_device(what, x, dh=dh, w_gate=w_gate, w_up=w_up, gate=gate, up=up, offsets=offsets, workspace=workspace)
     if workspace is None:
-        n = expert_gated_workspace_bytes(x.shape[0], w_gate.shape[-2], x, dense=offsets is None)[1]
+        n = expert_gated_workspace_bytes(x.shape[0], w_gate.shape[-2], x, dense=offsets is None and need_input, cols=x.shape[1])[1]
         workspace = torch.empty(n, dtype=torch.uint8, device=x.device)
     dx = x.new_empty(x.shape) if need_input else None
     dwg, dwu = (w_gate.new_empty(w_gate.shape), w_gate.new_empty(w_gate.shape)) if need_weights else (None, None)

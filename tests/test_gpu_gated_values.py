@@ -127,3 +127,20 @@ def test_gelu_of_16_bit_rows_in_its_lower_tail(torch, ops, dtype):
     bound = info.eps / 2 * v.abs().clamp(min=info.tiny) + (4e-6 + gates.double() ** 2 * 4 * U) * v.abs()
     for got in (h[0], dwu[:, 0]):
         assert ((got.double() - v).abs() <= bound).all(), ((got.double() - v).abs() / bound).max()
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+def test_the_workspace_asked_for_is_all_that_a_dense_call_takes(torch, ops, dtype):
+    """A call with far more room gives the bits of one with as much as it asks for, over the rules that choose its kernel."""
+    dt = getattr(torch, dtype)
+    gen = gen_for(torch, 60)
+    room = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
+    for n, k in ((72, 2560), (1024, 2568), (2064, 2560), (4104, 4096), (1216, 20000), (9000, 2504)):
+        wg, wu = (normal(torch, gen, n, k).mul(k ** -0.5).to(dt) for _ in range(2))
+        for rows in (1, 4, 5, 17, 64, 100, 300, 512, 600, 1100, 2500):
+            x, dh = normal(torch, gen, rows, k).to(dt), normal(torch, gen, rows, n).to(dt)
+            h, gate, up = ops.expert_gated(x, wg, wu, keep=True)
+            assert torch.equal(h, ops.expert_gated(x, wg, wu, workspace=room)), (rows, n, k)
+            own = ops.expert_gated_backward(dh, x, wg, wu, gate, up)
+            wide = ops.expert_gated_backward(dh, x, wg, wu, gate, up, workspace=room)
+            assert all(torch.equal(a, b) for a, b in zip(own, wide)), (rows, n, k)
