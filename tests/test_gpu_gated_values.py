@@ -144,3 +144,35 @@ def test_the_workspace_asked_for_is_all_that_a_dense_call_takes(torch, ops, dtyp
             own = ops.expert_gated_backward(dh, x, wg, wu, gate, up)
             wide = ops.expert_gated_backward(dh, x, wg, wu, gate, up, workspace=room)
             assert all(torch.equal(a, b) for a, b in zip(own, wide)), (rows, n, k)
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_each_gradient_against_differences_in_64_bits(torch, ops, act):
+    """The directional derivative of sum(c h), taken from the definition in 64 bits, along each of x, w_gate and w_up alone."""
+    gen = gen_for(torch, 19)
+    counts, n, k = [7, 0, 20, 5], 40, 72
+    x, c, wg, wu, offsets = make(torch, gen, torch.float32, counts, 2, n, k)
+    _, gate, up = ops.expert_gated(x, wg, wu, offsets, act=act, keep=True)
+    if act == "relu":
+        c = c * (gate.abs() > 1e-3)           # no gate changes its side within a step
+    dirs = [normal(torch, gen, *t.shape).double() for t in (x, wg, wu)]
+    bounds = offsets.tolist()
+
+    def loss(x, wg, wu):
+        total = 0.0
+        for e, (lo, hi) in enumerate(zip(bounds, bounds[1:])):
+            total += (c[lo:hi].double() * activate(torch, x[lo:hi] @ wg[e].T, act)[0] * (x[lo:hi] @ wu[e].T)).sum()
+        return total
+
+    grads = ops.expert_gated_backward(c, x, wg, wu, gate, up, offsets, act=act)
+    at = [t.double() for t in (x, wg, wu)]
+    step = 2.0 ** -18
+    for i, what in enumerate(("dx", "dw_gate", "dw_up")):
+        ends = [loss(*(t + s * step * dirs[i] if j == i else t for j, t in enumerate(at))) for s in (1, -1)]
+        want = (ends[0] - ends[1]) / (2 * step)
+        got = (grads[i].double() * dirs[i]).sum()
+        # three chained sums of at most 80 terms of random sign at 2^-24 each, with slopes and factors of order 1, are off by less than
+        # 20 sqrt(80) 2^-24 = 1.1e-5 of the gradient's norm, and a normal direction picks up its error's norm, four times that at most; the
+        # difference's own error, step^2 of third derivatives, is 1e-11. A gradient left out would be off by its norm.
+        bound = 5e-5 * grads[i].double().norm()
+        assert abs(got - want) <= bound and abs(want) > 20 * bound, (what, got, want, bound)
