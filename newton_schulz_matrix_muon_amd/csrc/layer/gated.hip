@@ -102,17 +102,23 @@ int run_few(const GatedArgs& a, int dt, int fit, hipStream_t s) {
   });
 }
 
-// The rule of the single products (layer.hip), with its tiles counted for two matrices. us with the kernel for few rows and
-// without, 64 experts of 1408 x 2048: one token of 6 experts 20 and 26 in bf16 (42 and 56 in fp32), 8 tokens 78 and 90
-// (167 and 183), but where each expert has 4 rows 154 and 137 (313 and 324); a dense 4096 x 3000 with 16 rows 18
-// and 19 (24 and 40); 27 experts of 2048 x 7168, 8 tokens, 261 and 279 (671 and 608). Rows of any address, 64 experts of
-// 1405 x 2045: 34 and 27 for one token in bf16, 50 and 57 in fp32.
+// Few rows: the kernel that reads the weights once for 16 rows of an expert. It wins where there are few tiles, and where a row
+// of W is short, so that the tiles' first stages count; it has nothing to hide its latency under where W's rows begin anywhere.
+// us with it and without (bf16; fp32):
+//   64 experts of 1408 x 2048  6 experts with a row 17 and 24; 42 and 55;  16: 37 and 51; 84 and 87;  one row each 124 and 157;
+//                              297 and 309;  four each 132 and 158; 311 and 311;  six each 140 and 159; 320 and 310
+//   27 of 2048 x 7168          6 (192 tiles) 79 and 80; 166 and 184;  16 (512) 173 and 161; 403 and 369;  one row each 295 and 286; 694 and 629
+//   12 of 5360 x 2944          6 (504) 83 and 85; 175 and 157;  one row each 135 and 137; 339 and 306
+//   dense 4096 x 3000          1 row 17 and 20; 27 and 40;  16 rows 18 and 21; 33 and 42;  24 rows 25 and 22; 51 and 44
+//   dense 18432 x 7168 (288)   1 row 105 and 127; 237 and 242;  4 rows 112 and 127; 247 and 241;  8 rows 121 and 127; 260 and 244
+//   64 of 1405 x 2045          6 (132) 34 and 26; 47 and 55;  16 (352) 64 and 57; 101 and 87
 bool few_rows(const GatedArgs& a, int dt, int fit) {
-  const int64_t tiles = std::min<int64_t>(a.experts, a.rows) * ((a.n + 63) / 64);
-  const int64_t most = (fit == CHUNK_ALIGNED ? 4 : 2) * (dt == F32 ? 2 : 1) * (int64_t)a.experts;
-  const bool whole = fit == CHUNK_ALIGNED || dt == F32;
-  if (2 * tiles <= device_cus()) return a.rows <= (whole ? 4 * most : most);
-  return a.rows <= most && a.k * dtype_size(dt) >= 512 && whole;
+  const int64_t tiles = std::min<int64_t>(a.experts, a.rows) * ((a.n + 63) / 64), cus = device_cus(), row = a.k * dtype_size(dt);
+  const bool aligned = fit == CHUNK_ALIGNED, whole = aligned || dt == F32;
+  const int64_t most = (whole ? 4 : 2) * (int64_t)a.experts;
+  if (2 * tiles <= cus) return a.rows <= (whole ? 4 * most : most);
+  if (a.rows > most || row < 512 || !whole) return false;
+  return aligned ? 2 * tiles <= 3 * cus || row <= 8192 : tiles <= cus;
 }
 
 // 64 x 64 tiles whose contraction eight waves share: where larger tiles would leave CUs idle, or would be mostly
