@@ -25,9 +25,9 @@ constexpr int held(int nt, int vpt) { return nt * vpt * 8; }
 constexpr int kRmsHeld = held(1024, 2);   // backward: longer rows take the kernels that read them again
 
 // Threads that hold a row, a chunk each, in whole waves. whole: past 256 threads as many on each of a CU's four
-// SIMDs, so that as many workgroups fit a CU as its registers allow; 16-bit forward kernels, of which eight waves
-// fit a SIMD, do better with none idle. 16384 rows, us without and with: 16-bit forward of 4500 columns 117 and 128 (in
-// 8 bits 108 and 133), of 2500 79 and 74 (72 and 77); fp32 forward of 4500 259 and 229, backward of 2500 132 and 116.
+// SIMDs, so that as many workgroups fit a CU as its registers allow (backward, 16384 x 2500 132 us without and 116 with);
+// forward kernels do better with none idle: 16384 rows, us without and with, 16-bit of 4500 columns 116 and 128 (in 8 bits
+// 107 and 132), of 2816 71 and 72 (60 and 66); fp32 of 4500 212 and 213 (186 and 188), of 2500 130 and 131 (103 and 106).
 int row_threads(int64_t cols, bool whole) {
   const int64_t nt = (cols + 511) / 512 * 64;
   return (int)std::min<int64_t>(1024, !whole || nt <= 256 ? nt : round_up(nt, 256));
@@ -45,15 +45,19 @@ int rms_parts(int64_t rows, int64_t cols) {
 // at once, each of which has the next row on its way. us of a workgroup a row, of 16 and of 32 waves a CU:
 //   bf16  16384 x 4500 147, 191, 128;  16384 x 7168 177, 188, 179 (in 8 bits 180, 194, 161);  8192 x 12000 203, 163, 166
 //   fp32  16384 x 2500 130, 132, 149;  16384 x 4500 226, 214, 229;  4096 x 12000 188, 156, 155;  65536 x 700 153, 166, 170
+// Six workgroups of five waves, or three of ten, do not run on a CU at once: the last of them come when the others
+// have ended. us with so many and with one less: 16384 x 2500 75 and 61 (in 8 bits 70 and 58), 16384 x 4864 145 and 117
+// (133 and 115), 4096 x 5120 31 and 28 (31 and 29); five of six waves and three of nine do (2816 71 and 70, 4500 116 and 120).
 unsigned rms_groups(int64_t turns, int nt, int64_t cols, int es) {
   if (es == 4 && (cols <= held(64, 1) || nt < 256)) return (unsigned)turns;   // fewer than 2^32 threads: 2^24 rows of 192
   const int waves = es == 4 || cols > held(1024, 1) ? 16 : 32;
-  return (unsigned)std::min<int64_t>(turns, (int64_t)device_cus() * (64 * waves / nt));
+  const int fit = 64 * waves / nt - (waves == 32 && (nt == 320 || nt == 640) ? 1 : 0);
+  return (unsigned)std::min<int64_t>(turns, (int64_t)device_cus() * fit);
 }
 
 template <typename T, typename WT, bool MX>
 void launch_rms_fwd(const RmsArgs& a, hipStream_t s) {
-  const int nt = a.cols <= held(64, 1) ? 256 : row_threads(a.cols, sizeof(T) == 4);
+  const int nt = a.cols <= held(64, 1) ? 256 : row_threads(a.cols, false);
   const dim3 g(rms_groups(a.cols <= held(64, 1) ? (a.rows + 3) / 4 : a.rows, nt, a.cols, sizeof(T)));
   if (a.cols <= held(64, 1)) hipLaunchKernelGGL((rms_fwd_row<T, WT, true, 1, MX>), g, dim3(nt), 0, s, a);
   else if (a.cols <= held(1024, 1)) hipLaunchKernelGGL((rms_fwd_row<T, WT, false, 1, MX>), g, dim3(nt), 0, s, a);
