@@ -13,7 +13,7 @@
 //
 // Bound by HBM: 3 elements, 4 bytes of codes and an eighth of a byte of powers per parameter (10.1 bytes
 // in bf16, 22 with moments in fp32) and, in 16 bits, as much by its arithmetic. One MI355X: 20480 x 7168 and eight
-// 384 x 7168 (169 M) 328 us in bf16 at 5.2 TB/s, 498 in fp32 at 5.5; 122 tensors of 7168 in three launches of 8 to 9 us.
+// 384 x 7168 (169 M) 324 to 329 us in bf16 at 5.2 TB/s, 498 in fp32 at 5.5; 122 tensors of 7168 in three launches of 6 to 8 us.
 // With each code rounded on its own bits and a full-precision quotient it was 425 in bf16.
 #pragma once
 

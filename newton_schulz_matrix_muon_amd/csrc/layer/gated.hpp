@@ -16,8 +16,8 @@
 // input gradient's contraction runs through one matrix and on through the other; the weight gradients' tiles
 // are those of both matrices, so X and its rows are shared in L2. Bound by MFMA and the board's power, by HBM where there
 // are few rows. One MI355X: 32768 rows over 27 experts of 2048 x 7168 bf16, gate and up kept, 1760 us (1093
-// TFLOP/s; a large plain product of the vendor's library 1360 to 1600); 24594 rows over 64 experts of 1408 x 2048 fp16, backward 790:
-// gated_grad 70, input gradient 305 to 330, weight gradients 390 to 440; one token of 6 such experts 16.0 us (4.3
+// TFLOP/s; a large plain product of the vendor's library 1360 to 1600); 24594 rows over 64 experts of 1408 x 2048 fp16, backward 800:
+// gated_grad 70, input gradient 303 to 332, weight gradients 388 to 432; one token of 6 such experts 15.9 us (4.3
 // TB/s with the launch).
 //
 // The activation takes the fp32 sums. What the backward pass needs is gate and up, kept in the rows' type.
@@ -57,7 +57,7 @@ struct GatedGradArgs {
 };
 
 // dgate and dup, eight columns a thread. Rows of nobody are left out: the products do not read them.
-// Bound by HBM: three rows read and two written; 24594 x 1408 fp16 70 us at 4.9 TB/s.
+// Bound by HBM: three rows read and two written; 24594 x 1408 fp16 67 to 71 us at 4.9 to 5.2 TB/s.
 template <typename T>
 __global__ void __launch_bounds__(256) gated_grad(const GatedGradArgs p, int act) {
   constexpr int N = 16 / (int)sizeof(T);

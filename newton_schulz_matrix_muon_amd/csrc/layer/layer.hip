@@ -225,7 +225,7 @@ bool split_tiles(const ExpertArgs& a, int dt) {
 
 // The kernel of a product. The 256 x 256 tiles need 16-bit types, whole 16-byte chunks everywhere,
 // extents that do not leave half of a tile empty, and enough tiles for half of the CUs. One
-// MI355X, bf16, rows per expert on average (a router's picks), 256 x 256 against 128 x 128 tiles: 27
+// MI355X (others take up to 10 % more or less for both), bf16, rows per expert on average (a router's picks), 256 x 256 against 128 x 128 tiles: 27
 // experts of 2048 x 7168, 8 rows, forward 144 against 154 us, weight gradient 173 against 237; 256
 // rows 317 against 417, 364 against 496 (exactly 256 rows each: 218 against 318, 360 against 449); 64
 // experts of 1408 x 2048, 16 rows 100 against 100 us, weight gradient 83 against 115; 128 rows 115
