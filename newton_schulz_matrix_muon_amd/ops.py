@@ -625,7 +625,7 @@ def hybrid_step(matrix_groups, vector_params, *, muon: dict, adamw: dict, seed: 
     moments are held in 8 bits; those need ``step`` in ``adamw`` and take ``seed``), enqueued on the
     current stream. A step on the device (adamw8_step) goes with moments in 32 bits only without their
     bias correction, which adamw_step works out on the host."""
-    entries = list(vector_params or ())   # may be an iterator, which is gone through once
+    entries = [tuple(v) for v in vector_params or ()]   # may be iterators, which are gone through once
     for i, v in enumerate(entries):
         if len(v) not in (3, 4):
             raise ValueError(f"hybrid_step: entry {i} of vector_params holds {len(v)} things, expected 3 or 4")
@@ -634,7 +634,7 @@ def hybrid_step(matrix_groups, vector_params, *, muon: dict, adamw: dict, seed: 
     if in8 and "step" not in adamw:
         raise TypeError("hybrid_step: moments in 8 bits need step in adamw")
     adamw32 = adamw
-    if isinstance(adamw.get("step"), _torch().Tensor):
+    if entries and isinstance(adamw.get("step"), _torch().Tensor):
         if adamw.get("bias_correction") and in32:
             raise ValueError("hybrid_step: adamw_step corrects its bias by a step on the host, got one on the device")
         adamw32 = {k: v for k, v in adamw.items() if k != "step"}

@@ -43,3 +43,12 @@ def test_refusals_come_before_the_first_update(torch, ops, seen):
     ops.hybrid_step([], [], muon={}, adamw={})
     ops.hybrid_step([], None, muon={}, adamw={})
     assert not seen
+
+
+def test_entries_that_are_iterators_and_no_adamw(torch, ops, seen):
+    p = torch.zeros(4)
+    s = ops.adamw8_state(p)
+    ops.hybrid_step([], (iter(e) for e in [(p, p, s), (p, p, p, p)]), muon={}, adamw=dict(lr=1e-3, step=2))
+    assert [(c[0], len(c[1][0])) for c in seen] == [("adamw_step", 1), ("adamw8_step", 1)]
+    ops.hybrid_step([(p, p, p)], [], muon={}, adamw=None)                    # nothing for AdamW to do
+    assert seen[-1][0] == "muon_step_grouped"
